@@ -316,6 +316,163 @@ mru_status mru_scan_fused_noalloc(const mru_problem* p, const void* x, const flo
                                   const mru_readout* ro, float* S_out, float* o_out,
                                   uint32_t* status_out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A recurrent block around the scan: the elementwise gated recurrence, the
+ * norms before and after a block with its gate and residual scale, and
+ * activations kept in 8 bits between the forward and the backward.  The
+ * method's pages have no counterpart to these calls.  Conventions are those
+ * of the calls above: the caller owns every buffer, calls are asynchronous on
+ * `stream` and argument problems are returned before anything is launched.
+ * Buffers are aligned to their element (the workspace to 16 bytes); the
+ * kernels take wider accesses where addresses and sizes allow them.  An
+ * output that overlaps an input or another output is MRU_ERR_INVALID_ARG
+ * (interleaved slices of rows of one length do not overlap).  Calls that
+ * share a workspace, or captured graphs that hold such calls, run one after
+ * another.
+ * ------------------------------------------------------------------------ */
+
+/* A [rows, D] array held in 8 bits: row-major int8 values q and one fp32
+ * scale per run of 64 channels of a row, scale [rows, ceil(D / 64)].  With
+ * amax the run's largest magnitude, scale = amax / 127 and
+ * q = rint(x * (127 / amax)) (fp32, ties to even); the value held is
+ * q * scale.  A run whose amax is below 2^-100 is held as zeros (scale 0); a
+ * run with an infinity or a NaN gets a NaN scale, so that all of it comes
+ * back as NaN.  q NULL: not given. */
+#define MRU_PACK8_GROUP 64
+typedef struct {
+    int8_t* q;                  /* [rows, D] */
+    float* scale;               /* [rows, ceil(D / 64)] */
+} mru_packed8;
+
+/* x [rows, D] (mru_dtype `dtype`, ld elements from one row to the next, 0: D)
+ * to and from 8 bits. */
+mru_status mru_pack8(int64_t rows, int64_t D, int64_t ld, int32_t dtype, const void* x, const mru_packed8* out,
+                     void* stream);
+mru_status mru_unpack8(int64_t rows, int64_t D, int64_t ld, int32_t dtype, const mru_packed8* in, void* x,
+                       void* stream);
+
+/* Gated linear recurrence over sequences, one scalar state per channel:
+ *     h_t = a_t h_{t-1} + b_t,   y_t = h_t,
+ *   DECAY    a = f,                              b = x
+ *   SIGMOID  a = s(f),                           b = (1 - a) x
+ *   LRU      a = exp(-c softplus(lam) s(f)),     b = sqrt(1 - a^2) s(i) x
+ * (s the logistic function).  States and products of decays are fp32.
+ * reset[b, t] != 0 starts a new sequence at t: h_{t-1} counts as zero there,
+ * whatever it was.  Tokens t >= lens[b] (clamped to 0 .. L) are padding: they
+ * are not used, the state stays as it was, and y and the token gradients are
+ * zero there.  A state that meets a product of decays of exactly zero (a
+ * reset, a = 0, or underflow) contributes nothing, even if not finite. */
+typedef enum { MRU_GATE_DECAY = 0, MRU_GATE_SIGMOID = 1, MRU_GATE_LRU = 2 } mru_gate;
+
+typedef struct {
+    int64_t B, L, D;            /* batch, tokens, channels (>= 0) */
+    int64_t ld, ld_grad;        /* elements from one token to the next in x, f, i and in dx, df, di
+                                 * (slices of one projection's output); 0: D.  Sequences are L * ld apart. */
+    int32_t dtype;              /* mru_dtype of x, f, i, y and their gradients */
+    int32_t gate;               /* mru_gate */
+    float c;                    /* LRU: > 0 */
+} mru_gated_problem;
+
+typedef struct {
+    const void* x;              /* [B, L, D] */
+    const void* f;              /* [B, L, D] decay, or its logit */
+    const void* i;              /* [B, L, D] input gate's logit: LRU, else NULL */
+    const float* lam;           /* [D]: LRU, else NULL */
+    const float* h0;            /* [B, D], or NULL: zero */
+    const uint8_t* reset;       /* [B, L] or NULL */
+    const int32_t* lens;        /* [B] or NULL */
+} mru_gated_inputs;
+
+/* What the forward keeps for the backward: the state before every 64th token
+ * and, where q is given, x, f (and i) in 8 bits, written in the same pass;
+ * the backward then reads those instead of x, f, i (all of them or none). */
+#define MRU_GATED_KEEP 64
+typedef struct {
+    float* states;              /* [B, ceil(L / 64), D]: h before token 64 k */
+    mru_packed8 x, f, i;        /* [B * L, D] each */
+} mru_gated_saved;
+
+/* Workspace bytes of the forward and of the backward; 0: invalid problem. */
+size_t mru_gated_workspace_size(const mru_gated_problem* p);
+size_t mru_gated_backward_workspace_size(const mru_gated_problem* p);
+
+/* y [B, L, D] (contiguous), h_last [B, D] fp32 or NULL: the state after the
+ * last token (may not be h0's buffer); saved: NULL, or what to keep.  One
+ * token per sequence (L = 1) is the serving step. */
+mru_status mru_gated_scan(const mru_gated_problem* p, const mru_gated_inputs* in, void* y, float* h_last,
+                          const mru_gated_saved* saved, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of sum <dy, y> + <dh_last, h_last>, h_{t-1} recomputed from the
+ * kept states.  With d_t = dy_t + a_{t+1} d_{t+1} (nothing across a reset):
+ *   DECAY    dx = d,                 df = d h_{t-1}
+ *   SIGMOID  dx = (1 - a) d,         df = a (1 - a) (h_{t-1} - x) d
+ *   LRU      dx = d u s(i),  di = d u x s'(i),  u = sqrt(1 - a^2),
+ *            q = d log(a) (a h_{t-1} - s(i) x a^2 / u),
+ *            df = q (1 - s(f)),      dlam = s(lam) / softplus(lam) sum q
+ *   dh0 = a_1 d_1 (zero where reset)
+ *   dy [B, L, D] contiguous;  dh_last [B, D] fp32 or NULL: zero
+ *   dx, df, di [B, L, D], ld_grad apart;  dlam [D], dh0 [B, D] fp32 or NULL
+ * in->h0 is not read.  Gradients of values kept in 8 bits are those at the
+ * values held.  The same call gives the same bits every time. */
+mru_status mru_gated_scan_backward(const mru_gated_problem* p, const mru_gated_inputs* in,
+                                   const mru_gated_saved* saved, const void* dy, const float* dh_last, void* dx,
+                                   void* df, void* di, float* dlam, float* dh0, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/* The ends of a block around a sublayer whose output is y, row by row:
+ *     r' = r + res_scale * s * act(g) * (N(y) w_y + b_y)
+ *     z  = N(r') w_z + b_z
+ * r' is the residual stream after the block and z the next sublayer's input
+ * (normalised before r' is rounded to its type).  N is the RMS norm
+ * v / sqrt(mean v^2 + eps) or the layer norm (v - mean) / sqrt(var + eps),
+ * act(g) is 1, g s(g) or s(g).  y NULL: no block before, z = N(r) w_z + b_z;
+ * z NULL: no norm after. */
+typedef enum { MRU_NORM_RMS = 0, MRU_NORM_LAYER = 1 } mru_norm;
+typedef enum { MRU_ACT_NONE = 0, MRU_ACT_SILU = 1, MRU_ACT_SIGMOID = 2 } mru_act;
+
+typedef struct {
+    int64_t rows, D;            /* rows >= 0, 0 <= D <= 16384 (else MRU_ERR_UNSUPPORTED) */
+    int64_t ld_y, ld_g;         /* elements between rows of y and of g; 0: D */
+    int64_t ld_dy, ld_dg;       /* the same of dy and dg */
+    int32_t dtype;              /* mru_dtype of r, y, g, z and their gradients */
+    int32_t norm;               /* mru_norm */
+    int32_t act;                /* mru_act; NONE: g is NULL */
+    float eps;                  /* >= 0 */
+    float res_scale;
+} mru_block_problem;
+
+typedef struct {                /* [D] fp32 each; NULL: ones (w_y, s, w_z) or zeros (b_y, b_z) */
+    const float *w_y, *b_y, *s, *w_z, *b_z;
+} mru_block_params;
+
+typedef struct {                /* 8-bit copies for the backward, [rows, D] each: all that apply, or none */
+    mru_packed8 r, y, g;        /* of the stored r', of y and of g */
+} mru_block_saved;
+
+typedef struct {                /* [D] fp32 each, or NULL: not wanted */
+    float *dw_y, *db_y, *ds, *dw_z, *db_z;
+} mru_block_grads;
+
+/* saved: NULL, or the 8-bit copies to write in the same pass (with y NULL, r
+ * is copied). */
+mru_status mru_block_norm(const mru_block_problem* p, const mru_block_params* prm, const void* r, const void* y,
+                          const void* g, void* r_out, void* z, const mru_block_saved* saved, void* stream);
+
+/* Gradients of sum <dr_out, r'> + <dz, z>, from the stored r' (r_out; only
+ * read when dz is given), y and g, or from their 8-bit copies (saved, which
+ * then are read instead):
+ *     e = dr_out + N'(r'; dz w_z),   dr = e,   dm = res_scale s e,
+ *     dy = N'(y; dm act(g) w_y),     dg = dm (N(y) w_y + b_y) act'(g)
+ * and the parameters' sums over rows.  dr_out or dz may be NULL (zero; not
+ * both).  dr may be NULL when not wanted; y (or its copy) NULL: no block
+ * before, then dy and dg are NULL.  The same call gives the same bits every
+ * time. */
+size_t mru_block_backward_workspace_size(const mru_block_problem* p);
+mru_status mru_block_norm_backward(const mru_block_problem* p, const mru_block_params* prm, const void* r_out,
+                                   const void* y, const void* g, const mru_block_saved* saved, const void* dr_out,
+                                   const void* dz, void* dr, void* dy, void* dg, const mru_block_grads* grads,
+                                   void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,141 @@
+// mru_ops.cuh -- device and host helpers shared by the gated recurrence, the
+// block's norms and the 8-bit copies (not part of the ABI).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "mru_internal.cuh"
+
+namespace mru {
+namespace ops {
+
+// ------------------------------------------------------------------ host ---
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline size_t elem_size(int32_t dtype) { return dtype == MRU_BF16 ? 2 : 4; }
+inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+inline mru_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MRU_OK : MRU_ERR_CUDA; }
+
+// Whether a * b (both >= 0) stays within `limit`.
+inline bool product_within(int64_t a, int64_t b, int64_t limit) { return a == 0 || b <= limit / a; }
+
+// The buffers of a call, as rows of `width` bytes `pitch` apart.  An output
+// may not overlap any other buffer; inputs may overlap one another.
+struct Buffers {
+    struct R {
+        uintptr_t lo, hi;
+        size_t width, pitch;
+        bool out;
+    } r[32];
+    int n = 0;
+    void add(const void* p, int64_t rows, size_t width, size_t pitch, bool out)
+    {
+        if (!p || rows <= 0 || width == 0) return;
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        r[n++] = {lo, lo + (size_t)(rows - 1) * pitch + width, width, pitch, out};
+    }
+    void in(const void* p, size_t bytes) { add(p, 1, bytes, bytes, false); }
+    void out(const void* p, size_t bytes) { add(p, 1, bytes, bytes, true); }
+    void in_rows(const void* p, int64_t rows, size_t width, size_t pitch) { add(p, rows, width, pitch, false); }
+    void out_rows(const void* p, int64_t rows, size_t width, size_t pitch) { add(p, rows, width, pitch, true); }
+    static bool overlap(const R& a, const R& b)
+    {
+        if (a.lo >= b.hi || b.lo >= a.hi) return false;
+        if (a.pitch != b.pitch || a.width > a.pitch || b.width > b.pitch) return true;
+        // columns of rows of one length: where b's rows start within a's
+        const size_t d = b.lo >= a.lo ? (b.lo - a.lo) % a.pitch : (a.pitch - (a.lo - b.lo) % a.pitch) % a.pitch;
+        return d < a.width || d + b.width > a.pitch;
+    }
+    bool clash() const
+    {
+        for (int i = 0; i < n; ++i)
+            for (int j = 0; j < i; ++j)
+                if ((r[i].out || r[j].out) && overlap(r[i], r[j])) return true;
+        return false;
+    }
+};
+
+// ---------------------------------------------------------------- device ---
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// s(v) and 1 - s(v) = s(-v), both to a few ulp: with e = exp(-|v|) in (0, 1]
+// neither form overflows or cancels.
+__device__ __forceinline__ void sigmoid2(float v, float& s, float& ns)
+{
+    const float e = __expf(-fabsf(v));
+    const float r = __fdividef(1.0f, 1.0f + e);
+    const float q = e * r;
+    s = v >= 0.0f ? r : q;
+    ns = v >= 0.0f ? q : r;
+    if (v != v) s = ns = v;
+}
+
+// e^v and e^v - 1 for v <= 0, both to a few ulp.  Near 0 the difference is the
+// Taylor series (eight terms: the ninth is below 2^-26 of the sum for
+// v >= -0.5) and e^v is 1 more, so that a decay near 1 keeps only its own
+// rounding; further out it is the other way round.
+__device__ __forceinline__ void exp_expm1_neg(float v, float& ev, float& m)
+{
+    float p = fmaf(v, 1.0f / 8.0f, 1.0f) * (1.0f / 7.0f);
+    p = fmaf(p, v, 1.0f) * (1.0f / 6.0f);
+    p = fmaf(p, v, 1.0f) * (1.0f / 5.0f);
+    p = fmaf(p, v, 1.0f) * (1.0f / 4.0f);
+    p = fmaf(p, v, 1.0f) * (1.0f / 3.0f);
+    p = fmaf(p, v, 1.0f) * (1.0f / 2.0f);
+    p = fmaf(p, v, 1.0f) * v;
+    const float e = __expf(v);
+    const bool near = v > -0.5f;
+    ev = near ? 1.0f + p : e;
+    m = near ? p : e - 1.0f;
+}
+
+// softplus and the ratio s(v) / softplus(v), which tends to 1 as v falls.
+__device__ __forceinline__ float softplus(float v) { return v > 20.0f ? v : log1pf(expf(v)); }
+__device__ __forceinline__ float softplus_slope_ratio(float v)
+{
+    if (v < -60.0f) return 1.0f;
+    float s, ns;
+    sigmoid2(v, s, ns);
+    return s / softplus(v);
+}
+
+// The 8-bit form of a run of 64 channels (see mru_packed8): the two factors
+// from its largest magnitude.  IEEE divisions, so that the bits held do not
+// depend on the kernel that packs.
+__device__ __forceinline__ void pack8_factors(float amax, float& inv, float& scale)
+{
+    const bool some = amax >= 7.8886090522101181e-31f;     // 2^-100
+    const bool fine = amax <= 3.402823466e+38f;            // false for infinities and NaN
+    inv = some && fine ? __fdiv_rn(127.0f, amax) : 0.0f;
+    scale = fine ? (some ? __fdiv_rn(amax, 127.0f) : 0.0f) : __int_as_float(0x7fffffff);
+}
+// The integer of x * inv, ties to even (0 for the NaN of infinity times 0).
+__device__ __forceinline__ int pack8_q(float x, float inv) { return __float2int_rn(x * inv); }
+
+// max of magnitudes as bit patterns, in which NaN stays above everything.
+__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+}  // namespace ops
+
+// mru_pack8.cu
+cudaError_t launch_pack8(int64_t rows, int64_t D, int64_t ld, int32_t dtype, const void* x, const mru_packed8& out,
+                         cudaStream_t s);
+
+}  // namespace mru

@@ -12,9 +12,15 @@ Tensor level:
     scan_fused_t(p, x, ...)      -> S [B, L, H, n, n]  or  (o, snapshots)
     scan_t(p, X, ...)            -> S
     build_states_t(p, x, ...)    -> X (or F)
+A recurrent block around the scan:
+    pack8_t(x) -> (q, scale), unpack8_t(q, scale)           activations held in 8 bits
+    gated_problem(...), gated_scan_t, gated_scan_backward_t  elementwise gated recurrence
+    block_problem(...), block_norm_t, block_norm_backward_t  norms, gate and residual of a block
 """
 from __future__ import annotations
 
+import collections
+import contextlib
 import ctypes
 import os
 import threading
@@ -32,7 +38,10 @@ EXPORTS = ["mru_workspace_size", "mru_build_states", "mru_scan", "mru_scan_fused
            "mru_last_device_status", "mru_status_string", "mru_chosen_chunk", "mru_launch_count",
            "mru_set_profile_events", "mru_scan_fused_noalloc", "mru_kernel_name", "mru_effective_math",
            "mru_backward_workspace_size", "mru_scan_backward", "mru_scan_fused_host",
-           "mru_debug_stall_next_fused", "mru_backward_readout_workspace_size", "mru_scan_backward_readout"]
+           "mru_debug_stall_next_fused", "mru_backward_readout_workspace_size", "mru_scan_backward_readout",
+           "mru_pack8", "mru_unpack8", "mru_gated_workspace_size", "mru_gated_backward_workspace_size",
+           "mru_gated_scan", "mru_gated_scan_backward", "mru_block_norm", "mru_block_backward_workspace_size",
+           "mru_block_norm_backward"]
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
 
@@ -49,6 +58,49 @@ class Problem(ctypes.Structure):
 class Readout(ctypes.Structure):
     _fields_ = [("u", ctypes.c_void_p), ("snapshot_every", ctypes.c_int64), ("snapshots", ctypes.c_void_p),
                 ("q", ctypes.c_int32), ("u_per_head", ctypes.c_int32)]
+
+
+GATES = {"decay": 0, "sigmoid": 1, "lru": 2}
+NORMS = {"rms": 0, "layer": 1}
+ACTS = {"none": 0, "silu": 1, "sigmoid": 2}
+PACK8_GROUP, GATED_KEEP = 64, 64
+
+
+class Packed8(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class GatedProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("L", ctypes.c_int64), ("D", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("ld_grad", ctypes.c_int64), ("dtype", ctypes.c_int32), ("gate", ctypes.c_int32),
+                ("c", ctypes.c_float)]
+
+
+class GatedInputs(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("x", "f", "i", "lam", "h0", "reset", "lens")]
+
+
+class GatedSavedBuffers(ctypes.Structure):
+    _fields_ = [("states", ctypes.c_void_p), ("x", Packed8), ("f", Packed8), ("i", Packed8)]
+
+
+class BlockProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int64), ("ld_y", ctypes.c_int64), ("ld_g", ctypes.c_int64),
+                ("ld_dy", ctypes.c_int64), ("ld_dg", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("act", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("res_scale", ctypes.c_float)]
+
+
+class BlockParams(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("w_y", "b_y", "s", "w_z", "b_z")]
+
+
+class BlockSavedBuffers(ctypes.Structure):
+    _fields_ = [("r", Packed8), ("y", Packed8), ("g", Packed8)]
+
+
+class BlockGradBuffers(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("dw_y", "db_y", "ds", "dw_z", "db_z")]
 
 
 class MruError(RuntimeError):
@@ -107,6 +159,23 @@ def load(path: str = LIB_PATH):
             lib.mru_scan_backward_readout.argtypes = [P, vp, vp, ctypes.POINTER(Readout), vp, vp, vp, vp, vp, sz,
                                                       vp]
             lib.mru_scan_backward_readout.restype = ctypes.c_int
+            i32, i64, R = ctypes.c_int32, ctypes.c_int64, ctypes.POINTER
+            lib.mru_pack8.argtypes = [i64, i64, i64, i32, vp, R(Packed8), vp]
+            lib.mru_unpack8.argtypes = [i64, i64, i64, i32, R(Packed8), vp, vp]
+            lib.mru_gated_scan.argtypes = [R(GatedProblem), R(GatedInputs), vp, vp, R(GatedSavedBuffers), vp, sz, vp]
+            lib.mru_gated_scan_backward.argtypes = [R(GatedProblem), R(GatedInputs), R(GatedSavedBuffers), vp, vp, vp,
+                                                    vp, vp, vp, vp, vp, sz, vp]
+            lib.mru_block_norm.argtypes = [R(BlockProblem), R(BlockParams), vp, vp, vp, vp, vp,
+                                           R(BlockSavedBuffers), vp]
+            lib.mru_block_norm_backward.argtypes = [R(BlockProblem), R(BlockParams), vp, vp, vp, R(BlockSavedBuffers),
+                                                    vp, vp, vp, vp, vp, R(BlockGradBuffers), vp, sz, vp]
+            for fn in (lib.mru_pack8, lib.mru_unpack8, lib.mru_gated_scan, lib.mru_gated_scan_backward,
+                       lib.mru_block_norm, lib.mru_block_norm_backward):
+                fn.restype = ctypes.c_int
+            for fn, P1 in ((lib.mru_gated_workspace_size, GatedProblem),
+                           (lib.mru_gated_backward_workspace_size, GatedProblem),
+                           (lib.mru_block_backward_workspace_size, BlockProblem)):
+                fn.argtypes, fn.restype = [R(P1)], sz
             lib.mru_debug_stall_next_fused.argtypes = [ctypes.c_int32]
             lib.mru_debug_stall_next_fused.restype = None
             _lib = lib
@@ -126,6 +195,21 @@ def problem_from_workload(w, **over) -> Problem:
               ldu_offdiag=w.ldu_offdiag, ldu_diag=w.ldu_diag)
     kw.update(over)
     return problem(w.B, w.H, w.L, w.n, **kw)
+
+
+def gated_problem(B, L, D, *, gate="sigmoid", x_dtype="bf16", c=8.0, ld=0, ld_grad=0) -> GatedProblem:
+    dt = {"f32": F32, "bf16": BF16}[x_dtype] if isinstance(x_dtype, str) else int(x_dtype)
+    gt = GATES[gate] if isinstance(gate, str) else int(gate)
+    return GatedProblem(int(B), int(L), int(D), int(ld), int(ld_grad), dt, gt, float(c))
+
+
+def block_problem(rows, D, *, norm="rms", act="silu", x_dtype="bf16", eps=1e-6, res_scale=1.0, ld_y=0, ld_g=0,
+                  ld_dy=0, ld_dg=0) -> BlockProblem:
+    dt = {"f32": F32, "bf16": BF16}[x_dtype] if isinstance(x_dtype, str) else int(x_dtype)
+    nm = NORMS[norm] if isinstance(norm, str) else int(norm)
+    ac = ACTS[act] if isinstance(act, str) else int(act)
+    return BlockProblem(int(rows), int(D), int(ld_y), int(ld_g), int(ld_dy), int(ld_dg), dt, nm, ac, float(eps),
+                        float(res_scale))
 
 
 # ---------------------------------------------------------------- C-ABI ---
@@ -227,6 +311,55 @@ def set_profile_events(handles) -> int:
         return load().mru_set_profile_events(None, 0)
     arr = (ctypes.c_void_p * len(handles))(*handles)
     return load().mru_set_profile_events(arr, len(handles))
+
+
+def _ref(v):
+    return ctypes.byref(v) if v is not None else None
+
+
+def pack8(rows: int, D: int, ld: int, dtype: int, x: int, out: Packed8, stream: int = 0) -> int:
+    return load().mru_pack8(rows, D, ld, dtype, x, _ref(out), stream)
+
+
+def unpack8(rows: int, D: int, ld: int, dtype: int, packed: Packed8, x: int, stream: int = 0) -> int:
+    return load().mru_unpack8(rows, D, ld, dtype, _ref(packed), x, stream)
+
+
+def gated_workspace_size(p: GatedProblem) -> int:
+    return int(load().mru_gated_workspace_size(ctypes.byref(p)))
+
+
+def gated_backward_workspace_size(p: GatedProblem) -> int:
+    return int(load().mru_gated_backward_workspace_size(ctypes.byref(p)))
+
+
+def gated_scan(p: GatedProblem, inputs: GatedInputs, y: int, h_last: int | None, saved: GatedSavedBuffers | None,
+               ws: int, ws_bytes: int, stream: int = 0) -> int:
+    return load().mru_gated_scan(_ref(p), _ref(inputs), y, h_last, _ref(saved), ws, ws_bytes, stream)
+
+
+def gated_scan_backward(p: GatedProblem, inputs: GatedInputs, saved: GatedSavedBuffers, dy: int,
+                        dh_last: int | None, dx: int, df: int, di: int | None, dlam: int | None, dh0: int | None,
+                        ws: int, ws_bytes: int, stream: int = 0) -> int:
+    return load().mru_gated_scan_backward(_ref(p), _ref(inputs), _ref(saved), dy, dh_last, dx, df, di, dlam, dh0,
+                                          ws, ws_bytes, stream)
+
+
+def block_norm(p: BlockProblem, prm: BlockParams | None, r: int, y: int | None, g: int | None, r_out: int | None,
+               z: int | None, saved: BlockSavedBuffers | None = None, stream: int = 0) -> int:
+    return load().mru_block_norm(_ref(p), _ref(prm), r, y, g, r_out, z, _ref(saved), stream)
+
+
+def block_backward_workspace_size(p: BlockProblem) -> int:
+    return int(load().mru_block_backward_workspace_size(ctypes.byref(p)))
+
+
+def block_norm_backward(p: BlockProblem, prm: BlockParams | None, r_out: int | None, y: int | None, g: int | None,
+                        saved: BlockSavedBuffers | None, dr_out: int | None, dz: int | None, dr: int | None,
+                        dy: int | None, dg: int | None, grads: BlockGradBuffers | None, ws: int, ws_bytes: int,
+                        stream: int = 0) -> int:
+    return load().mru_block_norm_backward(_ref(p), _ref(prm), r_out, y, g, _ref(saved), dr_out, dz, dr, dy, dg,
+                                          _ref(grads), ws, ws_bytes, stream)
 
 
 # --------------------------------------------------------- tensor level ---
@@ -406,3 +539,304 @@ def build_states_t(p: Problem, x, *, out=None, ws=None, stream=None):
     rc = build_states(p, _dev_ptr(x, "x"), _dev_ptr(out, "out"), ws.data_ptr(), ws.numel(), _stream(stream))
     _check(rc, "mru_build_states")
     return out
+
+
+# ------------------------------------------------ a block around the scan ---
+
+Packed = collections.namedtuple("Packed", "q scale")
+GatedSaved = collections.namedtuple("GatedSaved", "states x f i")            # x, f, i: Packed or None
+GatedGrads = collections.namedtuple("GatedGrads", "dx df di dlam dh0")
+BlockSaved = collections.namedtuple("BlockSaved", "r y g")                   # Packed, or None where absent
+BlockGrads = collections.namedtuple("BlockGrads", "dr dy dg dw_y db_y ds dw_z db_z")
+
+
+@contextlib.contextmanager
+def _launching(device, stream):
+    """The raw stream of a call on `device`.  Outputs and workspaces made
+    inside belong to that stream; inputs made on another one are the caller's
+    to order (a wait) and to keep alive (record_stream)."""
+    torch = _torch()
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+            return
+        st = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(st):
+            yield st.cuda_stream
+
+
+def _tensor(t, name, shape, dtype, device, contiguous=True):
+    """t's device pointer (None for None) after checking what it is."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _row_stride(t, name):
+    """Elements from one row to the next of a tensor whose last dimension is
+    contiguous and whose leading ones count rows (a slice of wider rows)."""
+    D, ld, rows = t.shape[-1], None, 1
+    if t.numel() == 0:
+        return D
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size != 1:
+            if ld is None:
+                ld = stride
+            elif stride != rows * ld:
+                raise ValueError(f"{name}'s rows must be evenly spaced")
+        rows *= size
+    if D > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    if ld is None:
+        return D
+    if ld < D:
+        raise ValueError(f"{name}'s rows overlap")
+    return ld
+
+
+def _same_stride(tensors):
+    lds = {_row_stride(t, n) for n, t in tensors if t is not None}
+    if len(lds) > 1:
+        raise ValueError(f"{', '.join(n for n, t in tensors if t is not None)} must have the same row stride")
+    return lds.pop() if lds else 0
+
+
+def _x_dtype(p):
+    torch = _torch()
+    return torch.bfloat16 if p.dtype == BF16 else torch.float32
+
+
+def _new_packed(rows, D, device):
+    torch = _torch()
+    return Packed(torch.empty((rows, D), dtype=torch.int8, device=device),
+                  torch.empty((rows, -(-D // PACK8_GROUP)), dtype=torch.float32, device=device))
+
+
+def _packed_arg(v, name, rows, D, device):
+    torch = _torch()
+    if v is None:
+        return Packed8(None, None)
+    return Packed8(_tensor(v.q, f"{name}.q", (rows, D), torch.int8, device),
+                   _tensor(v.scale, f"{name}.scale", (rows, -(-D // PACK8_GROUP)), torch.float32, device))
+
+
+def _new_workspace(nbytes, ws, device, what):
+    if nbytes == 0:
+        raise MruError(ERR_INVALID_ARG, what)
+    return _torch().empty(nbytes, dtype=_torch().uint8, device=device) if ws is None else ws
+
+
+def pack8_t(x, *, out=None, stream=None):
+    """x [..., D] (float32 or bfloat16) held in 8 bits: Packed(q [rows, D]
+    int8, scale [rows, ceil(D / 64)] float32)."""
+    torch = _torch()
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("x must be float32 or bfloat16")
+    D = x.shape[-1]
+    rows = x.numel() // D if D else 0
+    with _launching(x.device, stream) as s:
+        if out is None:
+            out = _new_packed(rows, D, x.device)
+        rc = pack8(rows, D, _row_stride(x, "x"), BF16 if x.dtype == torch.bfloat16 else F32,
+                   _tensor(x, "x", x.shape, x.dtype, x.device, False), _packed_arg(out, "out", rows, D, x.device), s)
+    _check(rc, "mru_pack8")
+    return out
+
+
+def unpack8_t(q, scale, *, dtype=None, out=None, stream=None):
+    """The values q [rows, D] and scale [rows, ceil(D / 64)] hold, as dtype
+    (float32 when not given)."""
+    torch = _torch()
+    rows, D = q.shape
+    if out is not None and dtype is None:
+        dtype = out.dtype
+    dtype = dtype or torch.float32
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("dtype must be float32 or bfloat16")
+    with _launching(q.device, stream) as s:
+        if out is None:
+            out = torch.empty((rows, D), dtype=dtype, device=q.device)
+        rc = unpack8(rows, D, _row_stride(out, "out"), BF16 if dtype == torch.bfloat16 else F32,
+                     _packed_arg(Packed(q, scale), "packed", rows, D, q.device),
+                     _tensor(out, "out", (rows, D), dtype, q.device, False), s)
+    _check(rc, "mru_unpack8")
+    return out
+
+
+def _gated_inputs(p, x, f, i, lam, h0, reset, lens, dev):
+    torch = _torch()
+    dt, shape = _x_dtype(p), (p.B, p.L, p.D)
+    p = GatedProblem(p.B, p.L, p.D, _same_stride([("x", x), ("f", f), ("i", i)]), p.ld_grad, p.dtype, p.gate, p.c)
+    return p, GatedInputs(*[_tensor(t, n, shape, dt, dev, False) for n, t in (("x", x), ("f", f), ("i", i))],
+                          _tensor(lam, "lam", (p.D,), torch.float32, dev),
+                          _tensor(h0, "h0", (p.B, p.D), torch.float32, dev),
+                          _tensor(reset, "reset", (p.B, p.L), torch.uint8, dev),
+                          _tensor(lens, "lens", (p.B,), torch.int32, dev))
+
+
+def _gated_saved(p, saved, dev):
+    K = -(-p.L // GATED_KEEP)
+    return GatedSavedBuffers(_tensor(saved.states, "states", (p.B, K, p.D), _torch().float32, dev),
+                             *[_packed_arg(v, n, p.B * p.L, p.D, dev)
+                               for n, v in (("x", saved.x), ("f", saved.f), ("i", saved.i))])
+
+
+def gated_scan_t(p: GatedProblem, x, f, *, i=None, lam=None, h0=None, reset=None, lens=None, save=None, y=None,
+                 h_last=None, ws=None, stream=None):
+    """Gated linear recurrence: x, f (and for "lru" i) [B, L, D], evenly spaced
+    rows of one stride (slices of one projection's output), lam [D], h0 [B, D]
+    float32, reset [B, L] uint8, lens [B] int32.  Returns (y [B, L, D], h_last
+    [B, D] float32, saved): saved is None, or with save="full" the states the
+    backward needs beside x, f, i, or with save="int8" those and x, f, i in 8
+    bits in their place (or pass a GatedSaved of your own to fill)."""
+    torch = _torch()
+    dev = x.device
+    if save not in (None, "full", "int8") and not isinstance(save, GatedSaved):
+        raise ValueError('save must be None, "full", "int8" or a GatedSaved')
+    with _launching(dev, stream) as s:
+        p, inputs = _gated_inputs(p, x, f, i, lam, h0, reset, lens, dev)
+        if y is None:
+            y = torch.empty((p.B, p.L, p.D), dtype=_x_dtype(p), device=dev)
+        if h_last is None:
+            h_last = torch.empty((p.B, p.D), dtype=torch.float32, device=dev)
+        saved = save if isinstance(save, GatedSaved) else None
+        if isinstance(save, str):
+            packed = [_new_packed(p.B * p.L, p.D, dev) if save == "int8" and t is not None else None
+                      for t in (x, f, i)]
+            saved = GatedSaved(torch.empty((p.B, -(-p.L // GATED_KEEP), p.D), dtype=torch.float32, device=dev),
+                               *packed)
+        ws = _new_workspace(gated_workspace_size(p), ws, dev, "gated_workspace_size")
+        rc = gated_scan(p, inputs, _tensor(y, "y", (p.B, p.L, p.D), _x_dtype(p), dev),
+                        _tensor(h_last, "h_last", (p.B, p.D), torch.float32, dev),
+                        None if saved is None else _gated_saved(p, saved, dev), ws.data_ptr(), ws.numel(), s)
+    _check(rc, "mru_gated_scan")
+    return y, h_last, saved
+
+
+def gated_scan_backward_t(p: GatedProblem, dy, saved, *, x=None, f=None, i=None, lam=None, reset=None, lens=None,
+                          dh_last=None, dx=None, df=None, di=None, dlam=None, dh0=None, ws=None, stream=None):
+    """Gradients of sum <dy, y> + <dh_last, h_last> from what the forward saved
+    (and x, f, i when it saved no 8-bit copies): GatedGrads(dx, df, di, dlam,
+    dh0), di and dlam None unless the gate is "lru"."""
+    torch = _torch()
+    dev = dy.device
+    dt, shape, lru = _x_dtype(p), (p.B, p.L, p.D), p.gate == GATES["lru"]
+    if saved.x is not None:
+        x = f = i = None
+    elif p.B * p.L * p.D and (x is None or f is None or (lru and i is None)):
+        raise ValueError("x, f (and i) are needed: the forward saved no 8-bit copies of them")
+    with _launching(dev, stream) as s:
+        p, inputs = _gated_inputs(p, x, f, i, lam, None, reset, lens, dev)
+        dx = torch.empty(shape, dtype=dt, device=dev) if dx is None else dx
+        df = torch.empty(shape, dtype=dt, device=dev) if df is None else df
+        if lru:
+            di = torch.empty(shape, dtype=dt, device=dev) if di is None else di
+            dlam = torch.empty((p.D,), dtype=torch.float32, device=dev) if dlam is None else dlam
+        if dh0 is None:
+            dh0 = torch.empty((p.B, p.D), dtype=torch.float32, device=dev)
+        p.ld_grad = _same_stride([("dx", dx), ("df", df), ("di", di)])
+        ws = _new_workspace(gated_backward_workspace_size(p), ws, dev, "gated_backward_workspace_size")
+        rc = gated_scan_backward(p, inputs, _gated_saved(p, saved, dev), _tensor(dy, "dy", shape, dt, dev),
+                                 _tensor(dh_last, "dh_last", (p.B, p.D), torch.float32, dev),
+                                 *[_tensor(t, n, shape, dt, dev, False)
+                                   for n, t in (("dx", dx), ("df", df), ("di", di))],
+                                 _tensor(dlam, "dlam", (p.D,), torch.float32, dev),
+                                 _tensor(dh0, "dh0", (p.B, p.D), torch.float32, dev), ws.data_ptr(), ws.numel(), s)
+    _check(rc, "mru_gated_scan_backward")
+    return GatedGrads(dx, df, di, dlam, dh0)
+
+
+def _block_params(p, dev, w_y, b_y, s, w_z, b_z):
+    return BlockParams(*[_tensor(t, n, (p.D,), _torch().float32, dev)
+                         for n, t in (("w_y", w_y), ("b_y", b_y), ("s", s), ("w_z", w_z), ("b_z", b_z))])
+
+
+def _block_with(p, **lds):
+    q = BlockProblem.from_buffer_copy(p)
+    for k, v in lds.items():
+        setattr(q, k, v)
+    return q
+
+
+def block_norm_t(p: BlockProblem, r, *, y=None, g=None, w_y=None, b_y=None, s=None, w_z=None, b_z=None,
+                 norm_after=True, save=None, r_out=None, z=None, stream=None):
+    """r' = r + res_scale * s * act(g) * (N(y) w_y + b_y) and z = N(r') w_z + b_z
+    over rows [..., D] (y and g may be slices of wider rows); parameters [D]
+    float32 or None.  Returns (r', z, saved): r' is r itself without y, z None
+    with norm_after=False, saved a BlockSaved of 8-bit copies with save="int8"
+    (or pass a BlockSaved of your own to fill), else None."""
+    torch = _torch()
+    dev, dt = r.device, _x_dtype(p)
+    if save not in (None, "int8") and not isinstance(save, BlockSaved):
+        raise ValueError('save must be None, "int8" or a BlockSaved')
+    if r.shape[-1] != p.D or r.numel() != p.rows * p.D:
+        raise ValueError(f"r must have {p.rows} rows of {p.D}")
+    with _launching(dev, stream) as st:
+        p = _block_with(p, ld_y=0 if y is None else _row_stride(y, "y"), ld_g=0 if g is None else _row_stride(g, "g"))
+        if y is not None and r_out is None:
+            r_out = torch.empty(r.shape, dtype=dt, device=dev)
+        if norm_after and z is None:
+            z = torch.empty(r.shape, dtype=dt, device=dev)
+        saved = save if isinstance(save, BlockSaved) else None
+        if isinstance(save, str):
+            saved = BlockSaved(*[None if t is None else _new_packed(p.rows, p.D, dev) for t in (r, y, g)])
+        buf = None if saved is None else BlockSavedBuffers(
+            *[_packed_arg(v, n, p.rows, p.D, dev) for n, v in zip(("r", "y", "g"), saved)])
+        rc = block_norm(p, _block_params(p, dev, w_y, b_y, s, w_z, b_z), _tensor(r, "r", r.shape, dt, dev),
+                        _tensor(y, "y", r.shape, dt, dev, False), _tensor(g, "g", r.shape, dt, dev, False),
+                        _tensor(r_out, "r_out", r.shape, dt, dev), _tensor(z, "z", r.shape, dt, dev), buf, st)
+    _check(rc, "mru_block_norm")
+    return (r if y is None else r_out), z, saved
+
+
+def block_norm_backward_t(p: BlockProblem, *, dr_out=None, dz=None, saved=None, r_out=None, y=None, g=None, w_y=None,
+                          b_y=None, s=None, w_z=None, dr=None, dy=None, dg=None, ws=None, stream=None):
+    """Gradients of sum <dr_out, r'> + <dz, z> (either may be None) from the
+    stored r', y and g or from the forward's 8-bit copies: BlockGrads(dr, dy,
+    dg, dw_y, db_y, ds, dw_z, db_z), None where there is no y, g or z; the
+    biases' sums where the norm is "layer" or a b_y was given."""
+    torch = _torch()
+    ref = dz if dz is not None else dr_out
+    if ref is None:
+        raise ValueError("dr_out or dz is needed")
+    dev, dt, shape = ref.device, _x_dtype(p), ref.shape
+    if shape[-1] != p.D or ref.numel() != p.rows * p.D:
+        raise ValueError(f"the gradients must have {p.rows} rows of {p.D}")
+    if saved is not None:
+        r_out = y = g = None
+        has_y, gate = saved.y is not None, saved.g is not None
+    else:
+        has_y, gate = y is not None, g is not None
+    bias = p.norm == NORMS["layer"] or b_y is not None
+    with _launching(dev, stream) as st:
+        dr = torch.empty(shape, dtype=dt, device=dev) if dr is None else dr
+        if has_y and dy is None:
+            dy = torch.empty(shape, dtype=dt, device=dev)
+        if gate and dg is None:
+            dg = torch.empty(shape, dtype=dt, device=dev)
+        p = _block_with(p, **{k: 0 if t is None else _row_stride(t, k[3:])
+                              for k, t in (("ld_y", y), ("ld_g", g), ("ld_dy", dy), ("ld_dg", dg))})
+        want = {"dw_y": has_y, "db_y": has_y and bias, "ds": has_y, "dw_z": dz is not None,
+                "db_z": dz is not None and bias}
+        sums = {k: torch.empty((p.D,), dtype=torch.float32, device=dev) if v else None for k, v in want.items()}
+        buf = None if saved is None else BlockSavedBuffers(
+            *[_packed_arg(v, n, p.rows, p.D, dev) for n, v in zip(("r", "y", "g"), saved)])
+        ws = _new_workspace(block_backward_workspace_size(p), ws, dev, "block_backward_workspace_size")
+        rc = block_norm_backward(p, _block_params(p, dev, w_y, b_y, s, w_z, None),
+                                 _tensor(r_out, "r_out", shape, dt, dev), _tensor(y, "y", shape, dt, dev, False),
+                                 _tensor(g, "g", shape, dt, dev, False), buf,
+                                 _tensor(dr_out, "dr_out", shape, dt, dev), _tensor(dz, "dz", shape, dt, dev),
+                                 _tensor(dr, "dr", shape, dt, dev), _tensor(dy, "dy", shape, dt, dev, False),
+                                 _tensor(dg, "dg", shape, dt, dev, False),
+                                 BlockGradBuffers(*[None if t is None else t.data_ptr() for t in sums.values()]),
+                                 ws.data_ptr(), ws.numel(), st)
+    _check(rc, "mru_block_norm_backward")
+    return BlockGrads(dr, dy, dg, **sums)

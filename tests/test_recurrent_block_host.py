@@ -1,0 +1,298 @@
+"""The block around the scan, without a GPU: the oracle's gradients against
+differences, the 8-bit form's properties, the structs against the header, and
+every refusal of the entry points (nothing is launched: the pointers are never
+followed)."""
+from __future__ import annotations
+
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+
+from linear_rnn_scan_b200 import mru
+from oracle import recurrent_block as orb
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+GATES = ["decay", "sigmoid", "lru"]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from linear_rnn_scan_b200 import build
+    build.build()
+    return mru.load()
+
+
+# ------------------------------------------------------------- the oracle ---
+
+def _gated_case(gate, seed=5, B=2, L=9, D=3):
+    r = np.random.default_rng(seed)
+    v = {"x": r.normal(size=(B, L, D)), "f": r.normal(size=(B, L, D)), "h0": r.normal(size=(B, D))}
+    if gate == "decay":
+        v["f"] = orb.sigmoid(v["f"] + 2)
+    if gate == "lru":
+        v["i"], v["lam"] = r.normal(size=(B, L, D)), r.normal(size=D) - 3
+    masks = {"reset": (r.random((B, L)) < 0.2).astype(np.uint8), "lens": np.array([L, L - 3])}
+    return v, masks, r.normal(size=(B, L, D)), r.normal(size=(B, D))
+
+
+@pytest.mark.parametrize("gate", GATES)
+def test_oracle_recurrence_gradients_match_differences(gate):
+    v, masks, dy, dh = _gated_case(gate)
+
+    def loss(w):
+        o = orb.gated_scan(gate, **w, **masks)
+        return (o["y"] * dy).sum() + (o["h_last"] * dh).sum()
+
+    g = orb.gated_backward(gate, **v, **masks, dy=dy, dh_last=dh)
+    for name, val in v.items():
+        d = g["d" + name]
+        for at in np.ndindex(val.shape):
+            step = 1e-5
+            hi, lo = ({k: (u.copy() if k == name else u) for k, u in v.items()} for _ in range(2))
+            hi[name][at] += step
+            lo[name][at] -= step
+            assert abs((loss(hi) - loss(lo)) / (2 * step) - d[at]) <= 1e-7 * max(1, abs(d[at])), (name, at)
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("act", ["none", "silu", "sigmoid"])
+def test_oracle_block_gradients_match_differences(kind, act):
+    rng = np.random.default_rng(6)
+    R, D = 2, 5
+    v = {k: rng.normal(size=(R, D)) for k in ("r", "y")}
+    if act != "none":
+        v["g"] = rng.normal(size=(R, D))
+    v.update({k: rng.normal(size=D) for k in ("w_y", "b_y", "s", "w_z", "b_z")})
+    dr_out, dz = rng.normal(size=(R, D)), rng.normal(size=(R, D))
+
+    def loss(w):
+        o = orb.block_norm(kind, act, eps=1e-3, res_scale=0.7, **w)
+        return (o["r"] * dr_out).sum() + (o["z"] * dz).sum()
+
+    o = orb.block_norm(kind, act, eps=1e-3, res_scale=0.7, **v)
+    g = orb.block_backward(kind, act, r=o["r"], y=v["y"], g=v.get("g"), dr_out=dr_out, dz=dz, eps=1e-3, res_scale=0.7,
+                           **{k: v[k] for k in ("w_y", "b_y", "s", "w_z")})
+    for name, val in v.items():
+        for at in np.ndindex(val.shape):
+            hi, lo = ({k: (u.copy() if k == name else u) for k, u in v.items()} for _ in range(2))
+            hi[name][at] += 1e-5
+            lo[name][at] -= 1e-5
+            d = g["d" + name][at]
+            assert abs((loss(hi) - loss(lo)) / 2e-5 - d) <= 1e-6 * max(1, abs(d)), (name, at)
+
+
+def test_oracle_recurrence_closed_forms():
+    # a constant decay and input sum a geometric series; a reset starts again; padding keeps the state
+    L, a, x = 50, 0.9, 2.0
+    o = orb.gated_scan("decay", np.full((1, L, 1), x), np.full((1, L, 1), a), h0=np.full((1, 1), 3.0))
+    t = np.arange(1, L + 1)
+    assert np.allclose(o["y"][0, :, 0], 3.0 * a ** t + x * (1 - a ** t) / (1 - a), rtol=1e-12)
+    reset = np.zeros((1, L), np.uint8)
+    reset[0, 20] = 1
+    r = orb.gated_scan("decay", np.full((1, L, 1), x), np.full((1, L, 1), a), reset=reset, lens=[40])
+    assert np.allclose(r["y"][0, 20:40, 0], x * (1 - a ** t[:20]) / (1 - a), rtol=1e-12)
+    assert np.all(r["y"][0, 40:] == 0) and r["h_last"][0, 0] == r["y"][0, 39, 0]
+
+
+def test_oracle_8bit_form():
+    rng = np.random.default_rng(7)
+    x = rng.normal(size=(9, 200)).astype(np.float32)
+    x[3, 64:128] = 0
+    x[4, 5] = np.inf
+    x[5, 199] = np.nan
+    x[6, :64] *= np.float32(1e-35)
+    q, scale = orb.pack8(x)
+    held = orb.unpack8(q, scale)
+    assert np.isnan(held[4, :64]).all() and np.isfinite(held[4, 64:]).all()
+    assert np.isnan(held[5, 192:]).all() and np.isfinite(held[5, :192]).all()
+    assert (held[3, 64:128] == 0).all() and (held[6, :64] == 0).all() and scale[6, 0] == 0
+    fine = np.isfinite(held)
+    step = np.repeat(scale, 64, axis=1)[:, :200]
+    assert (np.abs(held - x)[fine] <= 0.5001 * np.maximum(step, 2.0 ** -100)[fine]).all()
+    assert np.abs(q).max() == 127
+
+
+# ---------------------------------------------------------------- structs ---
+
+@pytest.mark.parametrize("name,cls", [("mru_gated_problem", mru.GatedProblem), ("mru_block_problem", mru.BlockProblem)])
+def test_problem_structs_match_header(name, cls):
+    text = open(os.path.join(ROOT, "include", "mru.h")).read()
+    body = re.search(r"typedef struct \{([^{}]*)\} " + name + ";", text, re.S).group(1)
+    body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+    widths = {"int64_t": 8, "int32_t": 4, "float": 4}
+    fields = [(nm.strip(), widths[d.split(None, 1)[0]])
+              for d in (d.strip() for d in body.split(";")) if d for nm in d.split(None, 1)[1].split(",")]
+    assert fields == [(f, ctypes.sizeof(t)) for f, t in cls._fields_]
+
+
+# --------------------------------------------------------------- refusals ---
+
+A = 1 << 30                          # fake addresses, 16 MB apart
+at = lambda k: A + k * (1 << 24)     # noqa: E731
+
+
+def _gated(lib, p=None, ws_bytes=None, backward=False, saved="full", **over):
+    p = p or mru.gated_problem(2, 100, 64, gate="lru")
+    a = {"x": at(1), "f": at(2), "i": at(3), "lam": at(4), "h0": at(5), "reset": at(6), "lens": at(7), "y": at(8),
+         "h_last": at(9), "states": at(10), "dy": at(11), "dh_last": at(12), "dx": at(13), "df": at(14), "di": at(15),
+         "dlam": at(16), "dh0": at(17), "ws": at(18)}
+    if backward:
+        a["h0"] = None
+    a.update(over)
+    inputs = mru.GatedInputs(*[a[k] for k in ("x", "f", "i", "lam", "h0", "reset", "lens")])
+    pk = [mru.Packed8(None, None)] * 3
+    if saved == "int8":
+        pk = [mru.Packed8(at(20 + 2 * k), at(21 + 2 * k)) for k in range(3)]
+    elif isinstance(saved, list):
+        pk = saved
+    keep = mru.GatedSavedBuffers(a["states"], *pk) if saved else None
+    if backward:
+        need = mru.gated_backward_workspace_size(p) if ws_bytes is None else ws_bytes
+        return mru.gated_scan_backward(p, inputs, keep, a["dy"], a["dh_last"], a["dx"], a["df"], a["di"], a["dlam"],
+                                       a["dh0"], a["ws"], need)
+    need = mru.gated_workspace_size(p) if ws_bytes is None else ws_bytes
+    return mru.gated_scan(p, inputs, a["y"], a["h_last"], keep, a["ws"], need)
+
+
+@pytest.mark.parametrize("over", [dict(x=None), dict(f=None), dict(i=None), dict(lam=None), dict(y=None), dict(ws=None),
+                                  dict(x=at(1) + 1), dict(lam=at(4) + 2), dict(h0=at(5) + 1), dict(h_last=at(9) + 2),
+                                  dict(ws=at(18) + 8), dict(states=None), dict(states=at(10) + 1), dict(lens=at(7) + 2),
+                                  dict(y=at(1)), dict(y=at(2) + 64), dict(h_last=at(5)), dict(states=at(8)),
+                                  dict(ws=at(9))])
+def test_recurrence_refuses_bad_buffers(lib, over):
+    assert _gated(lib, **over) == mru.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", [dict(x=None), dict(i=None), dict(lam=None), dict(dy=None), dict(dx=None),
+                                  dict(df=None), dict(di=None), dict(states=None), dict(saved=None), dict(ws=None),
+                                  dict(dy=at(11) + 1), dict(dlam=at(16) + 2), dict(dx=at(1)), dict(df=at(13) + 128),
+                                  dict(dh0=at(12)), dict(dx=at(10)), dict(di=at(11))])
+def test_recurrence_backward_refuses_bad_buffers(lib, over):
+    assert _gated(lib, backward=True, **over) == mru.ERR_INVALID_ARG
+
+
+def test_recurrence_refuses_bad_problems(lib):
+    ok = dict(B=2, L=100, D=64)
+    for kw in (dict(ok, B=-1), dict(ok, L=-1), dict(ok, D=-1), dict(ok, ld=63), dict(ok, ld=-64), dict(ok, ld_grad=1),
+               dict(ok, gate=3), dict(ok, gate=-1), dict(ok, x_dtype=2), dict(ok, gate="lru", c=0.0),
+               dict(ok, gate="lru", c=-1.0), dict(ok, gate="lru", c=float("nan")),
+               dict(ok, gate="lru", c=float("inf"))):
+        p = mru.gated_problem(**kw)
+        assert mru.gated_workspace_size(p) == 0 and mru.gated_backward_workspace_size(p) == 0
+        assert _gated(lib, p=p, ws_bytes=1 << 20) == mru.ERR_INVALID_ARG, kw
+        assert _gated(lib, p=p, ws_bytes=1 << 20, backward=True) == mru.ERR_INVALID_ARG, kw
+    for kw in (dict(B=1 << 20, L=1 << 30, D=64), dict(B=1 << 40, L=1, D=1), dict(B=1, L=1 << 40, D=1),
+               dict(B=1, L=1, D=1 << 40)):
+        p = mru.gated_problem(**kw)
+        assert mru.gated_workspace_size(p) == 0
+        assert _gated(lib, p=p, ws_bytes=1 << 20, saved=None, i=None, lam=None) == mru.ERR_UNSUPPORTED, kw
+    assert _gated(lib, ws_bytes=255) == mru.ERR_WORKSPACE
+    assert _gated(lib, ws_bytes=255, backward=True) == mru.ERR_WORKSPACE
+    # inputs of another gate, and 8-bit copies that are incomplete
+    p = mru.gated_problem(2, 100, 64, gate="sigmoid")
+    assert _gated(lib, p=p) == mru.ERR_INVALID_ARG                                        # i and lam given
+    assert _gated(lib, p=p, i=None) == mru.ERR_INVALID_ARG                                # lam given
+    assert _gated(lib, p=p, i=None, lam=None, backward=True) == mru.ERR_INVALID_ARG       # di and dlam given
+    none = mru.Packed8(None, None)
+    some = [mru.Packed8(at(20), at(21)), mru.Packed8(at(22), at(23)), none]
+    for bwd in (False, True):
+        assert _gated(lib, saved=some, backward=bwd) == mru.ERR_INVALID_ARG               # i's copy missing
+        assert _gated(lib, saved=[some[0], none, some[1]], backward=bwd) == mru.ERR_INVALID_ARG
+        assert _gated(lib, saved=[mru.Packed8(at(20), None)] + some[:2], backward=bwd) == mru.ERR_INVALID_ARG
+        assert _gated(lib, saved=[mru.Packed8(at(20), at(21) + 2)] + some[:2], backward=bwd) == mru.ERR_INVALID_ARG
+    assert mru.load().mru_gated_scan(None, None, None, None, None, None, 0, None) == mru.ERR_INVALID_ARG
+
+
+def test_recurrence_knows_interleaved_slices(lib):
+    # slices of rows of one projection do not overlap; slices that share a column do
+    p = mru.gated_problem(2, 100, 64, gate="lru", ld=256, ld_grad=192)
+    assert _gated(lib, p=p, x=at(1), f=at(1) + 128, i=at(1) + 256, ws_bytes=255) == mru.ERR_WORKSPACE
+    kw = dict(p=p, x=at(1), f=at(1) + 128, i=at(1) + 256, backward=True, ws_bytes=255)
+    assert _gated(lib, dx=at(13), df=at(13) + 128, di=at(13) + 256, **kw) == mru.ERR_WORKSPACE
+    assert _gated(lib, dx=at(13), df=at(13) + 126, di=at(13) + 256, **kw) == mru.ERR_INVALID_ARG
+    assert _gated(lib, dx=at(13), df=at(13) + 128, di=at(13) + 258, **kw) == mru.ERR_INVALID_ARG
+    # the last column wraps into the next row's first
+    assert _gated(lib, dx=at(13), df=at(13) + 128, di=at(13) + 260, **kw) == mru.ERR_INVALID_ARG
+
+
+def _block(lib, p=None, backward=False, ws_bytes=None, saved=None, **over):
+    p = p or mru.block_problem(10, 64)
+    a = {k: at(j + 1) for j, k in enumerate(("r", "y", "g", "r_out", "z", "w_y", "b_y", "s", "w_z", "b_z", "dro", "dz",
+                                             "dr", "dy", "dg", "dw_y", "db_y", "ds", "dw_z", "db_z", "ws"))}
+    a.update(over)
+    prm = mru.BlockParams(*[a[k] for k in ("w_y", "b_y", "s", "w_z", "b_z")])
+    keep = None
+    if saved:
+        keep = mru.BlockSavedBuffers(*[mru.Packed8(at(30 + 2 * k), at(31 + 2 * k)) if v else mru.Packed8(None, None)
+                                       for k, v in enumerate(saved)])
+    if backward:
+        gr = mru.BlockGradBuffers(*[a[k] for k in ("dw_y", "db_y", "ds", "dw_z", "db_z")])
+        need = mru.block_backward_workspace_size(p) if ws_bytes is None else ws_bytes
+        return mru.block_norm_backward(p, prm, a["r_out"], a["y"], a["g"], keep, a["dro"], a["dz"], a["dr"], a["dy"],
+                                       a["dg"], gr, a["ws"], need)
+    return mru.block_norm(p, prm, a["r"], a["y"], a["g"], a["r_out"], a["z"], keep)
+
+
+@pytest.mark.parametrize("over", [dict(r=None), dict(r_out=None), dict(y=None), dict(g=None), dict(y=None, r_out=None),
+                                  dict(y=None, g=None, r_out=None, z=None), dict(r=at(1) + 1), dict(z=at(5) + 1),
+                                  dict(w_y=at(6) + 2), dict(r_out=at(1)), dict(z=at(4)), dict(z=at(6)),
+                                  dict(saved=(1, 1, 0)), dict(saved=(0, 1, 1)), dict(saved=(1, 0, 1))])
+def test_block_refuses_bad_buffers(lib, over):
+    assert _block(lib, **over) == mru.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", [dict(r_out=None), dict(dro=None, dz=None), dict(dy=None), dict(dg=None), dict(g=None),
+                                  dict(y=None), dict(ws=None), dict(ws=at(21) + 4), dict(dz=at(12) + 1),
+                                  dict(ds=at(18) + 2), dict(dy=at(2)), dict(dr=at(11)), dict(dr=at(14)),
+                                  dict(saved=(1, 0, 0)), dict(saved=(0, 1, 1)), dict(saved=(1, 1, 0))])
+def test_block_backward_refuses_bad_buffers(lib, over):
+    assert _block(lib, backward=True, **over) == mru.ERR_INVALID_ARG
+
+
+def test_block_refuses_bad_problems(lib):
+    ok = dict(rows=10, D=64)
+    for kw in (dict(ok, rows=-1), dict(ok, D=-1), dict(ok, ld_y=63), dict(ok, ld_g=-1), dict(ok, ld_dy=2),
+               dict(ok, ld_dg=63), dict(ok, norm=2), dict(ok, act=3), dict(ok, act=-1), dict(ok, x_dtype=5),
+               dict(ok, eps=-1e-6), dict(ok, eps=float("nan"))):
+        p = mru.block_problem(**kw)
+        assert mru.block_backward_workspace_size(p) == 0
+        assert _block(lib, p=p) == mru.ERR_INVALID_ARG and \
+            _block(lib, p=p, backward=True, ws_bytes=1 << 20) == mru.ERR_INVALID_ARG, kw
+    p = mru.block_problem(10, 16385)
+    assert _block(lib, p=p) == mru.ERR_UNSUPPORTED
+    assert _block(lib, p=p, backward=True, ws_bytes=1 << 20) == mru.ERR_UNSUPPORTED
+    p = mru.block_problem(10, 64, act="none")
+    assert _block(lib, p=p) == mru.ERR_INVALID_ARG                          # a gate without an activation
+    assert _block(lib, backward=True, ws_bytes=255) == mru.ERR_WORKSPACE
+
+
+def test_pack8_refuses(lib):
+    pk = mru.Packed8(at(2), at(3))
+    call = lambda rows=4, D=100, ld=0, dt=1, x=at(1), h=pk: (mru.pack8(rows, D, ld, dt, x, h),  # noqa: E731
+                                                              mru.unpack8(rows, D, ld, dt, h, x))
+    bad = (mru.ERR_INVALID_ARG,) * 2
+    for kw in (dict(rows=-1), dict(D=-1), dict(ld=99), dict(ld=-1), dict(dt=2), dict(x=None), dict(x=at(1) + 1),
+               dict(h=None), dict(h=mru.Packed8(None, at(3))), dict(h=mru.Packed8(at(2), None)),
+               dict(h=mru.Packed8(at(2), at(3) + 1)), dict(h=mru.Packed8(at(1) + 10, at(3))),
+               dict(h=mru.Packed8(at(2), at(1) + 8))):
+        assert call(**kw) == bad, kw
+    assert call(rows=0) == call(D=0) == (mru.OK,) * 2
+
+
+def test_tensor_level_names_what_is_wrong(lib):
+    import torch
+    x = torch.zeros(2, 4, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        mru._tensor(x, "x", x.shape, x.dtype, x.device)
+    wide = torch.zeros(2, 4, 24)
+    assert mru._row_stride(wide[..., 8:16], "x") == 24 and mru._row_stride(x, "x") == 8
+    assert mru._row_stride(torch.zeros(2, 1, 24)[..., :8], "x") == 24
+    for v, what in ((x.transpose(1, 2), "evenly|contiguous"), (wide[:, :3, :8], "evenly"),
+                    (x[:1, :1].expand(2, 4, 8), "overlap"), (wide[..., ::3], "contiguous")):
+        with pytest.raises(ValueError, match=what):
+            mru._row_stride(v, "x")
+    with pytest.raises(ValueError, match="same row stride"):
+        mru._same_stride([("x", wide[..., :8]), ("f", x)])
