@@ -413,11 +413,22 @@ mru_status mru_gated_scan(const mru_gated_problem* p, const mru_gated_inputs* in
  *   dy [B, L, D] contiguous;  dh_last [B, D] fp32 or NULL: zero
  *   dx, df, di [B, L, D], ld_grad apart;  dlam [D], dh0 [B, D] fp32 or NULL
  * in->h0 is not read.  Gradients of values kept in 8 bits are those at the
- * values held.  The same call gives the same bits every time. */
+ * values held: x, f, i are, and h_{t-1} is run over them in pieces of 64 tokens
+ * from the kept states (before a piece's first token it is the last of the
+ * piece before).  The same call gives the same bits every time. */
 mru_status mru_gated_scan_backward(const mru_gated_problem* p, const mru_gated_inputs* in,
                                    const mru_gated_saved* saved, const void* dy, const float* dh_last, void* dx,
                                    void* df, void* di, float* dlam, float* dh0, void* ws, size_t ws_bytes,
                                    void* stream);
+
+/* Testing hook for the bounded waits of the recurrence.  Tiles of 64 tokens
+ * wait for the maps of the tiles before them (only for tiles that are being
+ * worked on); every wait gives up after 2 s, records MRU_ERR_TIMEOUT in the
+ * status word and the launch ends early, its outputs unspecified.  After this
+ * call, the next launch in the process with more than 64 tokens never
+ * publishes its first tile's map and waits for `ms` milliseconds (> 0) at
+ * most; ms <= 0 cancels a pending request. */
+void mru_debug_stall_next_gated(int32_t ms);
 
 /* The ends of a block around a sublayer whose output is y, row by row:
  *     r' = r + res_scale * s * act(g) * (N(y) w_y + b_y)

@@ -14,7 +14,10 @@ namespace ops {
 
 // ------------------------------------------------------------------ host ---
 
-inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+__host__ __device__ inline bool aligned(const void* p, size_t a)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
 inline size_t elem_size(int32_t dtype) { return dtype == MRU_BF16 ? 2 : 4; }
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align256(size_t v) { return (v + 255) / 256 * 256; }
@@ -75,35 +78,40 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// s(v) and 1 - s(v) = s(-v), both to a few ulp: with e = exp(-|v|) in (0, 1]
-// neither form overflows or cancels.
+// s(v) and 1 - s(v) = s(-v), both to a few ulp: with e = exp(-v) they are
+// 1 / (1 + e) and e / (1 + e), where nothing cancels.  Below -80 the logit
+// counts as -80 (s = 2e-35), so that e stays finite; NaN stays NaN.
 __device__ __forceinline__ void sigmoid2(float v, float& s, float& ns)
 {
-    const float e = __expf(-fabsf(v));
-    const float r = __fdividef(1.0f, 1.0f + e);
-    const float q = e * r;
-    s = v >= 0.0f ? r : q;
-    ns = v >= 0.0f ? q : r;
-    if (v != v) s = ns = v;
+    float c;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(v), "f"(-80.0f));
+    const float e = __expf(-c);
+    s = __fdividef(1.0f, 1.0f + e);
+    ns = e * s;
 }
 
 // e^v and e^v - 1 for v <= 0, both to a few ulp.  Near 0 the difference is the
 // Taylor series (eight terms: the ninth is below 2^-26 of the sum for
 // v >= -0.5) and e^v is 1 more, so that a decay near 1 keeps only its own
-// rounding; further out it is the other way round.
+// rounding; further out it is the other way round.  NEAR: v >= -0.5 is known.
+template <bool NEAR = false>
 __device__ __forceinline__ void exp_expm1_neg(float v, float& ev, float& m)
 {
-    float p = fmaf(v, 1.0f / 8.0f, 1.0f) * (1.0f / 7.0f);
-    p = fmaf(p, v, 1.0f) * (1.0f / 6.0f);
-    p = fmaf(p, v, 1.0f) * (1.0f / 5.0f);
-    p = fmaf(p, v, 1.0f) * (1.0f / 4.0f);
-    p = fmaf(p, v, 1.0f) * (1.0f / 3.0f);
-    p = fmaf(p, v, 1.0f) * (1.0f / 2.0f);
-    p = fmaf(p, v, 1.0f) * v;
-    const float e = __expf(v);
-    const bool near = v > -0.5f;
-    ev = near ? 1.0f + p : e;
-    m = near ? p : e - 1.0f;
+    float p = fmaf(v, 1.0f / 40320.0f, 1.0f / 5040.0f);
+    p = fmaf(p, v, 1.0f / 720.0f);
+    p = fmaf(p, v, 1.0f / 120.0f);
+    p = fmaf(p, v, 1.0f / 24.0f);
+    p = fmaf(p, v, 1.0f / 6.0f);
+    p = fmaf(p, v, 0.5f);
+    p = fmaf(p * v, v, v);
+    m = p;
+    ev = 1.0f + p;
+    if constexpr (!NEAR) {
+        if (v < -0.5f) {
+            ev = __expf(v);
+            m = ev - 1.0f;
+        }
+    }
 }
 
 // softplus and the ratio s(v) / softplus(v), which tends to 1 as v falls.
@@ -126,8 +134,12 @@ __device__ __forceinline__ void pack8_factors(float amax, float& inv, float& sca
     inv = some && fine ? __fdiv_rn(127.0f, amax) : 0.0f;
     scale = fine ? (some ? __fdiv_rn(amax, 127.0f) : 0.0f) : __int_as_float(0x7fffffff);
 }
-// The integer of x * inv, ties to even (0 for the NaN of infinity times 0).
-__device__ __forceinline__ int pack8_q(float x, float inv) { return __float2int_rn(x * inv); }
+// The integer of x * inv (at most 127 in size), ties to even: next to 1.5 * 2^23
+// floats are whole numbers, and the low byte of the sum's bits is the integer's.
+__device__ __forceinline__ int pack8_q(float x, float inv)
+{
+    return __float_as_int(__fadd_rn(__fmul_rn(x, inv), 12582912.0f)) & 0xff;
+}
 
 // max of magnitudes as bit patterns, in which NaN stays above everything.
 __device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }

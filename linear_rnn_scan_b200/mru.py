@@ -41,7 +41,7 @@ EXPORTS = ["mru_workspace_size", "mru_build_states", "mru_scan", "mru_scan_fused
            "mru_debug_stall_next_fused", "mru_backward_readout_workspace_size", "mru_scan_backward_readout",
            "mru_pack8", "mru_unpack8", "mru_gated_workspace_size", "mru_gated_backward_workspace_size",
            "mru_gated_scan", "mru_gated_scan_backward", "mru_block_norm", "mru_block_backward_workspace_size",
-           "mru_block_norm_backward"]
+           "mru_block_norm_backward", "mru_debug_stall_next_gated"]
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
 
@@ -169,6 +169,8 @@ def load(path: str = LIB_PATH):
                                            R(BlockSavedBuffers), vp]
             lib.mru_block_norm_backward.argtypes = [R(BlockProblem), R(BlockParams), vp, vp, vp, R(BlockSavedBuffers),
                                                     vp, vp, vp, vp, vp, R(BlockGradBuffers), vp, sz, vp]
+            lib.mru_debug_stall_next_gated.argtypes = [i32]
+            lib.mru_debug_stall_next_gated.restype = None
             for fn in (lib.mru_pack8, lib.mru_unpack8, lib.mru_gated_scan, lib.mru_gated_scan_backward,
                        lib.mru_block_norm, lib.mru_block_norm_backward):
                 fn.restype = ctypes.c_int
@@ -343,6 +345,12 @@ def gated_scan_backward(p: GatedProblem, inputs: GatedInputs, saved: GatedSavedB
                         ws: int, ws_bytes: int, stream: int = 0) -> int:
     return load().mru_gated_scan_backward(_ref(p), _ref(inputs), _ref(saved), dy, dh_last, dx, df, di, dlam, dh0,
                                           ws, ws_bytes, stream)
+
+
+def debug_stall_next_gated(ms: int) -> None:
+    """Testing hook: the next launch of the recurrence with more than 64 tokens
+    withholds its first tile's map and bounds its waits by `ms` milliseconds."""
+    load().mru_debug_stall_next_gated(int(ms))
 
 
 def block_norm(p: BlockProblem, prm: BlockParams | None, r: int, y: int | None, g: int | None, r_out: int | None,

@@ -94,8 +94,9 @@ def valid_mask(B, L, lens):
 
 def gated_scan(gate, x, f, i=None, lam=None, c=8.0, h0=None, reset=None, lens=None, restart=None):
     """y, h_last, kept states, h_{t-1} of every token, each with its error
-    bound: dict of float64 arrays.  restart: kept states from which every 64th
-    token starts anew (what the backward does)."""
+    bound: dict of float64 arrays.  restart: kept states from which pieces of
+    64 tokens start (what the backward does; the state before a piece's first
+    token is the last of the piece before)."""
     x, f = np.asarray(x, np.float64), np.asarray(f, np.float64)
     B, L, D = x.shape
     i = None if i is None else np.asarray(i, np.float64)
@@ -108,15 +109,16 @@ def gated_scan(gate, x, f, i=None, lam=None, c=8.0, h0=None, reset=None, lens=No
     h = np.zeros((B, D)) if h0 is None else np.asarray(h0, np.float64).copy()
     H, e = np.abs(h), np.zeros((B, D))
     for t in range(L):
+        m = ok[:, t][:, None]
+        r = np.zeros((B, 1), bool) if reset is None else (np.asarray(reset)[:, t] != 0)[:, None] & m
+        if restart is not None and t == 0:
+            h, H = restart[:, 0].copy(), np.abs(restart[:, 0])
+        out["prev"][:, t], out["prev_err"][:, t], out["prev_maj"][:, t] = (np.where(r, 0, v) for v in (h, e, H))
         if t % KEEP == 0:
             if restart is not None:
                 h, H, e = restart[:, t // KEEP].copy(), np.abs(restart[:, t // KEEP]), np.zeros((B, D))
             out["states"][:, t // KEEP], out["states_err"][:, t // KEEP] = h, e + U * np.abs(h)
-        m = ok[:, t][:, None]
-        if reset is not None:
-            r = (np.asarray(reset)[:, t] != 0)[:, None] & m
-            h, H, e = np.where(r, 0, h), np.where(r, 0, H), np.where(r, 0, e)
-        out["prev"][:, t], out["prev_err"][:, t], out["prev_maj"][:, t] = h, e, H
+        h, H, e = np.where(r, 0, h), np.where(r, 0, H), np.where(r, 0, e)
         with np.errstate(all="ignore"):
             g = gate_values(gate, x[:, t], f[:, t], None if i is None else i[:, t], lam, c)
             hn = g["a"] * h + g["b"]

@@ -365,6 +365,34 @@ def test_recurrence_writes_nothing_else():
     assert mru.last_device_status(wb.data_ptr(), t.cuda.current_stream().cuda_stream) == mru.OK
 
 
+@pytest.mark.parametrize("backward", [False, True])
+def test_recurrence_bounded_waits(backward):
+    """A map that never comes: the waits give up, the call reports a timeout,
+    and the next call is as ever."""
+    t = torch()
+    v, g = make_gated("sigmoid", "f32", 2, 1000, 70, seed=51)
+    want = run_gated_backward("sigmoid", "f32", v, g)
+    p = mru.gated_problem(2, 1000, 70, gate="sigmoid", x_dtype="f32")
+    x, f, rest = _dev(v["x"]), _dev(v["f"]), {k: _dev(v[k]) for k in ("reset", "lens")}
+    stream = t.cuda.current_stream().cuda_stream
+    ws = t.empty(mru.gated_workspace_size(p), dtype=t.uint8, device="cuda")
+    wb = t.empty(mru.gated_backward_workspace_size(p), dtype=t.uint8, device="cuda")
+    mru.debug_stall_next_gated(0 if backward else 20)
+    saved = mru.gated_scan_t(p, x, f, h0=_dev(v["h0"]), save="full", ws=ws, **rest)[2]
+    assert mru.last_device_status(ws.data_ptr(), stream) == (mru.OK if backward else mru.ERR_TIMEOUT)
+    if backward:
+        mru.debug_stall_next_gated(20)
+    else:
+        saved = mru.gated_scan_t(p, x, f, h0=_dev(v["h0"]), save="full", ws=ws, **rest)[2]
+        assert mru.last_device_status(ws.data_ptr(), stream) == mru.OK
+    kw = dict(x=x, f=f, dh_last=_dev(g["dh_last"]), ws=wb, **rest)
+    mru.gated_scan_backward_t(p, _dev(g["dy"]), saved, **kw)
+    assert mru.last_device_status(wb.data_ptr(), stream) == (mru.ERR_TIMEOUT if backward else mru.OK)
+    gr = mru.gated_scan_backward_t(p, _dev(g["dy"]), saved, **kw)
+    assert mru.last_device_status(wb.data_ptr(), stream) == mru.OK
+    assert t.equal(gr.dx, want[3].dx) and t.equal(gr.df, want[3].df) and t.equal(gr.dh0, want[3].dh0)
+
+
 # ------------------------------------------------------------------ block ---
 
 def make_block(norm, act, dtype, rows, D, seed):
