@@ -62,7 +62,7 @@ __device__ __forceinline__ void gradient_factors(float x, float f, float i, floa
         const float la = -csp * sf;
         exp_expm1_neg<NEAR>(la, a, m);
         const float v = -m * (1.0f + a);                   // 1 - a^2
-        const float r = v > 0.0f ? rsqrtf(v) : 0.0f;       // la / u tends to 0 with u
+        const float r = v > 0.0f ? inv_root(v) : 0.0f;     // la / u tends to 0 with u
         const float sx = si * x, u = v * r;
         cx = u * si;
         b = u * sx;
@@ -142,71 +142,99 @@ __global__ void __launch_bounds__(128) k_gated_short_bwd(Args g)
     if (GATE == MRU_GATE_LRU && g.dlam_part) g.dlam_part[ch] = dlam;
 }
 
-// ------------------------------------------------------------------ tiles ---
+// ---------------------------------------------------------------- forward ---
 
-// Shared memory of a tile kernel beside its stages.
+// Channels of a lane: tiles of 128 channels in bf16's forward, of 64 elsewhere.
+constexpr int fwd_channels(size_t elem) { return elem == 2 ? 4 : 2; }
+constexpr int kBwdC = 2;
+
+template <int C>
 struct TileMem {
-    float4 agg[kWarps][32];              // a warp's map, two channels to a lane
-    float4 ent[2 * kFan][32];            // what the carry is made of
-    float csp[2][kCh];
-    uint32_t next[2];
+    MapRow<C> agg[kWarps];               // the warps' maps
+    Entries<C> ent;
+    float csp[32 * C];                   // c softplus(lam) of the tile's channels
+    Tile tile[3];                        // this one, the next, the one after
 };
 
-// Draws tiles in the order of the scan.  A tile waits only for tiles drawn
-// before it, and a block works through its tiles in the order drawn, so the
-// earliest unfinished tile never waits.
-__device__ __forceinline__ uint32_t draw(const Args& g, uint32_t before)
+template <int C>
+__device__ __forceinline__ Vec<C> csp_of(const float* csp, int lane)
 {
-    return g.ticket ? atomicAdd(g.ticket, 1u) : before + gridDim.x;
+    return read_row<C>(csp + C * lane);
 }
 
-// Tokens of a warp that are not padding, and which of them start anew.
-__device__ __forceinline__ void warp_masks(const Args& g, const Tile& t, int w, int lane, int& n, uint32_t& resets)
+template <int C>
+__device__ __forceinline__ bool all_near(const Vec<C>& csp)
 {
-    const int64_t at = t.t0 + w * kStep, left = valid_tokens(g, t.b) - at;
-    n = left <= 0 ? 0 : left < kStep ? (int)left : kStep;
-    resets = 0;
-    if (g.reset) resets = __ballot_sync(~0u, lane < n && g.reset[t.b * g.L + at + lane] != 0);
+    bool near = true;
+#pragma unroll
+    for (int c = 0; c < C; ++c) near = near && csp.v[c] <= 0.5f;
+    return __all_sync(~0u, near);
 }
 
-// 8-bit copies of a warp's tokens: a run of 64 channels is the warp's row, so
-// a lane takes the factors of one run (token and input) for all.
-template <typename T, int NIN>
+// 8-bit copies of a warp's tokens.  A run of 64 channels is 64 / C lanes of a
+// row; the largest magnitudes of all runs (input, token, half) are found first
+// and a lane takes the factors of one or two of them for all.
+template <typename T, int C, int NIN>
 __device__ __forceinline__ void pack_rows(const Args& g, const Tile& t, int w, int lane, const T* stage, bool wide8)
 {
-    uint32_t mine = 0;
+    constexpr int kCh = 32 * C, HALVES = kCh / 64, RUNS = NIN * kStep * HALVES, SETS = (RUNS + 31) / 32;
+    uint32_t mine[SETS];
+#pragma unroll
+    for (int k = 0; k < SETS; ++k) mine[k] = 0;
 #pragma unroll
     for (int n = 0; n < NIN; ++n)
 #pragma unroll
         for (int s = 0; s < kStep; ++s) {
-            const float2 v = pair_at(stage + (n * kTok + w * kStep + s) * kCh + 2 * lane);
-            const uint32_t m = __reduce_max_sync(~0u, max(mag_bits(v.x), mag_bits(v.y)));
-            if (lane == n * kStep + s) mine = m;
+            const Vec<C> v = read_row<C>(stage + (n * kTok + w * kStep + s) * kCh + C * lane);
+            uint32_t m = 0;
+#pragma unroll
+            for (int c = 0; c < C; ++c) m = max(m, mag_bits(v.v[c]));
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+                const int run = (n * kStep + s) * HALVES + h;
+                const uint32_t r = __reduce_max_sync(~0u, lane * HALVES / 32 == h ? m : 0u);
+                if (lane == run % 32) mine[run / 32] = r;
+            }
         }
-    float inv, scale;
-    pack8_factors(__uint_as_float(mine), inv, scale);
-    const int64_t row0 = t.b * g.L + t.t0 + w * kStep, runs = g.cgs;
-    const int64_t left = g.L - t.t0 - w * kStep;
-    if (lane < NIN * kStep && lane % kStep < left) {
-        float* to = lane < kStep ? g.x8.scale : lane < 2 * kStep ? g.f8.scale : g.i8.scale;
-        to[(row0 + lane % kStep) * runs + t.d0 / kCh] = scale;
+    float inv[SETS];
+    const int64_t row0 = t.row + w * kStep, runs = (g.D + 63) / 64;
+    const int left = t.tokens - w * kStep;
+#pragma unroll
+    for (int k = 0; k < SETS; ++k) {
+        float scale;
+        pack8_factors(__uint_as_float(mine[k]), inv[k], scale);
+        const int run = 32 * k + lane, h = run % HALVES, s = run / HALVES % kStep, n = run / HALVES / kStep;
+        if (n < NIN && s < left && h * 64 < t.channels) {
+            float* to = n == 0 ? g.x8.scale : n == 1 ? g.f8.scale : g.i8.scale;
+            to[(row0 + s) * runs + t.d0 / 64 + h] = scale;
+        }
     }
-    const int64_t d = t.d0 + 2 * lane;
+    const int channels = t.channels - C * lane;
 #pragma unroll
     for (int n = 0; n < NIN; ++n) {
-        int8_t* to = n == 0 ? g.x8.q : n == 1 ? g.f8.q : g.i8.q;
+        int8_t* at = (n == 0 ? g.x8.q : n == 1 ? g.f8.q : g.i8.q) + row0 * g.D + t.d0 + C * lane;
 #pragma unroll
-        for (int s = 0; s < kStep; ++s) {
-            const float k = __shfl_sync(~0u, inv, n * kStep + s);
+        for (int s = 0; s < kStep; ++s, at += g.D) {
+            const int run = (n * kStep + s) * HALVES;
+            float k = __shfl_sync(~0u, inv[run / 32], run % 32);
+            if (HALVES == 2) {
+                const float k1 = __shfl_sync(~0u, inv[run / 32], run % 32 + 1);
+                if (lane >= 16) k = k1;
+            }
             if (s >= left) continue;
-            const float2 v = pair_at(stage + (n * kTok + w * kStep + s) * kCh + 2 * lane);
-            const int q0 = pack8_q(v.x, k), q1 = pack8_q(v.y, k);
-            int8_t* at = to + (row0 + s) * g.D + d;
+            const Vec<C> v = read_row<C>(stage + (n * kTok + w * kStep + s) * kCh + C * lane);
+            uint32_t q = 0;
+#pragma unroll
+            for (int c = 0; c < C; ++c) q |= (uint32_t)pack8_q(v.v[c], k) << (8 * c);
             if (wide8) {
-                if (d < g.D) *reinterpret_cast<char2*>(at) = make_char2((char)q0, (char)q1);
+                if (channels > 0) {
+                    if constexpr (C == 4) *reinterpret_cast<uint32_t*>(at) = q;
+                    else *reinterpret_cast<uint16_t*>(at) = (uint16_t)q;
+                }
             } else {
-                if (d < g.D) at[0] = (int8_t)q0;
-                if (d + 1 < g.D) at[1] = (int8_t)q1;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (c < channels) at[c] = (int8_t)(q >> (8 * c));
             }
         }
     }
@@ -214,72 +242,67 @@ __device__ __forceinline__ void pack_rows(const Args& g, const Tile& t, int w, i
 
 // The decays and inputs of a warp's tokens and their map.  SPECIAL: padding
 // (nothing happens) or resets (the state before counts as zero).
-template <typename T, int GATE, bool SPECIAL, bool NEAR>
-__device__ __forceinline__ float4 local_map(const T* stage, int w, int lane, float2 csp, int n, uint32_t resets,
-                                            float2 (&a)[kStep], float2 (&b)[kStep])
+template <typename T, int C, int GATE, bool SPECIAL, bool NEAR>
+__device__ __forceinline__ Map<C> local_map(const T* at, const Vec<C>& csp, int n, uint32_t resets,
+                                            Vec<C> (&a)[kStep], Vec<C> (&b)[kStep])
 {
-    float4 m = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+    constexpr int kCh = 32 * C, kIn = kTok * kCh;
+    Map<C> m = Map<C>::of(1.0f);
 #pragma unroll
     for (int s = 0; s < kStep; ++s) {
-        const T* at = stage + (w * kStep + s) * kCh + 2 * lane;
         if (SPECIAL && s >= n) {
-            a[s] = make_float2(1.0f, 1.0f);
-            b[s] = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                a[s].v[c] = 1.0f;
+                b[s].v[c] = 0.0f;
+            }
             continue;
         }
-        const float2 x = pair_at(at), f = pair_at(at + kTok * kCh);
-        const float2 i = GATE == MRU_GATE_LRU ? pair_at(at + 2 * kTok * kCh) : make_float2(0.0f, 0.0f);
-        gates<GATE, NEAR>(x.x, f.x, i.x, csp.x, a[s].x, b[s].x);
-        gates<GATE, NEAR>(x.y, f.y, i.y, csp.y, a[s].y, b[s].y);
-        if (SPECIAL && (resets >> s & 1)) m = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        m.x *= a[s].x;
-        m.z *= a[s].y;
-        if (GATE == MRU_GATE_DECAY) {
-            m.y = carry_in(a[s].x, m.y) + b[s].x;
-            m.w = carry_in(a[s].y, m.w) + b[s].y;
-        } else {
-            m.y = fmaf(a[s].x, m.y, b[s].x);
-            m.w = fmaf(a[s].y, m.w, b[s].y);
+        const Vec<C> x = read_row<C>(at + s * kCh), f = read_row<C>(at + kIn + s * kCh);
+        Vec<C> i = x;
+        if (GATE == MRU_GATE_LRU) i = read_row<C>(at + 2 * kIn + s * kCh);
+        if (SPECIAL && (resets >> s & 1)) m = Map<C>::of(0.0f);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            gates<GATE, NEAR>(x.v[c], f.v[c], i.v[c], csp.v[c], a[s].v[c], b[s].v[c]);
+            m.P[c] *= a[s].v[c];
+            m.H[c] = GATE == MRU_GATE_DECAY ? carry_in(a[s].v[c], m.H[c]) + b[s].v[c]
+                                            : fmaf(a[s].v[c], m.H[c], b[s].v[c]);
         }
     }
     return m;
 }
 
-template <typename T, int GATE, bool SPECIAL>
-__device__ __forceinline__ void run_states(const Args& g, const Tile& t, int w, int lane, float2 h, int n,
-                                           uint32_t resets, const float2 (&a)[kStep], const float2 (&b)[kStep],
-                                           bool wide)
+template <typename T, int C, int GATE, bool SPECIAL>
+__device__ __forceinline__ void run_states(T* y, int64_t D, int left, Vec<C> h, int n, uint32_t resets,
+                                           const Vec<C> (&a)[kStep], const Vec<C> (&b)[kStep], const Put& put)
 {
-    const int64_t d = t.d0 + 2 * lane, left = g.L - t.t0 - w * kStep;
-    T* y = (T*)g.y + (t.b * g.L + t.t0 + w * kStep) * g.D + d;
-    const bool one = d < g.D, two = d + 1 < g.D;
 #pragma unroll
-    for (int s = 0; s < kStep; ++s) {
-        if (SPECIAL && (resets >> s & 1)) h = make_float2(0.0f, 0.0f);
-        if (GATE == MRU_GATE_DECAY) {
-            h.x = carry_in(a[s].x, h.x) + b[s].x;
-            h.y = carry_in(a[s].y, h.y) + b[s].y;
-        } else {
-            h.x = fmaf(a[s].x, h.x, b[s].x);
-            h.y = fmaf(a[s].y, h.y, b[s].y);
-        }
-        const float2 out = SPECIAL && s >= n ? make_float2(0.0f, 0.0f) : h;
-        if (!SPECIAL || s < left) put_pair(y + s * g.D, out, wide && one, one, two);
+    for (int s = 0; s < kStep; ++s, y += D) {
+        if (SPECIAL && (resets >> s & 1)) h = Vec<C>{};
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            h.v[c] = GATE == MRU_GATE_DECAY ? carry_in(a[s].v[c], h.v[c]) + b[s].v[c]
+                                            : fmaf(a[s].v[c], h.v[c], b[s].v[c]);
+        Vec<C> out = h;
+        if (SPECIAL && s >= n) out = Vec<C>{};
+        if (!SPECIAL || s < left) write_row<C>(y, out, put);
     }
 }
 
-template <typename T, int GATE>
+template <typename T, int C, int GATE>
 constexpr size_t forward_stage_bytes()
 {
-    return (size_t)inputs_of(GATE) * kTok * kCh * sizeof(T);
+    return (size_t)inputs_of(GATE) * kTok * 32 * C * sizeof(T);
 }
 
-template <typename T, int GATE, bool VEC>
+template <typename T, int C, int GATE, bool VEC>
 __device__ __forceinline__ void load_inputs(const Args& g, const Tile& t, T* to)
 {
-    load_tile<T, VEC>(g, t, g.x, g.ld, to);
-    load_tile<T, VEC>(g, t, g.f, g.ld, to + kTok * kCh);
-    if (GATE == MRU_GATE_LRU) load_tile<T, VEC>(g, t, g.i, g.ld, to + 2 * kTok * kCh);
+    constexpr int kIn = kTok * 32 * C;
+    load_tile<T, C, VEC>(t, g.x, g.ld, to);
+    load_tile<T, C, VEC>(t, g.f, g.ld, to + kIn);
+    if (GATE == MRU_GATE_LRU) load_tile<T, C, VEC>(t, g.i, g.ld, to + 2 * kIn);
 }
 
 // Forward: every input is read once and every output written once.  Blocks
@@ -288,190 +311,203 @@ __device__ __forceinline__ void load_inputs(const Args& g, const Tile& t, T* to)
 // the maps meet in shared memory, the tile's map is published, the carry is
 // fetched (by then the tiles before have published theirs), and the states
 // are run again from it over decays and inputs that stayed in registers.
-template <typename T, int GATE, bool VEC, bool PACK>
-__global__ void __launch_bounds__(kThreads, 3) k_gated_tile(Args g)
+template <typename T, int C, int GATE, bool VEC, bool PACK>
+__global__ void __launch_bounds__(kThreads, C == 4 ? 2 : 3) k_gated_tile(Args g)
 {
     extern __shared__ __align__(16) unsigned char stages[];
-    __shared__ TileMem mem;
-    constexpr int NIN = inputs_of(GATE), kElems = NIN * kTok * kCh;
+    __shared__ TileMem<C> mem;
+    constexpr int NIN = inputs_of(GATE), kCh = 32 * C, kElems = NIN * kTok * kCh;
+    constexpr bool lru = GATE == MRU_GATE_LRU;
     T* stage = reinterpret_cast<T*>(stages);
     const int tid = threadIdx.x, lane = tid & 31, w = tid / 32;
-    const bool wide = g.D % 2 == 0 && aligned(g.y, 2 * sizeof(T));
-    const bool wide8 = PACK && g.D % 2 == 0 && aligned(g.x8.q, 2) && aligned(g.f8.q, 2) &&
-                       (GATE != MRU_GATE_LRU || aligned(g.i8.q, 2));
+    const bool whole = g.D % C == 0 && aligned(g.y, C * sizeof(T));
+    const bool wide8 = PACK && g.D % C == 0 && aligned(g.x8.q, C) && aligned(g.f8.q, C) && (!lru || aligned(g.i8.q, C));
     if (tid == 0) {
         const uint32_t first = g.ticket ? atomicAdd(g.ticket, 1u) : blockIdx.x;
-        mem.next[0] = first;
-        mem.next[1] = draw(g, first);
+        find_tile<C, false>(g, first, mem.tile[0]);
+        find_tile<C, false>(g, draw(g, first), mem.tile[1]);
         if (!g.ticket && blockIdx.x == 0) *g.status = 0;
     }
     __syncthreads();
-    uint32_t cur = mem.next[0], nxt = mem.next[1];
-    if (cur < g.tiles) {
-        const Tile t = tile_of<false>(g, cur);
-        load_inputs<T, GATE, VEC>(g, t, stage);
-        if (GATE == MRU_GATE_LRU && tid < kCh)
-            mem.csp[0][tid] = t.d0 + tid < g.D ? g.c * softplus(g.lam[t.d0 + tid]) : 0.0f;
+    if (mem.tile[0].ticket < g.tiles) {
+        const Tile& t = mem.tile[0];
+        load_inputs<T, C, GATE, VEC>(g, t, stage);
+        if (lru && tid < kCh) mem.csp[tid] = tid < t.channels ? g.c * softplus(g.lam[t.d0 + tid]) : 0.0f;
     }
     cp_commit();
-    for (int st = 0; cur < g.tiles; st ^= 1) {
+    for (int st = 0, now = 0; mem.tile[now].ticket < g.tiles; st ^= 1) {
+        const int then = now == 2 ? 0 : now + 1, later = then == 2 ? 0 : then + 1;
+        const Tile& t = mem.tile[now];
         uint32_t drawn = 0;
-        if (tid == 0) drawn = draw(g, nxt);
         float lam = 0.0f;
-        if (nxt < g.tiles) {
-            const Tile t = tile_of<false>(g, nxt);
-            load_inputs<T, GATE, VEC>(g, t, stage + (st ^ 1) * kElems);
-            if (GATE == MRU_GATE_LRU && tid < kCh && t.d0 + tid < g.D) lam = g.lam[t.d0 + tid];
+        if (tid == 0) drawn = draw(g, mem.tile[then].ticket);
+        if (mem.tile[then].ticket < g.tiles) {
+            const Tile& u = mem.tile[then];
+            load_inputs<T, C, GATE, VEC>(g, u, stage + (st ^ 1) * kElems);
+            if (lru && tid < u.channels) lam = g.lam[u.d0 + tid];
         }
         cp_commit();
-        const Tile t = tile_of<false>(g, cur);
         int n;
         uint32_t resets;
         warp_masks(g, t, w, lane, n, resets);
         cp_wait<1>();
         __syncthreads();
         const T* in = stage + st * kElems;
-        if constexpr (PACK) pack_rows<T, NIN>(g, t, w, lane, in, wide8);
-        float2 csp = make_float2(0.0f, 0.0f);
-        if (GATE == MRU_GATE_LRU) csp = *reinterpret_cast<const float2*>(&mem.csp[st][2 * lane]);
-        const bool near = GATE == MRU_GATE_LRU && __all_sync(~0u, csp.x <= 0.5f && csp.y <= 0.5f);
+        if constexpr (PACK) pack_rows<T, C, NIN>(g, t, w, lane, in, wide8);
+        Vec<C> csp = {};
+        if (lru) csp = csp_of<C>(mem.csp, lane);
         const bool special = n < kStep || resets;
-        float2 a[kStep], b[kStep];
-        float4 own;
-        if (special) own = local_map<T, GATE, true, false>(in, w, lane, csp, n, resets, a, b);
-        else if (near) own = local_map<T, GATE, false, GATE == MRU_GATE_LRU>(in, w, lane, csp, n, resets, a, b);
-        else own = local_map<T, GATE, false, false>(in, w, lane, csp, n, resets, a, b);
-        mem.agg[w][lane] = own;
+        Vec<C> a[kStep], b[kStep];
+        const T* rows = in + w * kStep * kCh + C * lane;
+        Map<C> own;
+        if (special) own = local_map<T, C, GATE, true, false>(rows, csp, n, resets, a, b);
+        else if (lru && all_near<C>(csp)) own = local_map<T, C, GATE, false, lru>(rows, csp, n, resets, a, b);
+        else own = local_map<T, C, GATE, false, false>(rows, csp, n, resets, a, b);
+        mem.agg[w].put(lane, own);
         __syncthreads();
-        float4 pre = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-        for (int v = 0; v < w; ++v) pre = after(mem.agg[v][lane], pre);
+        Map<C> pre = Map<C>::of(1.0f);
+        for (int v = 0; v < w; ++v) pre = mem.agg[v].get(lane).after(pre);
         if (w == kWarps - 1) {
-            own = after(own, pre);                         // the tile's map
-            if (!t.last && !(g.withhold && cur == 0)) publish(tile_words(g, t, t.order), lane, own);
+            own = own.after(pre);                          // the tile's map
+            if (!t.last && !(g.withhold && t.ticket == 0)) publish<C>(tile_words<C>(g, t, t.order), lane, own);
         }
-        fetch_carry(g, t, w, lane, g.h0, mem.ent);
-        if (tid == 0) mem.next[0] = drawn;
+        mem.ent.fetch(g, t, w, lane, g.h0);
+        if (tid == 0) find_tile<C, false>(g, drawn, mem.tile[later]);
         __syncthreads();
-        const float2 carry = carry_of(t, lane, mem.ent);
-        const int64_t d = t.d0 + 2 * lane;
+        const Vec<C> carry = mem.ent.carry(t, lane);
+        const int channels = t.channels - C * lane;
         if (w == kWarps - 1) {
-            publish_up(g, t, lane, own, carry, mem.ent);
-            if (t.last && g.h_last) {
-                const float2 h = apply(own, carry);
-                if (d < g.D) g.h_last[t.b * g.D + d] = h.x;
-                if (d + 1 < g.D) g.h_last[t.b * g.D + d + 1] = h.y;
-            }
+            mem.ent.publish_up(g, t, lane, own, carry);
+            if (t.last && g.h_last) write_state<C>(g.h_last + t.b * g.D + t.d0 + C * lane, own(carry), channels);
         }
-        if (w == 0 && g.states) {
-            float* to = g.states + (t.b * g.K + t.order) * g.D + d;
-            if (d < g.D) to[0] = carry.x;
-            if (d + 1 < g.D) to[1] = carry.y;
-        }
-        const float2 h = apply(pre, carry);
-        if (special) run_states<T, GATE, true>(g, t, w, lane, h, n, resets, a, b, wide);
-        else run_states<T, GATE, false>(g, t, w, lane, h, n, resets, a, b, wide);
-        if (GATE == MRU_GATE_LRU && tid < kCh) mem.csp[st ^ 1][tid] = g.c * softplus(lam);
-        cur = nxt;
-        nxt = mem.next[0];
+        if (w == 0 && g.states) write_state<C>(g.states + t.k * g.D + t.d0 + C * lane, carry, channels);
+        T* y = (T*)g.y + (t.row + w * kStep) * g.D + t.d0 + C * lane;
+        const Put put = {whole && channels > 0, channels};
+        const int left = t.tokens - w * kStep;
+        if (special) run_states<T, C, GATE, true>(y, g.D, left, pre(carry), n, resets, a, b, put);
+        else run_states<T, C, GATE, false>(y, g.D, left, pre(carry), n, resets, a, b, put);
+        if (lru && tid < kCh) mem.csp[tid] = g.c * softplus(lam);
+        now = then;
     }
 }
 
-// Shared memory of the backward beside its stages.
+// --------------------------------------------------------------- backward ---
+
+template <int C>
 struct BackMem {
-    float4 agg[kWarps][32];              // a warp's map of states
-    float4 back[kWarps][32];             // and of gradients
-    float4 ent[2 * kFan][32];
-    float2 dlam[kWarps][32];
-    float csp[2][kCh];
-    float state[2][kCh];                 // the kept state before the tile
+    MapRow<C> agg[kWarps];               // the warps' maps of states
+    MapRow<C> back[kWarps];              // and of gradients
+    Entries<C> ent;
+    float dlam[kWarps][32 * C];
+    float csp[32 * C];
+    float state[2][32 * C];              // the kept state before the tile
     float scale[2][3][kTok];             // 8-bit copies: the scale of a token's run
-    uint32_t next[2];
+    Tile tile[3];
 };
 
-template <typename T, int GATE, bool PACKED>
+template <typename T, int C, int GATE, bool PACKED>
 constexpr size_t backward_stage_bytes()
 {
-    return (size_t)kTok * kCh * (inputs_of(GATE) * (PACKED ? 1 : sizeof(T)) + sizeof(T));
+    return (size_t)kTok * 32 * C * (inputs_of(GATE) * (PACKED ? 1 : sizeof(T)) + sizeof(T));
 }
-// Two stages where three blocks of them fit an SM's 227 KB, else one.
-template <typename T, int GATE, bool PACKED>
+// Two stages where two blocks of them fit an SM's 227 KB, else one.
+template <typename T, int C, int GATE, bool PACKED>
 constexpr int backward_stages()
 {
-    return backward_stage_bytes<T, GATE, PACKED>() <= 36 * 1024 ? 2 : 1;
+    return backward_stage_bytes<T, C, GATE, PACKED>() <= 48 * 1024 ? 2 : 1;
 }
 
-template <typename T, int GATE, bool VEC, bool PACKED>
-__device__ __forceinline__ void load_back(const Args& g, const Tile& t, unsigned char* stage, BackMem& mem, int st)
+template <typename T, int C, int GATE, bool VEC, bool PACKED>
+__device__ __forceinline__ void load_back(const Args& g, const Tile& t, unsigned char* stage, BackMem<C>& mem, int st)
 {
-    constexpr int NIN = inputs_of(GATE);
+    static_assert(!PACKED || C == 2, "a tile's row is one run of 64 channels");
+    constexpr int NIN = inputs_of(GATE), kCh = 32 * C;
     T* dy = reinterpret_cast<T*>(stage);
-    load_tile<T, VEC>(g, t, g.dy, g.D, dy);
+    load_tile<T, C, VEC>(t, g.dy, g.D, dy);
     const int tid = threadIdx.x;
     if constexpr (PACKED) {
         int8_t* q = reinterpret_cast<int8_t*>(dy + kTok * kCh);
+        const int64_t runs = g.cgs;
 #pragma unroll
         for (int n = 0; n < NIN; ++n) {
             const mru_packed8& h = n == 0 ? g.x8 : n == 1 ? g.f8 : g.i8;
-            const int8_t* src = h.q + t.b * g.L * g.D;
+            const int8_t* src = h.q + t.row * g.D + t.d0;
             if constexpr (VEC) {
-                const int row = tid / 4, c = tid % 4 * 16;
-                const bool in = t.t0 + row < g.L && t.d0 + c < g.D;
-                cp_async(q + n * kTok * kCh + row * kCh + c, in ? src + (t.t0 + row) * g.D + t.d0 + c : src, in ? 16 : 0);
+                constexpr int chunks = kCh / 16;
+                for (int k = tid; k < kTok * chunks; k += kThreads) {
+                    const int row = k / chunks, c = k % chunks * 16;
+                    const bool in = row < t.tokens && c < t.channels;
+                    cp_async(q + (n * kTok + row) * kCh + c, in ? src + row * g.D + c : h.q, in ? 16 : 0);
+                }
             } else {
                 for (int k = tid; k < kTok * kCh; k += kThreads) {
                     const int row = k / kCh, c = k % kCh;
-                    const bool in = t.t0 + row < g.L && t.d0 + c < g.D;
-                    q[n * kTok * kCh + k] = in ? src[(t.t0 + row) * g.D + t.d0 + c] : (int8_t)0;
+                    q[n * kTok * kCh + k] = row < t.tokens && c < t.channels ? src[row * g.D + c] : (int8_t)0;
                 }
             }
             if (tid < kTok) {
-                const bool in = t.t0 + tid < g.L;
-                const float* at = h.scale + (in ? (t.b * g.L + t.t0 + tid) * (int64_t)g.cgs + t.d0 / kCh : 0);
-                cp_async4(&mem.scale[st][n][tid], at, in ? 4 : 0);
+                const bool in = tid < t.tokens;
+                cp_async4(&mem.scale[st][n][tid], in ? h.scale + (t.row + tid) * runs + t.d0 / 64 : h.scale, in ? 4 : 0);
             }
         }
     } else {
-        load_inputs<T, GATE, VEC>(g, t, dy + kTok * kCh);
+        load_inputs<T, C, GATE, VEC>(g, t, dy + kTok * kCh);
     }
     if (tid < kCh) {
-        const bool in = t.d0 + tid < g.D;
-        const float* at = g.states + (in ? (t.b * g.K + t.t0 / kTok) * g.D + t.d0 + tid : 0);
-        cp_async4(&mem.state[st][tid], at, in ? 4 : 0);
+        const bool in = tid < t.channels;
+        cp_async4(&mem.state[st][tid], in ? g.states + t.k * g.D + t.d0 + tid : g.states, in ? 4 : 0);
     }
 }
 
-// Two channels of a token's input n, from the stage.
-template <typename T, bool PACKED>
-__device__ __forceinline__ float2 input_pair(const unsigned char* stage, const float (&scale)[3][kTok], int n, int row,
-                                             int lane)
+// A lane's channels of a token's input n, from the stage.
+template <typename T, int C, bool PACKED>
+__device__ __forceinline__ Vec<C> input_row(const unsigned char* stage, const float (&scale)[3][kTok], int n, int row,
+                                            int lane)
 {
+    constexpr int kCh = 32 * C;
     const unsigned char* in = stage + kTok * kCh * sizeof(T);
     if constexpr (PACKED) {
-        const char2 q = *reinterpret_cast<const char2*>(in + (n * kTok + row) * kCh + 2 * lane);
+        const char2 q = *reinterpret_cast<const char2*>(in + (n * kTok + row) * kCh + C * lane);
         const float k = scale[n][row];
-        return make_float2((float)(signed char)q.x * k, (float)(signed char)q.y * k);
+        return Vec<C>{(float)(signed char)q.x * k, (float)(signed char)q.y * k};
     } else {
-        return pair_at(reinterpret_cast<const T*>(in) + (n * kTok + row) * kCh + 2 * lane);
+        return read_row<C>(reinterpret_cast<const T*>(in) + (n * kTok + row) * kCh + C * lane);
     }
 }
 
-template <typename T, int GATE, bool PACKED, bool NEAR>
-__device__ __forceinline__ float4 back_map(const unsigned char* stage, const float (&scale)[3][kTok], int w, int lane,
-                                           float2 csp, int n, uint32_t resets)
+// The map of a warp's tokens; a and, for the sigmoid gate, cx = 1 - a stay.
+template <typename T, int C, int GATE, bool PACKED, bool NEAR>
+__device__ __forceinline__ Map<C> back_map(const unsigned char* stage, const float (&scale)[3][kTok], int w, int lane,
+                                           const Vec<C>& csp, int n, uint32_t resets, Vec<C> (&a)[kStep],
+                                           Vec<C> (&cx)[kStep])
 {
-    float4 m = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+    Map<C> m = Map<C>::of(1.0f);
 #pragma unroll
     for (int s = 0; s < kStep; ++s) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            a[s].v[c] = 1.0f;
+            cx[s].v[c] = 0.0f;
+        }
         if (s >= n) continue;
         const int row = w * kStep + s;
-        const float2 x = input_pair<T, PACKED>(stage, scale, 0, row, lane);
-        const float2 f = input_pair<T, PACKED>(stage, scale, 1, row, lane);
-        const float2 i = GATE == MRU_GATE_LRU ? input_pair<T, PACKED>(stage, scale, 2, row, lane) : make_float2(0.0f, 0.0f);
-        float2 a, b;
-        gates<GATE, NEAR>(x.x, f.x, i.x, csp.x, a.x, b.x);
-        gates<GATE, NEAR>(x.y, f.y, i.y, csp.y, a.y, b.y);
-        if (resets >> s & 1) m = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        m = make_float4(m.x * a.x, carry_in(a.x, m.y) + b.x, m.z * a.y, carry_in(a.y, m.w) + b.y);
+        const Vec<C> x = input_row<T, C, PACKED>(stage, scale, 0, row, lane);
+        const Vec<C> f = input_row<T, C, PACKED>(stage, scale, 1, row, lane);
+        Vec<C> i = x;
+        if (GATE == MRU_GATE_LRU) i = input_row<T, C, PACKED>(stage, scale, 2, row, lane);
+        if (resets >> s & 1) m = Map<C>::of(0.0f);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float b;
+            if (GATE == MRU_GATE_SIGMOID) {
+                sigmoid2(f.v[c], a[s].v[c], cx[s].v[c]);
+                b = cx[s].v[c] * x.v[c];
+            } else {
+                gates<GATE, NEAR>(x.v[c], f.v[c], i.v[c], csp.v[c], a[s].v[c], b);
+            }
+            m.P[c] *= a[s].v[c];
+            m.H[c] = carry_in(a[s].v[c], m.H[c]) + b;
+        }
     }
     return m;
 }
@@ -480,46 +516,61 @@ __device__ __forceinline__ float4 back_map(const unsigned char* stage, const flo
 // gradients e -> P e + E from the token after the last to before the first.
 // dl: sum q d and sum q dd/de (for lam) at e = 0, without the first token where
 // it is a piece's edge (k_gated_edge counts it).  h: the state after the last.
-template <typename T, int GATE, bool PACKED, bool NEAR>
-__device__ __forceinline__ float4 back_factors(const unsigned char* stage, const float (&scale)[3][kTok], int w,
-                                               int lane, float2 csp, float2& h, int n, uint32_t resets, bool edge,
-                                               float2 (&a)[kStep], float2 (&cx)[kStep], float2 (&cf)[kStep],
-                                               float2 (&ci)[kStep], float4& dl)
+template <typename T, int C, int GATE, bool PACKED, bool NEAR>
+__device__ __forceinline__ Map<C> back_factors(const unsigned char* stage, const float (&scale)[3][kTok], int w,
+                                               int lane, const Vec<C>& csp, Vec<C>& h, int n, uint32_t resets,
+                                               bool edge, Vec<C> (&a)[kStep], Vec<C> (&cx)[kStep],
+                                               Vec<C> (&cf)[kStep], Vec<C> (&ci)[kStep], Vec<C>& dl0, Vec<C>& dl1)
 {
-    float2 q[kStep];
+    constexpr int kCh = 32 * C;
+    Vec<C> q[kStep];
 #pragma unroll
     for (int s = 0; s < kStep; ++s) {
-        a[s] = make_float2(1.0f, 1.0f);
-        cx[s] = cf[s] = ci[s] = q[s] = make_float2(0.0f, 0.0f);
+        cf[s] = ci[s] = q[s] = Vec<C>{};
         if (s >= n) continue;
         const int row = w * kStep + s;
-        const float2 x = input_pair<T, PACKED>(stage, scale, 0, row, lane);
-        const float2 f = input_pair<T, PACKED>(stage, scale, 1, row, lane);
-        const float2 i = GATE == MRU_GATE_LRU ? input_pair<T, PACKED>(stage, scale, 2, row, lane) : make_float2(0.0f, 0.0f);
+        const Vec<C> x = input_row<T, C, PACKED>(stage, scale, 0, row, lane);
+        Vec<C> f = x, i = x;
+        if (GATE == MRU_GATE_LRU) {
+            f = input_row<T, C, PACKED>(stage, scale, 1, row, lane);
+            i = input_row<T, C, PACKED>(stage, scale, 2, row, lane);
+        }
         const bool reset = resets >> s & 1;
-        if (reset) h = make_float2(0.0f, 0.0f);
-        float2 b;
-        gradient_factors<GATE, NEAR>(x.x, f.x, i.x, csp.x, h.x, a[s].x, b.x, cx[s].x, cf[s].x, ci[s].x, q[s].x);
-        gradient_factors<GATE, NEAR>(x.y, f.y, i.y, csp.y, h.y, a[s].y, b.y, cx[s].y, cf[s].y, ci[s].y, q[s].y);
-        h.x = carry_in(a[s].x, h.x) + b.x;
-        h.y = carry_in(a[s].y, h.y) + b.y;
-        if (reset) a[s] = make_float2(0.0f, 0.0f);
+        if (reset) h = Vec<C>{};
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float b;
+            if (GATE == MRU_GATE_DECAY) {
+                b = x.v[c];
+                cf[s].v[c] = h.v[c];
+            } else if (GATE == MRU_GATE_SIGMOID) {
+                b = cx[s].v[c] * x.v[c];
+                cf[s].v[c] = a[s].v[c] * cx[s].v[c] * (h.v[c] - x.v[c]);
+            } else {
+                gradient_factors<GATE, NEAR>(x.v[c], f.v[c], i.v[c], csp.v[c], h.v[c], a[s].v[c], b, cx[s].v[c],
+                                             cf[s].v[c], ci[s].v[c], q[s].v[c]);
+            }
+            h.v[c] = carry_in(a[s].v[c], h.v[c]) + b;
+            if (reset) a[s].v[c] = 0.0f;
+        }
     }
-    if (PACKED && edge) q[0] = make_float2(0.0f, 0.0f);
-    float4 m = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-    dl = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (PACKED && edge) q[0] = Vec<C>{};
+    Map<C> m = Map<C>::of(1.0f);
+    dl0 = dl1 = Vec<C>{};
 #pragma unroll
     for (int s = kStep - 1; s >= 0; --s) {
         if (s >= n) continue;
-        const float2 dy = pair_at(reinterpret_cast<const T*>(stage) + (w * kStep + s) * kCh + 2 * lane);
-        const float2 d = make_float2(m.y + dy.x, m.w + dy.y);
-        if (GATE == MRU_GATE_LRU) {
-            dl.x = fmaf(q[s].x, d.x, dl.x);
-            dl.y = fmaf(q[s].x, m.x, dl.y);
-            dl.z = fmaf(q[s].y, d.y, dl.z);
-            dl.w = fmaf(q[s].y, m.z, dl.w);
+        const Vec<C> dy = read_row<C>(reinterpret_cast<const T*>(stage) + (w * kStep + s) * kCh + C * lane);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const float d = m.H[c] + dy.v[c];
+            if (GATE == MRU_GATE_LRU) {
+                dl0.v[c] = fmaf(q[s].v[c], d, dl0.v[c]);
+                dl1.v[c] = fmaf(q[s].v[c], m.P[c], dl1.v[c]);
+            }
+            m.P[c] *= a[s].v[c];
+            m.H[c] = carry_in(a[s].v[c], d);
         }
-        m = make_float4(m.x * a[s].x, carry_in(a[s].x, d.x), m.z * a[s].y, carry_in(a[s].y, d.y));
     }
     return m;
 }
@@ -527,42 +578,43 @@ __device__ __forceinline__ float4 back_factors(const unsigned char* stage, const
 // Backward, tiles from the last to the first: the states of the tile again
 // from its kept state, the factors of the gradients, then the gradient's own
 // recurrence with its carry from the later tiles, as the forward's.
-template <typename T, int GATE, bool VEC, bool PACKED>
+template <typename T, int C, int GATE, bool VEC, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 2) k_gated_tile_bwd(Args g)
 {
     extern __shared__ __align__(16) unsigned char stages[];
-    __shared__ BackMem mem;
-    constexpr size_t kBytes = backward_stage_bytes<T, GATE, PACKED>();
-    constexpr int STAGES = backward_stages<T, GATE, PACKED>();
+    __shared__ BackMem<C> mem;
+    constexpr int kCh = 32 * C;
+    constexpr size_t kBytes = backward_stage_bytes<T, C, GATE, PACKED>();
+    constexpr int STAGES = backward_stages<T, C, GATE, PACKED>();
     constexpr bool lru = GATE == MRU_GATE_LRU;
     const int tid = threadIdx.x, lane = tid & 31, w = tid / 32;
-    const bool wide = g.D % 2 == 0 && g.ldg % 2 == 0 && aligned(g.dx, 2 * sizeof(T)) && aligned(g.df, 2 * sizeof(T)) &&
-                      (!lru || aligned(g.di, 2 * sizeof(T)));
+    const bool whole = g.D % C == 0 && g.ldg % C == 0 && aligned(g.dx, C * sizeof(T)) && aligned(g.df, C * sizeof(T)) &&
+                       (!lru || aligned(g.di, C * sizeof(T)));
     if (tid == 0) {
         const uint32_t first = g.ticket ? atomicAdd(g.ticket, 1u) : blockIdx.x;
-        mem.next[0] = first;
-        mem.next[1] = draw(g, first);
+        find_tile<C, true>(g, first, mem.tile[0]);
+        find_tile<C, true>(g, draw(g, first), mem.tile[1]);
         if (!g.ticket && blockIdx.x == 0) *g.status = 0;
     }
     __syncthreads();
-    uint32_t cur = mem.next[0], nxt = mem.next[1];
-    if (cur < g.tiles) {
-        const Tile t = tile_of<true>(g, cur);
-        if (STAGES == 2) load_back<T, GATE, VEC, PACKED>(g, t, stages, mem, 0);
-        if (lru && tid < kCh) mem.csp[0][tid] = t.d0 + tid < g.D ? g.c * softplus(g.lam[t.d0 + tid]) : 0.0f;
+    if (mem.tile[0].ticket < g.tiles) {
+        const Tile& t = mem.tile[0];
+        if (STAGES == 2) load_back<T, C, GATE, VEC, PACKED>(g, t, stages, mem, 0);
+        if (lru && tid < kCh) mem.csp[tid] = tid < t.channels ? g.c * softplus(g.lam[t.d0 + tid]) : 0.0f;
     }
     cp_commit();
-    for (int st = 0; cur < g.tiles; st ^= 1) {
+    for (int st = 0, now = 0; mem.tile[now].ticket < g.tiles; st ^= 1) {
+        const int then = now == 2 ? 0 : now + 1, later = then == 2 ? 0 : then + 1;
+        const Tile& t = mem.tile[now];
         unsigned char* stage = stages + (STAGES == 2 ? st * kBytes : 0);
         uint32_t drawn = 0;
-        if (tid == 0) drawn = draw(g, nxt);
         float lam = 0.0f;
-        const Tile t = tile_of<true>(g, cur);
-        if (STAGES == 1) load_back<T, GATE, VEC, PACKED>(g, t, stage, mem, st);
-        if (nxt < g.tiles) {
-            const Tile u = tile_of<true>(g, nxt);
-            if (STAGES == 2) load_back<T, GATE, VEC, PACKED>(g, u, stages + (st ^ 1) * kBytes, mem, st ^ 1);
-            if (lru && tid < kCh && u.d0 + tid < g.D) lam = g.lam[u.d0 + tid];
+        if (tid == 0) drawn = draw(g, mem.tile[then].ticket);
+        if (STAGES == 1) load_back<T, C, GATE, VEC, PACKED>(g, t, stage, mem, st);
+        if (mem.tile[then].ticket < g.tiles) {
+            const Tile& u = mem.tile[then];
+            if (STAGES == 2) load_back<T, C, GATE, VEC, PACKED>(g, u, stages + (st ^ 1) * kBytes, mem, st ^ 1);
+            if (lru && tid < u.channels) lam = g.lam[u.d0 + tid];
         }
         cp_commit();
         int n;
@@ -570,79 +622,86 @@ __global__ void __launch_bounds__(kThreads, 2) k_gated_tile_bwd(Args g)
         warp_masks(g, t, w, lane, n, resets);
         cp_wait<STAGES - 1>();
         __syncthreads();
-        float2 csp = make_float2(0.0f, 0.0f);
-        if (lru) csp = *reinterpret_cast<const float2*>(&mem.csp[st][2 * lane]);
-        const bool near = lru && __all_sync(~0u, csp.x <= 0.5f && csp.y <= 0.5f);
-        mem.agg[w][lane] = near ? back_map<T, GATE, PACKED, lru>(stage, mem.scale[st], w, lane, csp, n, resets)
-                                : back_map<T, GATE, PACKED, false>(stage, mem.scale[st], w, lane, csp, n, resets);
+        Vec<C> csp = {};
+        if (lru) csp = csp_of<C>(mem.csp, lane);
+        const bool near = lru && all_near<C>(csp);
+        Vec<C> a[kStep], cx[kStep], cf[kStep], ci[kStep];
+        mem.agg[w].put(lane, near ? back_map<T, C, GATE, PACKED, lru>(stage, mem.scale[st], w, lane, csp, n, resets, a, cx)
+                                  : back_map<T, C, GATE, PACKED, false>(stage, mem.scale[st], w, lane, csp, n, resets, a,
+                                                                        cx));
         __syncthreads();
-        float2 h = *reinterpret_cast<const float2*>(&mem.state[st][2 * lane]);
-        for (int v = 0; v < w; ++v) h = apply(mem.agg[v][lane], h);
-        float2 a[kStep], cx[kStep], cf[kStep], ci[kStep];
-        float4 dl;
-        const bool edge = PACKED && w == 0 && t.t0 > 0;
-        float4 own = near ? back_factors<T, GATE, PACKED, lru>(stage, mem.scale[st], w, lane, csp, h, n, resets, edge,
-                                                               a, cx, cf, ci, dl)
-                          : back_factors<T, GATE, PACKED, false>(stage, mem.scale[st], w, lane, csp, h, n, resets, edge,
-                                                                 a, cx, cf, ci, dl);
-        mem.back[w][lane] = own;
+        Vec<C> h = read_row<C>(&mem.state[st][C * lane]), dl0, dl1;
+        for (int v = 0; v < w; ++v) h = mem.agg[v].get(lane)(h);
+        const bool edge = PACKED && w == 0 && t.k % g.K > 0;
+        Map<C> own = near ? back_factors<T, C, GATE, PACKED, lru>(stage, mem.scale[st], w, lane, csp, h, n, resets, edge,
+                                                                  a, cx, cf, ci, dl0, dl1)
+                          : back_factors<T, C, GATE, PACKED, false>(stage, mem.scale[st], w, lane, csp, h, n, resets,
+                                                                    edge, a, cx, cf, ci, dl0, dl1);
+        mem.back[w].put(lane, own);
         __syncthreads();
-        float4 post = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-        for (int v = kWarps - 1; v > w; --v) post = after(mem.back[v][lane], post);
+        Map<C> post = Map<C>::of(1.0f);
+        for (int v = kWarps - 1; v > w; --v) post = mem.back[v].get(lane).after(post);
         if (w == 0) {
-            own = after(own, post);                        // the tile's map
-            if (!t.last && !(g.withhold && cur == 0)) publish(tile_words(g, t, t.order), lane, own);
+            own = own.after(post);                         // the tile's map
+            if (!t.last && !(g.withhold && t.ticket == 0)) publish<C>(tile_words<C>(g, t, t.order), lane, own);
         }
-        fetch_carry(g, t, w, lane, g.dh_last, mem.ent);
-        if (tid == 0) mem.next[0] = drawn;
+        mem.ent.fetch(g, t, w, lane, g.dh_last);
+        if (tid == 0) find_tile<C, true>(g, drawn, mem.tile[later]);
         __syncthreads();
-        const float2 carry = carry_of(t, lane, mem.ent);
-        const int64_t d0 = t.d0 + 2 * lane;
-        const bool one = d0 < g.D, two = d0 + 1 < g.D;
+        const Vec<C> carry = mem.ent.carry(t, lane);
+        const int channels = t.channels - C * lane;
         if (w == 0) {
-            publish_up(g, t, lane, own, carry, mem.ent);
-            if (t.last && g.dh0) {
-                const float2 e = apply(own, carry);
-                if (one) g.dh0[t.b * g.D + d0] = e.x;
-                if (two) g.dh0[t.b * g.D + d0 + 1] = e.y;
-            }
+            mem.ent.publish_up(g, t, lane, own, carry);
+            if (t.last && g.dh0) write_state<C>(g.dh0 + t.b * g.D + t.d0 + C * lane, own(carry), channels);
         }
-        if (PACKED && g.edge_h && w == kWarps - 1 && t.order > 0) {
-            float* to = g.edge_h + (t.b * g.K + t.t0 / kTok + 1) * g.D + d0;
-            if (one) to[0] = h.x;
-            if (two) to[1] = h.y;
-        }
-        float2 e = apply(post, carry);
-        if (lru) mem.dlam[w][lane] = make_float2(fmaf(dl.y, e.x, dl.x), fmaf(dl.w, e.y, dl.z));
-        const int64_t at = (t.b * g.L + t.t0 + w * kStep) * g.ldg + d0, left = g.L - t.t0 - w * kStep;
+        if (PACKED && g.edge_h && w == kWarps - 1 && t.order > 0)
+            write_state<C>(g.edge_h + (t.k + 1) * g.D + t.d0 + C * lane, h, channels);
+        Vec<C> e = post(carry);
+        if (lru) {
 #pragma unroll
-        for (int s = kStep - 1; s >= 0; --s) {
+            for (int c = 0; c < C; ++c) mem.dlam[w][C * lane + c] = fmaf(dl1.v[c], e.v[c], dl0.v[c]);
+        }
+        const int left = t.tokens - w * kStep;
+        const Put put = {whole && channels > 0, channels};
+        int64_t at = (t.row + w * kStep + kStep - 1) * g.ldg + t.d0 + C * lane;
+#pragma unroll
+        for (int s = kStep - 1; s >= 0; --s, at -= g.ldg) {
             if (s >= left) continue;
-            float2 d = make_float2(0.0f, 0.0f);
+            Vec<C> d = {};
             if (s < n) {
-                const float2 dy = pair_at(reinterpret_cast<const T*>(stage) + (w * kStep + s) * kCh + 2 * lane);
-                d = make_float2(e.x + dy.x, e.y + dy.y);
-                e = make_float2(carry_in(a[s].x, d.x), carry_in(a[s].y, d.y));
+                d = read_row<C>(reinterpret_cast<const T*>(stage) + (w * kStep + s) * kCh + C * lane);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    d.v[c] += e.v[c];
+                    e.v[c] = carry_in(a[s].v[c], d.v[c]);
+                }
             }
-            if (s == 0 && edge) {
-                float* to = g.edge_d + (t.b * g.K + t.t0 / kTok) * g.D + d0;
-                if (one) to[0] = d.x;
-                if (two) to[1] = d.y;
+            if (PACKED && s == 0 && edge) write_state<C>(g.edge_d + t.k * g.D + t.d0 + C * lane, d, channels);
+            Vec<C> o;
+            if (GATE == MRU_GATE_DECAY) {
+                write_row<C>((T*)g.dx + at, d, put);
+            } else {
+#pragma unroll
+                for (int c = 0; c < C; ++c) o.v[c] = cx[s].v[c] * d.v[c];
+                write_row<C>((T*)g.dx + at, o, put);
             }
-            put_pair((T*)g.dx + at + s * g.ldg, make_float2(cx[s].x * d.x, cx[s].y * d.y), wide && one, one, two);
-            put_pair((T*)g.df + at + s * g.ldg, make_float2(cf[s].x * d.x, cf[s].y * d.y), wide && one, one, two);
-            if (lru)
-                put_pair((T*)g.di + at + s * g.ldg, make_float2(ci[s].x * d.x, ci[s].y * d.y), wide && one, one, two);
+#pragma unroll
+            for (int c = 0; c < C; ++c) o.v[c] = cf[s].v[c] * d.v[c];
+            write_row<C>((T*)g.df + at, o, put);
+            if (lru) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) o.v[c] = ci[s].v[c] * d.v[c];
+                write_row<C>((T*)g.di + at, o, put);
+            }
         }
-        if (lru && tid < kCh) mem.csp[st ^ 1][tid] = g.c * softplus(lam);
-        cur = nxt;
-        nxt = mem.next[0];
+        if (lru && tid < kCh) mem.csp[tid] = g.c * softplus(lam);
         __syncthreads();                                   // the stage may be filled again
-        if (lru && g.dlam_part && tid < kCh && t.d0 + tid < g.D) {
+        if (lru && g.dlam_part && tid < t.channels) {
             float s = 0.0f;
-            for (int v = 0; v < kWarps; ++v) s += reinterpret_cast<const float*>(mem.dlam[v])[tid];
-            g.dlam_part[(t.b * g.K + t.t0 / kTok) * g.D + t.d0 + tid] = s;
+            for (int v = 0; v < kWarps; ++v) s += mem.dlam[v][tid];
+            g.dlam_part[t.k * g.D + t.d0 + tid] = s;
         }
+        now = then;
     }
 }
 
@@ -753,6 +812,7 @@ struct Layout {
 constexpr size_t kControl = 256;
 Layout layout(const mru_gated_problem& p, bool backward)
 {
+    const int64_t kCh = 32 * (backward ? kBwdC : fwd_channels(elem_size(p.dtype)));
     Layout W;
     memset(&W, 0, sizeof W);
     const int64_t K = div_up(p.L, kKeep);
@@ -848,13 +908,14 @@ struct Forward {
             k_gated_short<T, GATE><<<(unsigned)div_up(g.B * g.D, 128), 128, 0, s>>>(g);
             return cudaGetLastError();
         }
-        constexpr size_t smem = 2 * forward_stage_bytes<T, GATE>();
+        constexpr int C = fwd_channels(sizeof(T));
+        constexpr size_t smem = 2 * forward_stage_bytes<T, C, GATE>();
         static Fits fits[4];
         if (vec)
-            return pack ? launch_tiles(k_gated_tile<T, GATE, true, true>, fits[0], g, smem, s)
-                        : launch_tiles(k_gated_tile<T, GATE, true, false>, fits[1], g, smem, s);
-        return pack ? launch_tiles(k_gated_tile<T, GATE, false, true>, fits[2], g, smem, s)
-                    : launch_tiles(k_gated_tile<T, GATE, false, false>, fits[3], g, smem, s);
+            return pack ? launch_tiles(k_gated_tile<T, C, GATE, true, true>, fits[0], g, smem, s)
+                        : launch_tiles(k_gated_tile<T, C, GATE, true, false>, fits[1], g, smem, s);
+        return pack ? launch_tiles(k_gated_tile<T, C, GATE, false, true>, fits[2], g, smem, s)
+                    : launch_tiles(k_gated_tile<T, C, GATE, false, false>, fits[3], g, smem, s);
     }
 };
 
@@ -869,10 +930,11 @@ struct Backward {
             k_gated_short_bwd<T, GATE, PACKED><<<(unsigned)div_up(g.B * g.D, 128), 128, 0, s>>>(g);
             return cudaGetLastError();
         }
-        constexpr size_t smem = backward_stages<T, GATE, PACKED>() * backward_stage_bytes<T, GATE, PACKED>();
+        constexpr int C = kBwdC;
+        constexpr size_t smem = backward_stages<T, C, GATE, PACKED>() * backward_stage_bytes<T, C, GATE, PACKED>();
         static Fits fits[2];
-        const cudaError_t e = vec ? launch_tiles(k_gated_tile_bwd<T, GATE, true, PACKED>, fits[0], g, smem, s)
-                                  : launch_tiles(k_gated_tile_bwd<T, GATE, false, PACKED>, fits[1], g, smem, s);
+        const cudaError_t e = vec ? launch_tiles(k_gated_tile_bwd<T, C, GATE, true, PACKED>, fits[0], g, smem, s)
+                                  : launch_tiles(k_gated_tile_bwd<T, C, GATE, false, PACKED>, fits[1], g, smem, s);
         if (e != cudaSuccess || !g.edge_h) return e;
         k_gated_edge<T, GATE><<<(unsigned)div_up(g.B * (g.K - 1) * g.D, 128), 128, 0, s>>>(g);
         return cudaGetLastError();

@@ -10,7 +10,6 @@ namespace gated {
 using namespace ops;
 
 constexpr int kTok = MRU_GATED_KEEP;     // tokens of a tile: a kept state per tile
-constexpr int kCh = 64;                  // channels of a tile: two to a lane
 constexpr int kWarps = 8;
 constexpr int kStep = kTok / kWarps;     // tokens of a warp
 constexpr int kThreads = 32 * kWarps;
@@ -39,7 +38,7 @@ struct Args {
     uint32_t* ticket;                    // next tile to draw
     uint32_t* abort;                     // a wait gave up
     uint64_t *a0, *a1, *c2;              // aggregates of tiles and of groups, carries into blocks
-    uint32_t tiles, cols, cgs;           // tiles in all; columns (64 channels of a sequence); those per sequence
+    uint32_t tiles, cols, cgs;           // tiles in all; columns (a tile's channels of a sequence); those per sequence
     uint32_t groups, blocks;             // groups and blocks per column
     uint64_t wait_ns;
     int32_t withhold;                    // testing: the first tile publishes nothing
@@ -67,24 +66,133 @@ __device__ __forceinline__ void gates(float x, float f, float i, float csp, floa
         sigmoid2(f, a, na);
         b = na * x;
     } else {
-        const float sf = __fdividef(1.0f, 1.0f + __expf(-f)), si = __fdividef(1.0f, 1.0f + __expf(-i));
-        float m, u;                                   // a - 1; sqrt(1 - a^2), 1 - a^2 = -m (1 + a)
-        exp_expm1_neg<NEAR>(-csp * sf, a, m);
-        asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(u) : "f"(-m * (1.0f + a)));
-        b = u * si * x;
+        float m;                                      // a - 1
+        exp_expm1_neg<NEAR>(-csp * sigmoid(f), a, m);
+        b = root(-m * (1.0f + a)) * sigmoid(i) * x;   // 1 - a^2 = -m (1 + a)
     }
+}
+
+// The states of a lane's C channels, and the map h -> P h + H of a run of
+// tokens on them.
+template <int C>
+struct Vec {
+    float v[C];
+};
+template <int C>
+struct Map {
+    float P[C], H[C];
+    __device__ __forceinline__ static Map of(float p)
+    {
+        Map m;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            m.P[c] = p;
+            m.H[c] = 0.0f;
+        }
+        return m;
+    }
+    // this one after `first`
+    __device__ __forceinline__ Map after(const Map& first) const
+    {
+        Map m;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            m.P[c] = P[c] * first.P[c];
+            m.H[c] = carry_in(P[c], first.H[c]) + H[c];
+        }
+        return m;
+    }
+    __device__ __forceinline__ Vec<C> operator()(const Vec<C>& h) const
+    {
+        Vec<C> r;
+#pragma unroll
+        for (int c = 0; c < C; ++c) r.v[c] = carry_in(P[c], h.v[c]) + H[c];
+        return r;
+    }
+};
+// A row of maps in shared memory, (P, H, P, H) of two channels to 16 bytes.
+template <int C>
+struct MapRow {
+    float4 q[C / 2][32];
+    __device__ __forceinline__ void put(int lane, const Map<C>& m)
+    {
+#pragma unroll
+        for (int k = 0; k < C / 2; ++k)
+            q[k][lane] = make_float4(m.P[2 * k], m.H[2 * k], m.P[2 * k + 1], m.H[2 * k + 1]);
+    }
+    __device__ __forceinline__ Map<C> get(int lane) const
+    {
+        Map<C> m;
+#pragma unroll
+        for (int k = 0; k < C / 2; ++k) {
+            const float4 v = q[k][lane];
+            m.P[2 * k] = v.x;
+            m.H[2 * k] = v.y;
+            m.P[2 * k + 1] = v.z;
+            m.H[2 * k + 1] = v.w;
+        }
+        return m;
+    }
+};
+
+// ------------------------------------------------------------------ tiles ---
+
+// Place of a tile, worked out by one thread for its block.  `order` counts
+// along the scan (from the last tile in the backward).
+struct Tile {
+    uint32_t ticket, col, order;
+    int32_t tokens, channels, valid;     // in the tile: tokens and channels there are, tokens that are not padding
+    int64_t row, b;                      // first token's row, sequence
+    int64_t d0, k;                       // first channel, index of its kept state
+    int32_t last;                        // nothing is carried out of it
+};
+
+template <int C, bool REVERSE>
+__device__ __forceinline__ void find_tile(const Args& g, uint32_t ticket, Tile& t)
+{
+    t.ticket = ticket;
+    if (ticket >= g.tiles) return;
+    const uint32_t order = ticket / g.cols, col = ticket - order * g.cols, b = col / g.cgs;
+    const int64_t t0 = (REVERSE ? g.K - 1 - (int64_t)order : (int64_t)order) * kTok;
+    const int64_t d0 = (int64_t)(col - b * g.cgs) * (32 * C), left = valid_tokens(g, b) - t0;
+    t.order = order;
+    t.col = col;
+    t.tokens = (int32_t)(g.L - t0 < kTok ? g.L - t0 : kTok);
+    t.channels = (int32_t)(g.D - d0 < 32 * C ? g.D - d0 : 32 * C);
+    t.valid = left <= 0 ? 0 : left < kTok ? (int32_t)left : kTok;
+    t.row = b * g.L + t0;
+    t.b = b;
+    t.d0 = d0;
+    t.k = b * g.K + t0 / kTok;
+    t.last = order + 1 == (uint32_t)g.K;
+}
+
+// Draws the next tile, in the order of the scan.  A tile waits only for tiles
+// drawn before it, and a block works through its tiles in the order drawn, so
+// the earliest unfinished tile never waits.
+__device__ __forceinline__ uint32_t draw(const Args& g, uint32_t before)
+{
+    return g.ticket ? atomicAdd(g.ticket, 1u) : before + gridDim.x;
+}
+
+// A warp's tokens that are not padding, and which of them start anew.
+__device__ __forceinline__ void warp_masks(const Args& g, const Tile& t, int w, int lane, int& n, uint32_t& resets)
+{
+    n = min(max(t.valid - w * kStep, 0), kStep);
+    resets = 0;
+    if (g.reset) resets = __ballot_sync(~0u, lane < n && g.reset[t.row + w * kStep + lane] != 0);
 }
 
 // ------------------------------------------------------------------ carry ---
 //
-// The map of a run of tokens is h -> P h + H.  Tiles publish theirs, the last
-// tile of 8 the composition of the group, and the last of 64 (a block) the
-// state itself, so that a tile's carry is one block carry and at most 7 groups
-// and 7 tiles, all in a fixed order: the same bits on every run, and a chain
-// of one hop per 64 tiles.  A pair (P, H) of a channel is one 64-bit word,
-// complemented so that zeroed memory reads as "not there yet" (no pair is all
-// ones: such a NaN is published as another NaN): word and flag arrive
-// together, which saves a fence before the flag and a round trip after it.
+// Tiles publish their maps, the last tile of 8 the composition of the group,
+// and the last of 64 (a block) the state itself, so that a tile's carry is one
+// block carry and at most 7 groups and 7 tiles, all in a fixed order: the same
+// bits on every run, and a chain of one hop per 64 tiles.  A pair (P, H) of a
+// channel is one 64-bit word, complemented so that zeroed memory reads as "not
+// there yet" (no pair is all ones: such a NaN is published as another NaN):
+// word and flag arrive together, which saves a fence before the flag and a
+// round trip after it.
 
 __device__ __forceinline__ uint64_t pair_word(float P, float H)
 {
@@ -93,12 +201,31 @@ __device__ __forceinline__ uint64_t pair_word(float P, float H)
     return ~(((uint64_t)p << 32) | __float_as_uint(H));
 }
 
-// Two channels of a lane: word 2 lane, 2 lane + 1 of the tile's 64.
-__device__ __forceinline__ void publish(uint64_t* at, int lane, float4 v)
+template <int C>
+__device__ __forceinline__ uint64_t* tile_words(const Args& g, const Tile& t, uint32_t order)
 {
-    asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(at + 2 * lane), "l"(pair_word(v.x, v.y)),
-                 "l"(pair_word(v.z, v.w))
-                 : "memory");
+    return g.a0 + ((uint64_t)t.col * (uint64_t)g.K + order) * (32 * C);
+}
+template <int C>
+__device__ __forceinline__ uint64_t* group_words(const Args& g, const Tile& t, uint32_t group)
+{
+    return g.a1 + ((uint64_t)t.col * g.groups + group) * (32 * C);
+}
+template <int C>
+__device__ __forceinline__ uint64_t* block_words(const Args& g, const Tile& t, uint32_t block)
+{
+    return g.c2 + ((uint64_t)t.col * g.blocks + block) * (32 * C);
+}
+
+// Words [2 k, lane, 2]: 16 bytes of a lane next to its neighbours'.
+template <int C>
+__device__ __forceinline__ void publish(uint64_t* at, int lane, const Map<C>& m)
+{
+#pragma unroll
+    for (int k = 0; k < C / 2; ++k)
+        asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(at + 64 * k + 2 * lane),
+                     "l"(pair_word(m.P[2 * k], m.H[2 * k])), "l"(pair_word(m.P[2 * k + 1], m.H[2 * k + 1]))
+                     : "memory");
 }
 
 __device__ __forceinline__ uint64_t now_ns()
@@ -108,13 +235,41 @@ __device__ __forceinline__ uint64_t now_ns()
     return t;
 }
 
-// Waits for a published pair of the lane's channels, for a limited time.
-__device__ __forceinline__ float4 await(const Args& g, const uint64_t* at, int lane)
+template <int C>
+__device__ __forceinline__ bool peek(const uint64_t* at, int lane, uint64_t (&u)[C])
 {
-    uint64_t u, v, t0 = 0;
+    bool there = true;
+#pragma unroll
+    for (int k = 0; k < C / 2; ++k)
+        asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];"
+                     : "=l"(u[2 * k]), "=l"(u[2 * k + 1])
+                     : "l"(at + 64 * k + 2 * lane)
+                     : "memory");
+#pragma unroll
+    for (int c = 0; c < C; ++c) there = there && u[c] != 0;
+    return there;
+}
+template <int C>
+__device__ __forceinline__ Map<C> map_of(const uint64_t (&u)[C])
+{
+    Map<C> m;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        m.P[c] = __uint_as_float((uint32_t)(~u[c] >> 32));
+        m.H[c] = __uint_as_float((uint32_t)~u[c]);
+    }
+    return m;
+}
+
+// Waits for two published maps (either may be absent: the identity), for a
+// limited time, and composes them, `one` first.
+template <int C>
+__device__ __forceinline__ Map<C> await(const Args& g, const uint64_t* one, const uint64_t* two, int lane)
+{
+    uint64_t u[C], v[C], t0 = 0;
     for (int n = 0;; ++n) {
-        asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(u), "=l"(v) : "l"(at + 2 * lane) : "memory");
-        if (__all_sync(~0u, u != 0 && v != 0)) break;
+        const bool a = !one || peek<C>(one, lane, u), b = !two || peek<C>(two, lane, v);
+        if (__all_sync(~0u, a && b)) break;
         if ((n & 63) == 63) {
             uint32_t stop;
             asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(stop) : "l"(g.abort) : "memory");
@@ -126,109 +281,82 @@ __device__ __forceinline__ float4 await(const Args& g, const uint64_t* at, int l
                 atomicExch(g.abort, 1u);
                 out = true;
             }
-            if (__any_sync(~0u, out || stop)) return make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+            if (__any_sync(~0u, out || stop)) return Map<C>::of(1.0f);
         }
     }
-    u = ~u;
-    v = ~v;
-    return make_float4(__uint_as_float((uint32_t)(u >> 32)), __uint_as_float((uint32_t)u),
-                       __uint_as_float((uint32_t)(v >> 32)), __uint_as_float((uint32_t)v));
+    if (!one) return Map<C>::of(1.0f);
+    const Map<C> first = map_of<C>(u);
+    return two ? map_of<C>(v).after(first) : first;
 }
 
-// The later map after the earlier one, two channels.
-__device__ __forceinline__ float4 after(float4 later, float4 first)
-{
-    return make_float4(later.x * first.x, carry_in(later.x, first.y) + later.y, later.z * first.z,
-                       carry_in(later.z, first.w) + later.w);
-}
-__device__ __forceinline__ float2 apply(float4 m, float2 h)
-{
-    return make_float2(carry_in(m.x, h.x) + m.y, carry_in(m.z, h.y) + m.w);
-}
+// What a tile's carry is made of, in shared memory: [0 .. 3] the block's carry
+// in and the block's groups before this one, [4 .. 7] the tiles before in the
+// group; two to an entry, so that [0] is the carry in and group 0, [1] groups 1
+// and 2, and so on.
+template <int C>
+struct Entries {
+    MapRow<C> e[8];
 
-// Place of a tile: `order` counts along the scan (from the last tile in the
-// backward).
-struct Tile {
-    uint32_t col, order;
-    int64_t b, d0, t0;
-    bool last;                           // nothing is carried out of it
+    // Warp w fetches entry w.  `start` is the state before the first tile (h0,
+    // or the last state's gradient).
+    __device__ __forceinline__ void fetch(const Args& g, const Tile& t, int w, int lane, const float* start)
+    {
+        const uint32_t block = t.order / (kFan * kFan), group = t.order / kFan % kFan, j = t.order % kFan;
+        if (w >= 4) {
+            const uint32_t k = 2 * (w - 4);
+            if (k < j) {
+                const uint64_t* at = tile_words<C>(g, t, t.order - j + k);
+                e[w].put(lane, await<C>(g, at, k + 1 < j ? at + 32 * C : nullptr, lane));
+            }
+        } else if (w == 0 && block == 0) {
+            Map<C> m = Map<C>::of(0.0f);
+            if (start) {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (C * lane + c < t.channels) m.H[c] = start[t.b * g.D + t.d0 + C * lane + c];
+            }
+            e[0].put(lane, group ? await<C>(g, group_words<C>(g, t, 0), nullptr, lane).after(m) : m);
+        } else if (2u * w <= group) {
+            const uint64_t* at = group_words<C>(g, t, block * kFan + 2 * w);
+            e[w].put(lane, await<C>(g, w ? at - 32 * C : block_words<C>(g, t, block), 2u * w < group ? at : nullptr, lane));
+        }
+    }
+    __device__ __forceinline__ Vec<C> carry(const Tile& t, int lane) const
+    {
+        const uint32_t group = t.order / kFan % kFan, j = t.order % kFan;
+        const Map<C> first = e[0].get(lane);
+        Vec<C> h;
+#pragma unroll
+        for (int c = 0; c < C; ++c) h.v[c] = first.H[c];
+        for (uint32_t k = 1; 2 * k <= group; ++k) h = e[k].get(lane)(h);
+        for (uint32_t k = 0; 2 * k < j; ++k) h = e[4 + k].get(lane)(h);
+        return h;
+    }
+    // After the carry is known: the group's map (last tile of a group) and the
+    // next block's carry (last tile of a block), by one warp.
+    __device__ __forceinline__ void publish_up(const Args& g, const Tile& t, int lane, const Map<C>& own,
+                                               const Vec<C>& carry) const
+    {
+        if (t.last || t.order % kFan != kFan - 1) return;
+        const uint32_t group = t.order / kFan;
+        Map<C> m;
+        if (group % kFan != kFan - 1) {
+            m = e[4].get(lane);
+            for (int k = 5; k < 8; ++k) m = e[k].get(lane).after(m);
+            publish<C>(group_words<C>(g, t, group), lane, own.after(m));
+        } else {
+            const Vec<C> h = own(carry);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                m.P[c] = 0.0f;
+                m.H[c] = h.v[c];
+            }
+            publish<C>(block_words<C>(g, t, group / kFan + 1), lane, m);
+        }
+    }
 };
-template <bool REVERSE>
-__device__ __forceinline__ Tile tile_of(const Args& g, uint32_t ticket)
-{
-    Tile t;
-    t.order = ticket / g.cols;
-    t.col = ticket - t.order * g.cols;
-    const uint32_t b = t.col / g.cgs;
-    t.b = b;
-    t.d0 = (int64_t)(t.col - b * g.cgs) * kCh;
-    t.t0 = (REVERSE ? g.K - 1 - (int64_t)t.order : (int64_t)t.order) * kTok;
-    t.last = t.order + 1 == (uint32_t)g.K;
-    return t;
-}
-__device__ __forceinline__ uint64_t* tile_words(const Args& g, const Tile& t, uint32_t order)
-{
-    return g.a0 + ((uint64_t)t.col * (uint64_t)g.K + order) * kCh;
-}
-__device__ __forceinline__ uint64_t* group_words(const Args& g, const Tile& t, uint32_t group)
-{
-    return g.a1 + ((uint64_t)t.col * g.groups + group) * kCh;
-}
-__device__ __forceinline__ uint64_t* block_words(const Args& g, const Tile& t, uint32_t block)
-{
-    return g.c2 + ((uint64_t)t.col * g.blocks + block) * kCh;
-}
 
-// Fetches what a tile's carry is made of into ent: [0] the block's carry in,
-// [1 .. 7] groups, [8 .. 14] tiles; warp w fetches w and 8 + w.  `start` is the
-// state before the first tile (h0, or the last state's gradient).
-__device__ __forceinline__ void fetch_carry(const Args& g, const Tile& t, int w, int lane, const float* start,
-                                            float4 (*ent)[32])
-{
-    const uint32_t block = t.order / (kFan * kFan), group = t.order / kFan % kFan, j = t.order % kFan;
-    if (w == 0) {
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (block) {
-            v = await(g, block_words(g, t, block), lane);
-        } else if (start) {
-            const int64_t d = t.d0 + 2 * lane;
-            if (d < g.D) v.y = start[t.b * g.D + d];
-            if (d + 1 < g.D) v.w = start[t.b * g.D + d + 1];
-        }
-        ent[0][lane] = v;
-    } else if ((uint32_t)w <= group) {
-        ent[w][lane] = await(g, group_words(g, t, block * kFan + w - 1), lane);
-    }
-    if ((uint32_t)w < j) ent[kFan + w][lane] = await(g, tile_words(g, t, t.order - j + w), lane);
-}
-
-__device__ __forceinline__ float2 carry_of(const Tile& t, int lane, const float4 (*ent)[32])
-{
-    const uint32_t group = t.order / kFan % kFan, j = t.order % kFan;
-    float2 h = make_float2(ent[0][lane].y, ent[0][lane].w);
-    for (uint32_t k = 1; k <= group; ++k) h = apply(ent[k][lane], h);
-    for (uint32_t k = 0; k < j; ++k) h = apply(ent[kFan + k][lane], h);
-    return h;
-}
-
-// After the carry is known: the group's map (last tile of a group) and the
-// next block's carry (last tile of a block), by one warp.
-__device__ __forceinline__ void publish_up(const Args& g, const Tile& t, int lane, float4 own, float2 carry,
-                                           const float4 (*ent)[32])
-{
-    if (t.last || t.order % kFan != kFan - 1) return;
-    const uint32_t group = t.order / kFan;
-    if (group % kFan != kFan - 1) {
-        float4 m = ent[kFan][lane];
-        for (int k = 1; k < kFan - 1; ++k) m = after(ent[kFan + k][lane], m);
-        publish(group_words(g, t, group), lane, after(own, m));
-    } else {
-        const float2 h = apply(own, carry);
-        publish(block_words(g, t, group / kFan + 1), lane, make_float4(0.0f, h.x, 0.0f, h.y));
-    }
-}
-
-// ------------------------------------------------------------------ loads ---
+// ------------------------------------------------------- loads and stores ---
 
 __device__ __forceinline__ void cp_async(void* smem, const void* gmem, int bytes16)
 {
@@ -247,54 +375,113 @@ __device__ __forceinline__ void cp_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A tile of one input into shared memory [64][64], zeros past the last token
+// A tile of one input into shared memory [64][32 C], zeros past the last token
 // or channel.  VEC: rows start on 16 bytes; else element by element.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_tile(const Args& g, const Tile& t, const void* from, int64_t ld, T* to)
+template <typename T, int C, bool VEC>
+__device__ __forceinline__ void load_tile(const Tile& t, const void* from, int64_t ld, T* to)
 {
-    const T* src = (const T*)from + t.b * g.L * ld;
+    constexpr int kCh = 32 * C;
+    const T* src = (const T*)from + t.row * ld + t.d0;
     if constexpr (VEC) {
-        constexpr int per = 16 / sizeof(T), chunks = kCh / per;
+        constexpr int per = 16 / sizeof(T), chunks = kCh / per, rows = kThreads / chunks;
+        const int row = threadIdx.x / chunks, c = threadIdx.x % chunks * per;
+        const T* at = src + row * ld + c;
+        T* put = to + row * kCh + c;
+        const int bytes = c >= t.channels ? 0 : t.channels - c >= per ? 16 : (t.channels - c) * (int)sizeof(T);
+        const int64_t jump = rows * ld;
 #pragma unroll
-        for (int k = threadIdx.x; k < kTok * chunks; k += kThreads) {
-            const int row = k / chunks, c = k % chunks * per;
-            const int64_t tok = t.t0 + row, left = g.D - t.d0 - c;
-            const bool in = tok < g.L && left > 0;
-            const int bytes = !in ? 0 : left >= per ? 16 : (int)left * (int)sizeof(T);
-            cp_async(to + row * kCh + c, in ? src + tok * ld + t.d0 + c : src, bytes);
+        for (int k = 0; k < kTok / rows; ++k) {
+            const bool in = row + k * rows < t.tokens && bytes > 0;
+            cp_async(put + k * rows * kCh, in ? at : src, in ? bytes : 0);
+            at += jump;
         }
     } else {
         for (int k = threadIdx.x; k < kTok * kCh; k += kThreads) {
             const int row = k / kCh, c = k % kCh;
-            const int64_t tok = t.t0 + row;
-            const bool in = tok < g.L && t.d0 + c < g.D;
-            const T* at = in ? src + tok * ld + t.d0 + c : src;
+            const bool in = row < t.tokens && c < t.channels;
+            const T* at = in ? src + row * ld + c : src;
             if constexpr (sizeof(T) == 4) cp_async4(to + k, at, in ? 4 : 0);
             else to[k] = in ? *at : from_f32<T>(0.0f);
         }
     }
 }
 
-__device__ __forceinline__ float2 pair_at(const float* p) { return *reinterpret_cast<const float2*>(p); }
-__device__ __forceinline__ float2 pair_at(const __nv_bfloat16* p)
+// C adjacent channels of a row.
+template <int C>
+__device__ __forceinline__ Vec<C> read_row(const float* p)
 {
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    Vec<C> r;
+    if constexpr (C == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        r.v[0] = v.x; r.v[1] = v.y; r.v[2] = v.z; r.v[3] = v.w;
+    } else {
+        const float2 v = *reinterpret_cast<const float2*>(p);
+        r.v[0] = v.x; r.v[1] = v.y;
+    }
+    return r;
+}
+template <int C>
+__device__ __forceinline__ Vec<C> read_row(const __nv_bfloat16* p)
+{
+    Vec<C> r;
+    uint32_t u[C / 2];
+    if constexpr (C == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        u[0] = v.x; u[1] = v.y;
+    } else {
+        u[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+#pragma unroll
+    for (int k = 0; k < C / 2; ++k) {
+        r.v[2 * k] = __uint_as_float(u[k] << 16);
+        r.v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    }
+    return r;
 }
 
-// Two adjacent channels of a row (d the first; `wide`: the pair is aligned and
-// both are there).
-__device__ __forceinline__ void put_pair(float* p, float2 v, bool wide, bool one, bool two)
+// Whether rows of C channels can be written in one piece, and how many
+// channels of the lane there are otherwise.
+struct Put {
+    bool whole;
+    int channels;
+};
+template <int C>
+__device__ __forceinline__ void write_row(float* p, const Vec<C>& r, const Put& put)
 {
-    if (wide) { *reinterpret_cast<float2*>(p) = v; return; }
-    if (one) p[0] = v.x;
-    if (two) p[1] = v.y;
+    if (put.whole) {
+        if constexpr (C == 4) *reinterpret_cast<float4*>(p) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+        else *reinterpret_cast<float2*>(p) = make_float2(r.v[0], r.v[1]);
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (c < put.channels) p[c] = r.v[c];
 }
-__device__ __forceinline__ void put_pair(__nv_bfloat16* p, float2 v, bool wide, bool one, bool two)
+template <int C>
+__device__ __forceinline__ void write_row(__nv_bfloat16* p, const Vec<C>& r, const Put& put)
 {
-    if (wide) { *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y); return; }
-    if (one) p[0] = __float2bfloat16_rn(v.x);
-    if (two) p[1] = __float2bfloat16_rn(v.y);
+    if (put.whole) {
+        uint32_t u[C / 2];
+#pragma unroll
+        for (int k = 0; k < C / 2; ++k) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(r.v[2 * k], r.v[2 * k + 1]);
+            u[k] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        if constexpr (C == 4) *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+        else *reinterpret_cast<uint32_t*>(p) = u[0];
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (c < put.channels) p[c] = __float2bfloat16_rn(r.v[c]);
+}
+// fp32 rows of one value per channel ([B, D] arrays).
+template <int C>
+__device__ __forceinline__ void write_state(float* p, const Vec<C>& r, int channels)
+{
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (c < channels) p[c] = r.v[c];
 }
 
 }  // namespace gated

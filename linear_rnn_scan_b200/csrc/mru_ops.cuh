@@ -78,6 +78,34 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// The hardware's 2^v, 1/v, v^(1/2) and v^(-1/2), subnormals flushed: a few
+// instructions less than the forms that keep them.
+__device__ __forceinline__ float ex2(float v)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float root(float v)
+{
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float inv_root(float v)
+{
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+constexpr float kLog2e = 1.44269504088896340736f;
+
 // s(v) and 1 - s(v) = s(-v), both to a few ulp: with e = exp(-v) they are
 // 1 / (1 + e) and e / (1 + e), where nothing cancels.  Below -80 the logit
 // counts as -80 (s = 2e-35), so that e stays finite; NaN stays NaN.
@@ -85,10 +113,11 @@ __device__ __forceinline__ void sigmoid2(float v, float& s, float& ns)
 {
     float c;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(v), "f"(-80.0f));
-    const float e = __expf(-c);
-    s = __fdividef(1.0f, 1.0f + e);
+    const float e = ex2(-kLog2e * c);
+    s = rcp(1.0f + e);
     ns = e * s;
 }
+__device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + ex2(-kLog2e * v)); }
 
 // e^v and e^v - 1 for v <= 0, both to a few ulp.  Near 0 the difference is the
 // Taylor series (eight terms: the ninth is below 2^-26 of the sum for
@@ -108,7 +137,7 @@ __device__ __forceinline__ void exp_expm1_neg(float v, float& ev, float& m)
     ev = 1.0f + p;
     if constexpr (!NEAR) {
         if (v < -0.5f) {
-            ev = __expf(v);
+            ev = ex2(kLog2e * v);
             m = ev - 1.0f;
         }
     }
