@@ -105,30 +105,101 @@ __device__ __forceinline__ void load_param(const float* p, float none, const Col
     }
 }
 
-// The values 8 bits hold of a row.
-template <bool VEC>
-__device__ __forceinline__ void load_packed(const mru_packed8& h, int64_t row, const Cols<VEC>& c, float (&v)[8])
+// The values 8 bits hold, from 8 of them and their run's scale.
+__device__ __forceinline__ void held8(uint2 q, float s, float (&v)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[e] = (float)(int8_t)(q.x >> (8 * e)) * s;
+        v[4 + e] = (float)(int8_t)(q.y >> (8 * e)) * s;
+    }
+}
+
+// A row of values held in 8 bits, column by column.
+__device__ __forceinline__ void load_packed(const mru_packed8& h, int64_t row, const Cols<false>& c, float (&v)[8])
 {
     const int8_t* q = h.q + row * c.D;
     const float* sc = h.scale + row * ((c.D + 63) / 64);
-    if constexpr (VEC) {
-        if (c.c0 >= c.D) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-            return;
-        }
-        const uint2 w = *reinterpret_cast<const uint2*>(q + c.c0);
-        const float s = sc[c.c0 / 64];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[e] = (float)(int8_t)(w.x >> (8 * e)) * s;
-            v[4 + e] = (float)(int8_t)(w.y >> (8 * e)) * s;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c.ok(e) ? (float)q[c.at(e)] * sc[c.at(e) / 64] : 0.0f;
-    }
+    for (int e = 0; e < 8; ++e) v[e] = c.ok(e) ? (float)q[c.at(e)] * sc[c.at(e) / 64] : 0.0f;
 }
+
+// Rows on their way: every thread copies its own columns of the coming rows
+// into its own slots of shared memory and later reads them back itself, so
+// that no barrier is needed; the memory's latency is covered by the rows in
+// flight, not by resident warps (whose registers hold whole rows).
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* smem, const void* gmem)
+{
+    const unsigned s = (unsigned)__cvta_generic_to_shared(smem);
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(gmem) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(gmem), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Bytes of 8 columns of one input in a stage, and stages of `inputs` plain
+// ones and `held` 8-bit ones (with their scales): up to 4 in 160 KB for 512
+// threads.
+template <typename T>
+constexpr int plane_bytes() { return 8 * (int)sizeof(T); }
+template <typename T>
+constexpr int stage_bytes(int inputs, int held) { return inputs * plane_bytes<T>() + held * 12; }
+template <typename T>
+constexpr int stages_of(int inputs, int held)
+{
+    const int n = 160 * 1024 / (512 * stage_bytes<T>(inputs, held));
+    return n > 4 ? 4 : n < 2 ? 2 : n;
+}
+
+// A thread's slots of one input: plane `at` (bytes per thread before it).
+template <typename T>
+struct Slot {
+    unsigned char* base;                   // the stage
+    __device__ __forceinline__ unsigned char* piece(int at, int k) const
+    {
+        return base + (size_t)(at + 16 * k) * blockDim.x + 16 * threadIdx.x;
+    }
+    __device__ __forceinline__ void fill(int at, const T* from) const
+    {
+#pragma unroll
+        for (int k = 0; k < plane_bytes<T>() / 16; ++k) copy_async<16>(piece(at, k), (const char*)from + 16 * k);
+    }
+    __device__ __forceinline__ void read(int at, float (&v)[8]) const
+    {
+        if constexpr (sizeof(T) == 2) {
+            const uint4 w = *reinterpret_cast<const uint4*>(piece(at, 0));
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[2 * e] = __uint_as_float(u[e] << 16);
+                v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+            }
+        } else {
+            const float4 a = *reinterpret_cast<const float4*>(piece(at, 0));
+            const float4 b = *reinterpret_cast<const float4*>(piece(at, 1));
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        }
+    }
+    // 8-bit values: 8 bytes, then the scale
+    __device__ __forceinline__ void fill8(int at, const mru_packed8& h, int64_t row, int c0, int D) const
+    {
+        copy_async<8>(base + (size_t)at * blockDim.x + 8 * threadIdx.x, h.q + row * D + c0);
+        copy_async<4>(base + (size_t)(at + 8) * blockDim.x + 4 * threadIdx.x, h.scale + row * ((D + 63) / 64) + c0 / 64);
+    }
+    __device__ __forceinline__ void read8(int at, float (&v)[8]) const
+    {
+        held8(*reinterpret_cast<const uint2*>(base + (size_t)at * blockDim.x + 8 * threadIdx.x),
+              *reinterpret_cast<const float*>(base + (size_t)(at + 8) * blockDim.x + 4 * threadIdx.x), v);
+    }
+};
 
 // Writes a row's 8-bit copy (VEC: a run of 64 channels is 8 lanes in a row).
 __device__ __forceinline__ void store_packed(const mru_packed8& h, int64_t row, const Cols<true>& c, const float (&v)[8])
@@ -262,40 +333,76 @@ __device__ __forceinline__ Cols<VEC> place(const BArgs& p, int64_t& row, int64_t
 }
 
 template <typename T, int TEAM, bool VEC, bool PACK>
-__global__ void __launch_bounds__(TEAM ? 256 : 512) k_block(BArgs p)
+__global__ void __launch_bounds__(TEAM ? 256 : 512, TEAM ? 4 : 2) k_block(BArgs p)
 {
+    extern __shared__ __align__(16) unsigned char ring[];
     __shared__ ReduceMem mem;
+    constexpr int STAGES = stages_of<T>(3, 0), PLANE = plane_bytes<T>();
     int phase = 0;
     int64_t row, step;
     const Cols<VEC> c = place<TEAM, VEC>(p, row, step);
     // teams of a warp take their shuffles together: rows past the end go through the motions
     const int64_t last = TEAM ? (p.rows + step - 1) / step * step : p.rows;
+    const bool gate = p.has_y && p.act != MRU_ACT_NONE;
+    auto slot = [&](int k) { return Slot<T>{ring + (size_t)k * 3 * PLANE * blockDim.x}; };
+    auto fill = [&](int64_t to, int k) {
+        if (to < p.rows && c.c0 < p.D) {
+            const Slot<T> s = slot(k);
+            s.fill(0, (const T*)p.r + to * p.D + c.c0);
+            if (p.has_y) s.fill(PLANE, (const T*)p.y + to * p.ldy + c.c0);
+            if (gate) s.fill(2 * PLANE, (const T*)p.g + to * p.ldg + c.c0);
+        }
+        copy_commit();
+    };
+    int stage = 0;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int k = 0; k < STAGES - 1; ++k) fill(row + k * step, k);
+    }
     for (; row < last; row += step) {
         const bool live = row < p.rows;
         const int64_t rr = live ? row : 0;
         Cols<VEC> cc = c;
         if (!live) cc.D = 0;
         const Cols<VEC> pc = live ? c : Cols<VEC>{c.D, c.step, c.D};   // the 8-bit copies' columns
-        float r[8];
-        load8<T, VEC>((const T*)p.r + rr * p.D, cc, r);
+        float r[8], y[8], g[8];
+        if constexpr (VEC) {
+            fill(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+            copy_wait<STAGES - 1>();
+            const Slot<T> s = slot(stage);
+            const bool in = cc.c0 < cc.D;
+            s.read(0, r);
+            if (p.has_y) s.read(PLANE, y);
+            if (gate) s.read(2 * PLANE, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                r[e] = in ? r[e] : 0.0f;
+                y[e] = in && p.has_y ? y[e] : 0.0f;
+                g[e] = in && gate ? g[e] : 0.0f;
+            }
+            stage = stage == STAGES - 1 ? 0 : stage + 1;
+        } else {
+            load8<T, VEC>((const T*)p.r + rr * p.D, cc, r);
+            if (p.has_y) load8<T, VEC>((const T*)p.y + rr * p.ldy, cc, y);
+            if (gate) load8<T, VEC>((const T*)p.g + rr * p.ldg, cc, g);
+        }
         if (p.has_y) {
-            float y[8], g[8], w[8], b[8], s[8];
-            load8<T, VEC>((const T*)p.y + rr * p.ldy, cc, y);
-            if (p.act != MRU_ACT_NONE) load8<T, VEC>((const T*)p.g + rr * p.ldg, cc, g);
-            load_param<VEC>(p.prm.w_y, 1.0f, cc, w);
-            load_param<VEC>(p.prm.b_y, 0.0f, cc, b);
-            load_param<VEC>(p.prm.s, 1.0f, cc, s);
+            float w[8], b[8];
             if constexpr (PACK && VEC) {
                 store_packed(p.y8, rr, pc, y);
-                if (p.act != MRU_ACT_NONE) store_packed(p.g8, rr, pc, g);
+                if (gate) store_packed(p.g8, rr, pc, g);
             }
             const float rstd = normalise<TEAM, VEC>(p, cc, y, mem, phase);
+            load_param<VEC>(p.prm.w_y, 1.0f, cc, w);
+            load_param<VEC>(p.prm.b_y, 0.0f, cc, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e] * rstd, w[e], b[e]);
+            load_param<VEC>(p.prm.s, 1.0f, cc, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float a, da;
                 activation(p.act, g[e], a, da);
-                const float n = fmaf(y[e] * rstd, w[e], b[e]);
-                r[e] = fmaf(p.rs * s[e] * a, n, r[e]);
+                r[e] = fmaf(p.rs * w[e] * a, y[e], r[e]);
                 if (!cc.ok(e)) r[e] = 0.0f;
             }
             store8<T, VEC>((T*)p.r_out + rr * p.D, cc, r);
@@ -308,9 +415,9 @@ __global__ void __launch_bounds__(TEAM ? 256 : 512) k_block(BArgs p)
         }
         if (p.has_z) {
             float w[8], b[8];
+            const float rstd = normalise<TEAM, VEC>(p, cc, r, mem, phase);
             load_param<VEC>(p.prm.w_z, 1.0f, cc, w);
             load_param<VEC>(p.prm.b_z, 0.0f, cc, b);
-            const float rstd = normalise<TEAM, VEC>(p, cc, r, mem, phase);
 #pragma unroll
             for (int e = 0; e < 8; ++e) r[e] = fmaf(r[e] * rstd, w[e], b[e]);
             store8<T, VEC>((T*)p.z + rr * p.D, cc, r);
@@ -346,8 +453,12 @@ __device__ __forceinline__ void write_part(const BArgs& p, const Cols<VEC>& c, i
 template <typename T, int TEAM, bool VEC, bool PACKED, bool FULL>
 __global__ void __launch_bounds__(TEAM ? 256 : 512) k_block_bwd(BArgs p)
 {
+    extern __shared__ __align__(16) unsigned char ring[];
     __shared__ ReduceMem mem;
     __shared__ float sums[TEAM ? 2048 : 1];
+    constexpr int STAGES = stages_of<T>(PACKED ? 2 : 5, PACKED ? 3 : 0), PLANE = plane_bytes<T>();
+    constexpr int STAGE = stage_bytes<T>(PACKED ? 2 : 5, PACKED ? 3 : 0);
+    constexpr int R8 = 2 * PLANE, NEXT = PACKED ? 12 : PLANE;      // planes: dr', dz, r', y, g
     int phase = 0;
     int64_t row, step;
     const Cols<VEC> c = place<TEAM, VEC>(p, row, step);
@@ -357,24 +468,72 @@ __global__ void __launch_bounds__(TEAM ? 256 : 512) k_block_bwd(BArgs p)
     float dwy[8], ds[8], dwz[8], dby[8], dbz[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) dwy[e] = ds[e] = dwz[e] = dby[e] = dbz[e] = 0.0f;
+    const bool gate = p.has_y && p.act != MRU_ACT_NONE;
+    auto slot = [&](int k) { return Slot<T>{ring + (size_t)k * STAGE * blockDim.x}; };
+    auto fill = [&](int64_t to, int k) {
+        if (to < p.rows && c.c0 < p.D) {
+            const Slot<T> s = slot(k);
+            if (p.dro) s.fill(0, (const T*)p.dro + to * p.D + c.c0);
+            if (p.has_z) s.fill(PLANE, (const T*)p.dz + to * p.D + c.c0);
+            if constexpr (PACKED) {
+                if (p.has_z) s.fill8(R8, p.r8, to, c.c0, p.D);
+                if (p.has_y) s.fill8(R8 + NEXT, p.y8, to, c.c0, p.D);
+                if (gate) s.fill8(R8 + 2 * NEXT, p.g8, to, c.c0, p.D);
+            } else {
+                if (p.has_z) s.fill(R8, (const T*)p.r + to * p.D + c.c0);
+                if (p.has_y) s.fill(R8 + NEXT, (const T*)p.y + to * p.ldy + c.c0);
+                if (gate) s.fill(R8 + 2 * NEXT, (const T*)p.g + to * p.ldg + c.c0);
+            }
+        }
+        copy_commit();
+    };
+    int stage = 0;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int k = 0; k < STAGES - 1; ++k) fill(row + k * step, k);
+    }
     for (; row < last; row += step) {
         const bool live = row < p.rows;
         const int64_t rr = live ? row : 0;
         Cols<VEC> cc = c;
         if (!live) cc.D = 0;
         float e_[8], u[8], r[8], y[8], g[8], dz[8], w[8];
-        const Cols<VEC> pc = live ? c : Cols<VEC>{c.D, c.step, c.D};
-        if (p.dro) load8<T, VEC>((const T*)p.dro + rr * p.D, cc, e_);
-        if (p.has_z) {
-            load8<T, VEC>((const T*)p.dz + rr * p.D, cc, dz);
-            if constexpr (PACKED) load_packed<VEC>(p.r8, rr, pc, r);
-            else load8<T, VEC>((const T*)p.r + rr * p.D, cc, r);
-        }
-        if (p.has_y) {
-            if constexpr (PACKED) load_packed<VEC>(p.y8, rr, pc, y);
-            else load8<T, VEC>((const T*)p.y + rr * p.ldy, cc, y);
-            if (p.act != MRU_ACT_NONE) {
-                if constexpr (PACKED) load_packed<VEC>(p.g8, rr, pc, g);
+        if constexpr (VEC) {
+            fill(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+            copy_wait<STAGES - 1>();
+            const Slot<T> s = slot(stage);
+            if (p.dro) s.read(0, e_);
+            if (p.has_z) {
+                s.read(PLANE, dz);
+                if constexpr (PACKED) s.read8(R8, r);
+                else s.read(R8, r);
+            }
+            if (p.has_y) {
+                if constexpr (PACKED) s.read8(R8 + NEXT, y);
+                else s.read(R8 + NEXT, y);
+            }
+            if (gate) {
+                if constexpr (PACKED) s.read8(R8 + 2 * NEXT, g);
+                else s.read(R8 + 2 * NEXT, g);
+            }
+            if (cc.c0 >= cc.D) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) e_[e] = dz[e] = r[e] = y[e] = g[e] = 0.0f;
+            }
+            stage = stage == STAGES - 1 ? 0 : stage + 1;
+        } else {
+            if (p.dro) load8<T, VEC>((const T*)p.dro + rr * p.D, cc, e_);
+            if (p.has_z) {
+                load8<T, VEC>((const T*)p.dz + rr * p.D, cc, dz);
+                if constexpr (PACKED) load_packed(p.r8, rr, cc, r);
+                else load8<T, VEC>((const T*)p.r + rr * p.D, cc, r);
+            }
+            if (p.has_y) {
+                if constexpr (PACKED) load_packed(p.y8, rr, cc, y);
+                else load8<T, VEC>((const T*)p.y + rr * p.ldy, cc, y);
+            }
+            if (gate) {
+                if constexpr (PACKED) load_packed(p.g8, rr, cc, g);
                 else load8<T, VEC>((const T*)p.g + rr * p.ldg, cc, g);
             }
         }
@@ -513,13 +672,20 @@ Shape shape_of(int64_t rows, int64_t D, bool vec, int per_sm)
     return s;
 }
 
+// `per_thread`: bytes of shared memory of a thread's rows on their way.
 template <typename K>
-cudaError_t launch(K kernel, const Shape& sh, const BArgs& p, cudaStream_t s)
+cudaError_t launch(K kernel, const Shape& sh, const BArgs& p, int per_thread, cudaStream_t s)
 {
+    const size_t smem = (size_t)per_thread * (size_t)sh.threads;
+    if (smem > 32 * 1024) {                                        // with the static part, beyond the default 48 KB
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3(sh.grid);
     cfg.blockDim = dim3((unsigned)sh.threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -534,22 +700,25 @@ cudaError_t launch(K kernel, const Shape& sh, const BArgs& p, cudaStream_t s)
 template <typename T>
 cudaError_t run_forward(const Shape& sh, const BArgs& p, bool vec, bool pack, cudaStream_t s)
 {
-    if (!vec) return launch(k_block<T, 0, false, false>, sh, p, s);
-    if (sh.team == 8) return launch(pack ? k_block<T, 8, true, true> : k_block<T, 8, true, false>, sh, p, s);
-    if (sh.team == 32) return launch(pack ? k_block<T, 32, true, true> : k_block<T, 32, true, false>, sh, p, s);
-    return launch(pack ? k_block<T, 0, true, true> : k_block<T, 0, true, false>, sh, p, s);
+    constexpr int ring = stages_of<T>(3, 0) * stage_bytes<T>(3, 0);
+    if (!vec) return launch(k_block<T, 0, false, false>, sh, p, 0, s);
+    if (sh.team == 8) return launch(pack ? k_block<T, 8, true, true> : k_block<T, 8, true, false>, sh, p, ring, s);
+    if (sh.team == 32) return launch(pack ? k_block<T, 32, true, true> : k_block<T, 32, true, false>, sh, p, ring, s);
+    return launch(pack ? k_block<T, 0, true, true> : k_block<T, 0, true, false>, sh, p, ring, s);
 }
 
 template <typename T, bool PACKED, bool FULL>
 cudaError_t run_backward(const Shape& sh, const BArgs& p, bool vec, cudaStream_t s)
 {
-    if (!vec) return launch(k_block_bwd<T, 0, false, PACKED, FULL>, sh, p, s);
-    if (sh.team == 8) return launch(k_block_bwd<T, 8, true, PACKED, FULL>, sh, p, s);
-    if (sh.team == 32) return launch(k_block_bwd<T, 32, true, PACKED, FULL>, sh, p, s);
-    return launch(k_block_bwd<T, 0, true, PACKED, FULL>, sh, p, s);
+    constexpr int plain = PACKED ? 2 : 5, held = PACKED ? 3 : 0;
+    constexpr int ring = stages_of<T>(plain, held) * stage_bytes<T>(plain, held);
+    if (!vec) return launch(k_block_bwd<T, 0, false, PACKED, FULL>, sh, p, 0, s);
+    if (sh.team == 8) return launch(k_block_bwd<T, 8, true, PACKED, FULL>, sh, p, ring, s);
+    if (sh.team == 32) return launch(k_block_bwd<T, 32, true, PACKED, FULL>, sh, p, ring, s);
+    return launch(k_block_bwd<T, 0, true, PACKED, FULL>, sh, p, ring, s);
 }
 
-constexpr int kBwdPerSm = 1, kFwdPerSm = 4;
+constexpr int kBwdPerSm = 1, kFwdPerSm = 2;
 
 mru_status check_problem(const mru_block_problem* p)
 {

@@ -39,6 +39,106 @@ __global__ void __launch_bounds__(256) k_unpack8(int64_t rows, int64_t D, int64_
     }
 }
 
+// 16 channels to a lane, 4 lanes to a run: rows, x and q on 16 bytes.
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, float (&v)[16])
+{
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p) + k);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[8 * k + 2 * e] = __uint_as_float(u[e] << 16);
+                v[8 * k + 2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 w = __ldcs(reinterpret_cast<const float4*>(p) + k);
+            v[4 * k] = w.x; v[4 * k + 1] = w.y; v[4 * k + 2] = w.z; v[4 * k + 3] = w.w;
+        }
+    }
+}
+
+// Quotient of a count that mostly fits 32 bits, whose division is far shorter.
+__device__ __forceinline__ int64_t quotient(int64_t k, int32_t d)
+{
+    return k >> 32 ? k / d : (int64_t)((uint32_t)k / (uint32_t)d);
+}
+
+// Pieces of 16 channels, `rows` x `per_row`; a row's pieces fill whole runs of
+// lanes (per_row a multiple of 4 lanes' pieces, the last ones empty).
+template <typename T>
+__global__ void __launch_bounds__(256) k_pack8_wide(int64_t rows, int32_t D, int32_t per_row, int64_t ld,
+                                                    const T* __restrict__ x, int8_t* __restrict__ q,
+                                                    float* __restrict__ scale)
+{
+    const int64_t n = rows * per_row, step = (int64_t)gridDim.x * blockDim.x, runs = (D + 63) / 64;
+    const int64_t end = (n + 31) / 32 * 32;                  // whole warps
+    for (int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; k < end; k += step) {
+        const int64_t row = quotient(k, per_row);
+        const int c = (int)(k - row * per_row) * 16;
+        const bool in = k < n && c < D;
+        float v[16];
+        uint32_t m = 0;
+        if (in) load16(x + row * ld + c, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) m = in ? max(m, mag_bits(v[e])) : 0u;
+        m = max(m, __shfl_xor_sync(~0u, m, 1));
+        m = max(m, __shfl_xor_sync(~0u, m, 2));
+        if (!in) continue;
+        float inv, sc;
+        pack8_factors(__uint_as_float(m), inv, sc);
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e / 4] |= (uint32_t)pack8_q(v[e], inv) << (8 * (e % 4));
+        *reinterpret_cast<uint4*>(q + row * D + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (c % 64 == 0) scale[row * runs + c / 64] = sc;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) k_unpack8_wide(int64_t rows, int32_t D, int64_t ld, const int8_t* __restrict__ q,
+                                                      const float* __restrict__ scale, T* __restrict__ x)
+{
+    const int32_t per_row = D / 16;
+    const int64_t n = rows * per_row, step = (int64_t)gridDim.x * blockDim.x, runs = (D + 63) / 64;
+    for (int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; k < n; k += step) {
+        const int64_t row = quotient(k, per_row);
+        const int c = (int)(k - row * per_row) * 16;
+        const uint4 w = __ldcs(reinterpret_cast<const uint4*>(q + row * D + c));
+        const float s = scale[row * runs + c / 64];
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        T* to = x + row * ld + c;
+#pragma unroll
+        for (int h = 0; h < 16 * (int)sizeof(T) / 16; ++h) {
+            constexpr int per = 16 / sizeof(T);
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (sizeof(T) == 4) {
+                    o[e] = __float_as_uint((float)(int8_t)(u[h] >> (8 * e)) * s);
+                } else {
+                    const int at = per * h + 2 * e;
+                    const __nv_bfloat162 b = __floats2bfloat162_rn((float)(int8_t)(u[at / 4] >> (8 * (at % 4))) * s,
+                                                                   (float)(int8_t)(u[at / 4] >> (8 * (at % 4 + 1))) * s);
+                    o[e] = *reinterpret_cast<const uint32_t*>(&b);
+                }
+            }
+            __stcs(reinterpret_cast<uint4*>(to) + h, make_uint4(o[0], o[1], o[2], o[3]));
+        }
+    }
+}
+
+// Rows that take the wide kernels: whole pieces of 16 channels, on 16 bytes.
+bool wide_rows(int64_t D, int64_t ld, int32_t dtype, const void* x, const int8_t* q)
+{
+    return D % 16 == 0 && D <= (1 << 30) && (ld * (int64_t)elem_size(dtype)) % 16 == 0 && aligned(x, 16) && aligned(q, 16);
+}
+
 unsigned grid_for(int64_t blocks) { return (unsigned)(blocks < 148 * 16 ? blocks : 148 * 16); }
 
 mru_status check(int64_t rows, int64_t D, int64_t& ld, int32_t dtype, const void* x, const mru_packed8* h, bool packs)
@@ -62,6 +162,15 @@ mru_status check(int64_t rows, int64_t D, int64_t& ld, int32_t dtype, const void
 cudaError_t launch_pack8(int64_t rows, int64_t D, int64_t ld, int32_t dtype, const void* x, const mru_packed8& out,
                          cudaStream_t s)
 {
+    if (wide_rows(D, ld, dtype, x, out.q)) {
+        const int32_t per_row = (int32_t)(div_up(D, 64) * 4);
+        const unsigned blocks = grid_for(div_up(rows * per_row, 256));
+        if (dtype == MRU_BF16)
+            k_pack8_wide<<<blocks, 256, 0, s>>>(rows, (int32_t)D, per_row, ld, (const __nv_bfloat16*)x, out.q, out.scale);
+        else
+            k_pack8_wide<<<blocks, 256, 0, s>>>(rows, (int32_t)D, per_row, ld, (const float*)x, out.q, out.scale);
+        return cudaGetLastError();
+    }
     const unsigned grid = grid_for(div_up(rows * div_up(D, 64), 8));
     if (dtype == MRU_BF16)
         k_pack8<<<grid, 256, 0, s>>>(rows, D, ld, (const __nv_bfloat16*)x, out.q, out.scale);
@@ -90,6 +199,14 @@ mru_status mru_unpack8(int64_t rows, int64_t D, int64_t ld, int32_t dtype, const
     const mru_status st = check(rows, D, ld, dtype, x, in, false);
     if (st != MRU_OK || rows == 0 || D == 0) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (wide_rows(D, ld, dtype, x, in->q)) {
+        const unsigned blocks = grid_for(ops::div_up(rows * (D / 16), 256));
+        if (dtype == MRU_BF16)
+            k_unpack8_wide<<<blocks, 256, 0, s>>>(rows, (int32_t)D, ld, in->q, in->scale, (__nv_bfloat16*)x);
+        else
+            k_unpack8_wide<<<blocks, 256, 0, s>>>(rows, (int32_t)D, ld, in->q, in->scale, (float*)x);
+        return ops::cuda_status(cudaGetLastError());
+    }
     const unsigned grid = grid_for(ops::div_up(rows * D, 256));
     if (dtype == MRU_BF16)
         k_unpack8<<<grid, 256, 0, s>>>(rows, D, ld, in->q, in->scale, (__nv_bfloat16*)x);
