@@ -224,68 +224,115 @@ __device__ __forceinline__ void store_packed(const mru_packed8& h, int64_t row, 
 // that one barrier serves a reduction: a buffer is written again only after
 // the next reduction's barrier, which every reader has reached.
 struct ReduceMem {
-    float warp[2][16][4];
-    float cta[2][kMaxCluster][4];
+    float4 warp[2][4][4];                  // [sum][warps by fours]; warps that are not there stay 0
+    float4 cta[2][4];                      // [sum], a CTA of the cluster to a component
 };
+
+__device__ __forceinline__ void clear(ReduceMem& m)
+{
+    float* f = reinterpret_cast<float*>(&m);
+    for (int k = threadIdx.x; k < (int)(sizeof(ReduceMem) / 4); k += blockDim.x) f[k] = 0.0f;
+    __syncthreads();
+}
+
+// N sums of a warp: halves of it take over half of the sums each, so that 4
+// sums take 6 shuffles.  Returns the lane's sum; lane 32 / N * k holds sum k.
+template <int N>
+__device__ __forceinline__ float warp_sums(const float (&v)[N], int lane)
+{
+    float r;
+    if constexpr (N == 4) {
+        const bool hi = lane & 16, up = lane & 8;
+        const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(~0u, hi ? v[0] : v[2], 16);
+        const float b = (hi ? v[3] : v[1]) + __shfl_xor_sync(~0u, hi ? v[1] : v[3], 16);
+        r = (up ? b : a) + __shfl_xor_sync(~0u, up ? a : b, 8);
+    } else if constexpr (N == 2) {
+        const bool hi = lane & 16;
+        r = (hi ? v[1] : v[0]) + __shfl_xor_sync(~0u, hi ? v[0] : v[1], 16);
+        r += __shfl_xor_sync(~0u, r, 8);
+    } else {
+        static_assert(N == 1, "1, 2 or 4 sums");
+        r = v[0] + __shfl_xor_sync(~0u, v[0], 16);
+        r += __shfl_xor_sync(~0u, r, 8);
+    }
+#pragma unroll
+    for (int o = 4; o; o >>= 1) r += __shfl_xor_sync(~0u, r, o);
+    return r;
+}
 
 template <int TEAM, int N>
 __device__ __forceinline__ void team_sum(float (&v)[N], ReduceMem& m, int cluster, int& phase)
 {
+    if constexpr (TEAM > 0) {
 #pragma unroll
-    for (int o = (TEAM ? TEAM : 32) / 2; o; o >>= 1)
+        for (int o = TEAM / 2; o; o >>= 1)
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(~0u, v[k], o);
-    if constexpr (TEAM == 0) {
-        const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
-        if (warps > 1) {
-            if ((threadIdx.x & 31) == 0) {
+            for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(~0u, v[k], o);
+    } else {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+        const float r = warp_sums(v, lane);
+        if (lane % (32 / N) == 0) reinterpret_cast<float*>(&m.warp[phase][lane * N / 32][0])[warp] = r;
+        __syncthreads();
+        const int fours = (int)(blockDim.x + 127) / 128;
 #pragma unroll
-                for (int k = 0; k < N; ++k) m.warp[phase][warp][k] = v[k];
+        for (int k = 0; k < N; ++k) {
+            float4 q = m.warp[phase][k][0];
+            for (int w = 1; w < fours; ++w) {
+                const float4 t = m.warp[phase][k][w];
+                q = make_float4(q.x + t.x, q.y + t.y, q.z + t.z, q.w + t.w);
             }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = 0.0f;
-            for (int w = 0; w < warps; ++w) {
-#pragma unroll
-                for (int k = 0; k < N; ++k) v[k] += m.warp[phase][w][k];
-            }
+            v[k] = (q.x + q.y) + (q.z + q.w);
         }
         if (cluster > 1) {
             cg::cluster_group cl = cg::this_cluster();
             const unsigned rank = cl.block_rank();
             if ((int)threadIdx.x < cluster) {
-                float* to = cl.map_shared_rank(&m.cta[phase][rank][0], threadIdx.x);
+                float* to = cl.map_shared_rank(reinterpret_cast<float*>(&m.cta[phase][0]), threadIdx.x);
 #pragma unroll
-                for (int k = 0; k < N; ++k) to[k] = v[k];
+                for (int k = 0; k < N; ++k) to[4 * k + rank] = v[k];
             }
             cl.sync();
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = 0.0f;
-            for (int w = 0; w < cluster; ++w) {
-#pragma unroll
-                for (int k = 0; k < N; ++k) v[k] += m.cta[phase][w][k];
+            for (int k = 0; k < N; ++k) {
+                const float4 q = m.cta[phase][k];
+                v[k] = (q.x + q.y) + (q.z + q.w);
             }
         }
         phase ^= 1;
     }
 }
 
-// act(g) and its derivative.
-__device__ __forceinline__ void activation(int act, float g, float& a, float& da)
+// g becomes act(g), and da its derivative where it is asked for.
+template <bool DERIVATIVE>
+__device__ __forceinline__ void activation(int act, float (&g)[8], float (&da)[8])
 {
-    if (act == MRU_ACT_NONE) {
-        a = 1.0f;
-        da = 0.0f;
-        return;
-    }
-    float s, ns;
-    sigmoid2(g, s, ns);
     if (act == MRU_ACT_SILU) {
-        a = g * s;
-        da = s * fmaf(g, ns, 1.0f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float c = logit(g[e]);
+            if constexpr (DERIVATIVE) {
+                float s, ns;
+                sigmoid2(c, s, ns);
+                da[e] = s * fmaf(c, ns, 1.0f);
+                g[e] = c * s;
+            } else {
+                g[e] = c * sigmoid(c);
+            }
+        }
+    } else if (act == MRU_ACT_SIGMOID) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float s, ns;
+            sigmoid2(g[e], s, ns);
+            if constexpr (DERIVATIVE) da[e] = s * ns;
+            g[e] = s;
+        }
     } else {
-        a = s;
-        da = s * ns;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            g[e] = 1.0f;
+            if constexpr (DERIVATIVE) da[e] = 0.0f;
+        }
     }
 }
 
@@ -308,7 +355,7 @@ __device__ __forceinline__ float normalise(const BArgs& p, const Cols<VEC>& c, f
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[0] = fmaf(v[e], v[e], s[0]);
     team_sum<TEAM>(s, m, p.cluster, phase);
-    return rsqrtf(fmaf(s[0], inv_d, p.eps));
+    return inv_root(fmaf(s[0], inv_d, p.eps));
 }
 
 // The thread's place: team (row within the CTA's rows) and columns.
@@ -339,6 +386,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 512, TEAM ? 4 : 2) k_block(BArgs 
     __shared__ ReduceMem mem;
     constexpr int STAGES = stages_of<T>(3, 0), PLANE = plane_bytes<T>();
     int phase = 0;
+    if (TEAM == 0) clear(mem);
     int64_t row, step;
     const Cols<VEC> c = place<TEAM, VEC>(p, row, step);
     // teams of a warp take their shuffles together: rows past the end go through the motions
@@ -369,16 +417,14 @@ __global__ void __launch_bounds__(TEAM ? 256 : 512, TEAM ? 4 : 2) k_block(BArgs 
         if constexpr (VEC) {
             fill(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
             copy_wait<STAGES - 1>();
-            const Slot<T> s = slot(stage);
-            const bool in = cc.c0 < cc.D;
-            s.read(0, r);
-            if (p.has_y) s.read(PLANE, y);
-            if (gate) s.read(2 * PLANE, g);
+            if (cc.c0 < cc.D) {
+                const Slot<T> s = slot(stage);
+                s.read(0, r);
+                if (p.has_y) s.read(PLANE, y);
+                if (gate) s.read(2 * PLANE, g);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                r[e] = in ? r[e] : 0.0f;
-                y[e] = in && p.has_y ? y[e] : 0.0f;
-                g[e] = in && gate ? g[e] : 0.0f;
+                for (int e = 0; e < 8; ++e) r[e] = y[e] = g[e] = 0.0f;
             }
             stage = stage == STAGES - 1 ? 0 : stage + 1;
         } else {
@@ -398,12 +444,15 @@ __global__ void __launch_bounds__(TEAM ? 256 : 512, TEAM ? 4 : 2) k_block(BArgs 
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e] * rstd, w[e], b[e]);
             load_param<VEC>(p.prm.s, 1.0f, cc, w);
+            activation<false>(p.act, g, b);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float a, da;
-                activation(p.act, g[e], a, da);
-                r[e] = fmaf(p.rs * w[e] * a, y[e], r[e]);
-                if (!cc.ok(e)) r[e] = 0.0f;
+                r[e] = fmaf(p.rs * w[e] * g[e], y[e], r[e]);
+                if (!VEC && !cc.ok(e)) r[e] = 0.0f;
+            }
+            if (VEC && cc.c0 >= cc.D) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) r[e] = 0.0f;
             }
             store8<T, VEC>((T*)p.r_out + rr * p.D, cc, r);
         }
@@ -460,6 +509,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 512) k_block_bwd(BArgs p)
     constexpr int STAGE = stage_bytes<T>(PACKED ? 2 : 5, PACKED ? 3 : 0);
     constexpr int R8 = 2 * PLANE, NEXT = PACKED ? 12 : PLANE;      // planes: dr', dz, r', y, g
     int phase = 0;
+    if (TEAM == 0) clear(mem);
     int64_t row, step;
     const Cols<VEC> c = place<TEAM, VEC>(p, row, step);
     const int64_t last = TEAM ? (p.rows + step - 1) / step * step : p.rows;
@@ -569,9 +619,9 @@ __global__ void __launch_bounds__(TEAM ? 256 : 512) k_block_bwd(BArgs p)
         }
         team_sum<TEAM>(s, mem, p.cluster, phase);
         // a row past the end adds nothing to the sums, whatever eps is
-        const float rstd_y = live ? rsqrtf(fmaf(s[2], inv_d, p.eps)) : 0.0f;
+        const float rstd_y = live ? inv_root(fmaf(s[2], inv_d, p.eps)) : 0.0f;
         if (p.has_z) {
-            const float rstd = live ? rsqrtf(fmaf(s[0], inv_d, p.eps)) : 0.0f;
+            const float rstd = live ? inv_root(fmaf(s[0], inv_d, p.eps)) : 0.0f;
             const float c1 = rstd * s[1] * inv_d, c0 = layer ? s[3] * inv_d : 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -588,16 +638,15 @@ __global__ void __launch_bounds__(TEAM ? 256 : 512) k_block_bwd(BArgs p)
         load_param<VEC>(p.prm.b_y, 0.0f, cc, b);
         load_param<VEC>(p.prm.s, 1.0f, cc, sc);
         float t[2] = {0.0f, 0.0f};                         // q yhat, q
+        activation<true>(p.act, g, dz);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float a, da;
-            activation(p.act, g[e], a, da);
             const float hat = y[e] * rstd_y, n = fmaf(hat, w[e], b[e]);
-            const float re = cc.ok(e) ? p.rs * e_[e] : 0.0f, dm = re * sc[e], dn = dm * a;
-            ds[e] = fmaf(re * a, n, ds[e]);
+            const float re = !FULL || cc.ok(e) ? p.rs * e_[e] : 0.0f, dm = re * sc[e], dn = dm * g[e];
+            ds[e] = fmaf(re * g[e], n, ds[e]);
             dwy[e] = fmaf(dn, hat, dwy[e]);
             if (FULL) dby[e] += dn;
-            g[e] = dm * n * da;
+            g[e] = dm * n * dz[e];
             u[e] = dn * w[e];
             y[e] = hat;
             t[0] = fmaf(u[e], hat, t[0]);

@@ -106,14 +106,19 @@ __device__ __forceinline__ float inv_root(float v)
 }
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// s(v) and 1 - s(v) = s(-v), both to a few ulp: with e = exp(-v) they are
-// 1 / (1 + e) and e / (1 + e), where nothing cancels.  Below -80 the logit
-// counts as -80 (s = 2e-35), so that e stays finite; NaN stays NaN.
-__device__ __forceinline__ void sigmoid2(float v, float& s, float& ns)
+// A logit below -80 counts as -80 (s = 2e-35), so that exp(-v) stays finite;
+// NaN stays NaN.
+__device__ __forceinline__ float logit(float v)
 {
     float c;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(v), "f"(-80.0f));
-    const float e = ex2(-kLog2e * c);
+    return c;
+}
+// s(v) and 1 - s(v) = s(-v), both to a few ulp: with e = exp(-v) they are
+// 1 / (1 + e) and e / (1 + e), where nothing cancels.
+__device__ __forceinline__ void sigmoid2(float v, float& s, float& ns)
+{
+    const float e = ex2(-kLog2e * logit(v));
     s = rcp(1.0f + e);
     ns = e * s;
 }
