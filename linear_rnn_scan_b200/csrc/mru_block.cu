@@ -1,11 +1,16 @@
 // mru_block.cu -- the ends of a block, row by row: r' = r + rs s act(g) N(y),
 // z = N(r'), and the backward with the parameters' sums over rows.
 //
-// A row is held in registers, 8 columns to a thread, from its one read to its
-// one write; its sums go through shuffles, then shared memory, then (rows
-// wider than 4096) the distributed shared memory of a cluster of CTAs.
+// A row is held in registers, 8 or 16 columns to a thread, from its one read
+// to its one write; its sums go through shuffles, then shared memory, then
+// (rows wider than 2048) the distributed shared memory of a cluster of CTAs.
+// 16 columns to a thread, packed fp32 arithmetic and sums exchanged by halves
+// of a warp keep the instructions per element below what memory allows.
 #include <cooperative_groups.h>
 #include <string.h>
+
+#include <atomic>
+#include <type_traits>
 
 #include "mru_ops.cuh"
 
@@ -17,7 +22,7 @@ namespace {
 using namespace ops;
 
 constexpr int kMaxD = 16384;
-constexpr int kCtaCols = 4096;             // 512 threads of 8 columns
+constexpr int kCtaCols = 2048;             // a CTA's columns: 128 threads, 16 to a thread
 constexpr int kMaxCluster = kMaxD / kCtaCols;
 
 struct BArgs {
@@ -35,107 +40,151 @@ struct BArgs {
     bool has_y, has_z;
 };
 
-// The columns of a thread: 8 in a row (VEC), or 8 a team apart.
-template <bool VEC>
+// How a thread's columns lie: NV times 8 in a row (kWide; kExact: every one of
+// them is there), or 8 NV of them a team apart (kSingle).  D counts as 0 for
+// rows past the end.
+enum Lay { kSingle, kWide, kExact };
+template <int NV, Lay LAY>
 struct Cols {
-    int c0, step, D;             // D is also the row pitch of the 8-bit copies
-    __device__ __forceinline__ int at(int e) const { return VEC ? c0 + e : c0 + e * step; }
-    __device__ __forceinline__ bool ok(int e) const { return VEC ? c0 < D : at(e) < D; }
+    int c0, step, D;
+    __device__ __forceinline__ int at(int e) const { return LAY ? c0 + e / 8 * (8 * step) + e % 8 : c0 + e * step; }
+    __device__ __forceinline__ bool ok(int e) const { return LAY == kExact || at(e) < D; }
 };
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* row, const Cols<VEC>& c, float (&v)[8])
+// 8 columns in a row of memory.
+__device__ __forceinline__ void load8(const float* p, F2* v)
 {
-    if constexpr (VEC) {
-        if (c.c0 >= c.D) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = F2{a.x, a.y};
+    v[1] = F2{a.z, a.w};
+    v[2] = F2{b.x, b.y};
+    v[3] = F2{b.z, b.w};
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, F2* v)
+{
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    v[0] = bf16_pair(w.x);
+    v[1] = bf16_pair(w.y);
+    v[2] = bf16_pair(w.z);
+    v[3] = bf16_pair(w.w);
+}
+__device__ __forceinline__ void store8(float* p, const F2* v)
+{
+    *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const F2* v)
+{
+    uint32_t u[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-        } else if constexpr (sizeof(T) == 2) {
-            const uint4 w = *reinterpret_cast<const uint4*>(row + c.c0);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    for (int k = 0; k < 4; ++k) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[k].x, v[k].y);
+        u[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// 8 of a thread's columns (its k-th eight) from and to a row in memory.
+template <typename T, int NV, Lay LAY>
+__device__ __forceinline__ void store_eight(T* row, const Cols<NV, LAY>& c, int k, const F2 (&v)[4])
+{
+    if constexpr (LAY != kSingle) {
+        if (c.ok(8 * k)) store8(row + c.at(8 * k), v);
+    } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[2 * e] = __uint_as_float(u[e] << 16);
-                v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-            }
-        } else {
-            const float4 a = *reinterpret_cast<const float4*>(row + c.c0);
-            const float4 b = *reinterpret_cast<const float4*>(row + c.c0 + 4);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        for (int j = 0; j < 4; ++j) {
+            if (c.ok(8 * k + 2 * j)) row[c.at(8 * k + 2 * j)] = from_f32<T>(v[j].x);
+            if (c.ok(8 * k + 2 * j + 1)) row[c.at(8 * k + 2 * j + 1)] = from_f32<T>(v[j].y);
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c.ok(e) ? to_f32(row[c.at(e)]) : 0.0f;
     }
 }
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* row, const Cols<VEC>& c, const float (&v)[8])
+template <int NV, Lay LAY>
+__device__ __forceinline__ void load_param(const float* p, float none, const Cols<NV, LAY>& c, int k, F2 (&v)[4])
 {
-    if constexpr (VEC) {
-        if (c.c0 >= c.D) return;
-        if constexpr (sizeof(T) == 2) {
-            uint32_t u[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-                u[e] = *reinterpret_cast<const uint32_t*>(&p);
-            }
-            *reinterpret_cast<uint4*>(row + c.c0) = make_uint4(u[0], u[1], u[2], u[3]);
-        } else {
-            *reinterpret_cast<float4*>(row + c.c0) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(row + c.c0 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    for (int j = 0; j < 4; ++j) v[j] = both(none);
+    if (!p) return;
+    if constexpr (LAY != kSingle) {
+        if (c.ok(8 * k)) load8(p + c.at(8 * k), v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (c.ok(8 * k + 2 * j)) v[j].x = p[c.at(8 * k + 2 * j)];
+            if (c.ok(8 * k + 2 * j + 1)) v[j].y = p[c.at(8 * k + 2 * j + 1)];
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (c.ok(e)) row[c.at(e)] = from_f32<T>(v[e]);
     }
 }
-
-template <bool VEC>
-__device__ __forceinline__ void load_param(const float* p, float none, const Cols<VEC>& c, float (&v)[8])
+// Columns that are not there become zero.
+template <int NV, Lay LAY>
+__device__ __forceinline__ void mask(const Cols<NV, LAY>& c, int k, F2 (&v)[4])
 {
-    if (p) {
-        load8<float, VEC>(p, c, v);
-    } else {
+    if constexpr (LAY == kWide) {
+        if (!c.ok(8 * k)) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = none;
+            for (int j = 0; j < 4; ++j) v[j] = both(0.0f);
+        }
+    } else if constexpr (LAY == kSingle) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (!c.ok(8 * k + 2 * j)) v[j].x = 0.0f;
+            if (!c.ok(8 * k + 2 * j + 1)) v[j].y = 0.0f;
+        }
     }
 }
-
-// The values 8 bits hold, from 8 of them and their run's scale.
-__device__ __forceinline__ void held8(uint2 q, float s, float (&v)[8])
+__device__ __forceinline__ float total(const F2 (&v)[4])
 {
+    const F2 s = (v[0] + v[1]) + (v[2] + v[3]);
+    return s.x + s.y;
+}
+__device__ __forceinline__ float dot(const F2 (&a)[4], const F2 (&b)[4])
+{
+    const F2 s = fma2(a[0], b[0], a[1] * b[1]) + fma2(a[2], b[2], a[3] * b[3]);
+    return s.x + s.y;
+}
+// Keeps the work on a thread's first eight columns ahead of that on its
+// second, so that their inputs are not all in registers at once.
+__device__ __forceinline__ void in_turn() { asm volatile("" ::: "memory"); }
+
+// Writes a row's 8-bit copy (a run of 64 channels is 8 lanes in a row).  The
+// pitch is `D`; columns that are not there are zero in v and not written.
+template <int NV, Lay LAY>
+__device__ __forceinline__ void store_packed(const mru_packed8& h, int64_t row, int D, const Cols<NV, LAY>& c, int k,
+                                             const F2 (&v)[4])
+{
+    uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        v[e] = (float)(int8_t)(q.x >> (8 * e)) * s;
-        v[4 + e] = (float)(int8_t)(q.y >> (8 * e)) * s;
-    }
+    for (int j = 0; j < 4; ++j) m = max(m, max(mag_bits(v[j].x), mag_bits(v[j].y)));
+#pragma unroll
+    for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(~0u, m, o));
+    if (!c.ok(8 * k)) return;
+    float inv, sc;
+    pack8_factors(__uint_as_float(m), inv, sc);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        w[e / 4] |= (uint32_t)pack8_q(e % 2 ? v[e / 2].y : v[e / 2].x, inv) << (8 * (e % 4));
+    const int col = c.at(8 * k);
+    *reinterpret_cast<uint2*>(h.q + row * D + col) = make_uint2(w[0], w[1]);
+    if (col % 64 == 0) h.scale[row * ((D + 63) / 64) + col / 64] = sc;
 }
 
-// A row of values held in 8 bits, column by column.
-__device__ __forceinline__ void load_packed(const mru_packed8& h, int64_t row, const Cols<false>& c, float (&v)[8])
-{
-    const int8_t* q = h.q + row * c.D;
-    const float* sc = h.scale + row * ((c.D + 63) / 64);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c.ok(e) ? (float)q[c.at(e)] * sc[c.at(e) / 64] : 0.0f;
-}
+// ------------------------------------------------------- rows on their way ---
+//
+// The coming rows' inputs are copied to shared memory asynchronously, 2 to 4
+// rows ahead, so that the memory's latency is covered by rows in flight and
+// not by resident warps (whose registers hold whole rows).  kWide, kExact:
+// every thread copies its own columns and reads them back itself, without a
+// barrier, in pieces of 16 bytes (8 and 4 for 8-bit values and their scale),
+// each piece of all threads side by side.  kSingle: a row, wherever it starts,
+// is copied in the aligned 16-byte pieces that hold it by all threads.
 
-// Rows on their way: every thread copies its own columns of the coming rows
-// into its own slots of shared memory and later reads them back itself, so
-// that no barrier is needed; the memory's latency is covered by the rows in
-// flight, not by resident warps (whose registers hold whole rows).
 template <int BYTES>
-__device__ __forceinline__ void copy_async(void* smem, const void* gmem)
+__device__ __forceinline__ void copy_async(unsigned smem, const void* gmem, int bytes = BYTES)
 {
-    const unsigned s = (unsigned)__cvta_generic_to_shared(smem);
     if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(gmem) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(gmem), "n"(BYTES) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem), "l"(gmem), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -144,95 +193,148 @@ __device__ __forceinline__ void copy_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Bytes of 8 columns of one input in a stage, and stages of `inputs` plain
-// ones and `held` 8-bit ones (with their scales): up to 4 in 160 KB for 512
-// threads.
+// Bytes of a thread's columns in a stage of `plain` inputs and `held` 8-bit
+// ones (with their scales), what a stage has besides (kSingle), and stages: as
+// many as leave an SM its blocks.
 template <typename T>
-constexpr int plane_bytes() { return 8 * (int)sizeof(T); }
-template <typename T>
-constexpr int stage_bytes(int inputs, int held) { return inputs * plane_bytes<T>() + held * 12; }
-template <typename T>
-constexpr int stages_of(int inputs, int held)
+__host__ __device__ constexpr int stage_bytes(int nv, int plain, int held)
 {
-    const int n = 160 * 1024 / (512 * stage_bytes<T>(inputs, held));
+    return nv * (plain * 8 * (int)sizeof(T) + held * 12);
+}
+constexpr int kMargin = 32;                // kSingle: the pieces at a row's two ends
+template <typename T>
+__host__ __device__ constexpr int stages_of(int plain, int held)
+{
+    const int n = (plain == 3 && held == 0 ? 320 : 576) / stage_bytes<T>(2, plain, held);
     return n > 4 ? 4 : n < 2 ? 2 : n;
 }
 
-// A thread's slots of one input: plane `at` (bytes per thread before it).
-template <typename T>
-struct Slot {
-    unsigned char* base;                   // the stage
-    __device__ __forceinline__ unsigned char* piece(int at, int k) const
+// One input of the rows: `at` is where it starts in a stage.
+template <typename T, int NV, Lay LAY>
+struct Feed {
+    const T* next;                         // of the row to copy next, at the CTA's first column
+    const T* now;                          // of the row to read next
+    int64_t jump;                          // to the CTA's next row
+    uintptr_t end;                         // behind the last row
+    __device__ __forceinline__ Feed(const void* base, int64_t row, int64_t step, int64_t ld, int64_t rows, int D, int c0)
+        : next((const T*)base + row * ld + c0), now(next), jump(step * ld),
+          end(reinterpret_cast<uintptr_t>((const T*)base + (rows - 1) * ld + D))
     {
-        return base + (size_t)(at + 16 * k) * blockDim.x + 16 * threadIdx.x;
     }
-    __device__ __forceinline__ void fill(int at, const T* from) const
+    __device__ __forceinline__ void copy(unsigned stage, unsigned at, const Cols<NV, LAY>& c, int cols)
     {
+        if constexpr (LAY != kSingle) {
 #pragma unroll
-        for (int k = 0; k < plane_bytes<T>() / 16; ++k) copy_async<16>(piece(at, k), (const char*)from + 16 * k);
-    }
-    __device__ __forceinline__ void read(int at, float (&v)[8]) const
-    {
-        if constexpr (sizeof(T) == 2) {
-            const uint4 w = *reinterpret_cast<const uint4*>(piece(at, 0));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            for (int k = 0; k < NV; ++k)
+                if (c.ok(8 * k)) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[2 * e] = __uint_as_float(u[e] << 16);
-                v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-            }
+                    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+                        copy_async<16>(stage + at + ((k * (int)sizeof(T) / 2 + i) * blockDim.x + threadIdx.x) * 16,
+                                       (const char*)(next + 8 * k * c.step) + 16 * i);
+                }
         } else {
-            const float4 a = *reinterpret_cast<const float4*>(piece(at, 0));
-            const float4 b = *reinterpret_cast<const float4*>(piece(at, 1));
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+            const uintptr_t first = reinterpret_cast<uintptr_t>(next) & ~(uintptr_t)15;
+            const uintptr_t last = reinterpret_cast<uintptr_t>(next + cols);
+            const int pieces = cols > 0 ? (int)((last - first + 15) / 16) : 0;
+            for (int k = threadIdx.x; k < pieces; k += blockDim.x) {
+                const uintptr_t from = first + 16 * (uintptr_t)k;
+                copy_async<16>(stage + at + 16 * k, (const void*)from, end - from < 16 ? (int)(end - from) : 16);
+            }
+        }
+        next += jump;
+    }
+    // The thread's k-th eight columns of the row to read.
+    __device__ __forceinline__ void read(const unsigned char* stage, unsigned at, const Cols<NV, LAY>& c, int k, F2 (&v)[4]) const
+    {
+        if constexpr (LAY == kSingle) {
+            const T* row = reinterpret_cast<const T*>(stage + at + (reinterpret_cast<uintptr_t>(now) & 15));
+            auto one = [&](int e) { return c.ok(e) ? to_f32(row[threadIdx.x + e * c.step]) : 0.0f; };
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = F2{one(8 * k + 2 * j), one(8 * k + 2 * j + 1)};
+        } else if (!c.ok(8 * k)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = both(0.0f);
+        } else if constexpr (sizeof(T) == 2) {
+            load8(reinterpret_cast<const __nv_bfloat16*>(stage + at + (k * blockDim.x + threadIdx.x) * 16), v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float4 q = *reinterpret_cast<const float4*>(stage + at + ((2 * k + i) * blockDim.x + threadIdx.x) * 16);
+                v[2 * i] = F2{q.x, q.y};
+                v[2 * i + 1] = F2{q.z, q.w};
+            }
         }
     }
-    // 8-bit values: 8 bytes, then the scale
-    __device__ __forceinline__ void fill8(int at, const mru_packed8& h, int64_t row, int c0, int D) const
-    {
-        copy_async<8>(base + (size_t)at * blockDim.x + 8 * threadIdx.x, h.q + row * D + c0);
-        copy_async<4>(base + (size_t)(at + 8) * blockDim.x + 4 * threadIdx.x, h.scale + row * ((D + 63) / 64) + c0 / 64);
-    }
-    __device__ __forceinline__ void read8(int at, float (&v)[8]) const
-    {
-        held8(*reinterpret_cast<const uint2*>(base + (size_t)at * blockDim.x + 8 * threadIdx.x),
-              *reinterpret_cast<const float*>(base + (size_t)(at + 8) * blockDim.x + 4 * threadIdx.x), v);
-    }
+    __device__ __forceinline__ void done() { now += jump; }
 };
 
-// Writes a row's 8-bit copy (VEC: a run of 64 channels is 8 lanes in a row).
-__device__ __forceinline__ void store_packed(const mru_packed8& h, int64_t row, const Cols<true>& c, const float (&v)[8])
-{
-    uint32_t m = 0;
+// The same for values held in 8 bits.
+template <int NV, Lay LAY>
+struct HeldFeed {
+    Feed<int8_t, NV, LAY> q;
+    const float *next, *now;               // scales of the rows
+    int64_t jump;
+    __device__ __forceinline__ HeldFeed(const mru_packed8& h, int64_t row, int64_t step, int64_t rows, int D, int c0)
+        : q(h.q, row, step, D, rows, D, c0), next(h.scale + row * ((D + 63) / 64)), now(next), jump(step * ((D + 63) / 64))
+    {
+    }
+    __device__ __forceinline__ void copy(unsigned stage, unsigned at, const Cols<NV, LAY>& c, int cols)
+    {
+        if constexpr (LAY != kSingle) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, mag_bits(v[e]));
+            for (int k = 0; k < NV; ++k)
+                if (c.ok(8 * k)) {
+                    copy_async<8>(stage + at + (k * blockDim.x + threadIdx.x) * 8, q.next + 8 * k * c.step);
+                    copy_async<4>(stage + at + NV * blockDim.x * 8 + (k * blockDim.x + threadIdx.x) * 4, next + c.at(8 * k) / 64);
+                }
+            q.next += q.jump;
+            next += jump;
+        } else {
+            q.copy(stage, at, c, cols);
+        }
+    }
+    __device__ __forceinline__ void read(const unsigned char* stage, unsigned at, const Cols<NV, LAY>& c, int k, F2 (&v)[4]) const
+    {
+        if constexpr (LAY == kSingle) {
+            const int8_t* row = reinterpret_cast<const int8_t*>(stage + at + (reinterpret_cast<uintptr_t>(q.now) & 15));
+            auto one = [&](int e) { return c.ok(e) ? (float)row[threadIdx.x + e * c.step] * now[c.at(e) / 64] : 0.0f; };
 #pragma unroll
-    for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(~0u, m, o));
-    if (c.c0 >= c.D) return;
-    float inv, sc;
-    pack8_factors(__uint_as_float(m), inv, sc);
-    uint32_t w[2] = {0, 0};
+            for (int j = 0; j < 4; ++j) v[j] = F2{one(8 * k + 2 * j), one(8 * k + 2 * j + 1)};
+        } else if (!c.ok(8 * k)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e / 4] |= (uint32_t)(pack8_q(v[e], inv) & 0xff) << (8 * (e % 4));
-    *reinterpret_cast<uint2*>(h.q + row * c.D + c.c0) = make_uint2(w[0], w[1]);
-    if (c.c0 % 64 == 0) h.scale[row * ((c.D + 63) / 64) + c.c0 / 64] = sc;
-}
+            for (int j = 0; j < 4; ++j) v[j] = both(0.0f);
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(stage + at + (k * blockDim.x + threadIdx.x) * 8);
+            const float s = *reinterpret_cast<const float*>(stage + at + NV * blockDim.x * 8 + (k * blockDim.x + threadIdx.x) * 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t b = (j < 2 ? u.x : u.y) >> (16 * (j % 2));
+                v[j] = F2{(float)(int8_t)b, (float)(int8_t)(b >> 8)} * both(s);
+            }
+        }
+    }
+    __device__ __forceinline__ void done()
+    {
+        q.done();
+        now += jump;
+    }
+};
 
 // Sums over a row's team, the same bits in every thread.  TEAM > 0: lanes of a
 // warp; 0: the CTA, and its cluster where there is one.  Buffers alternate, so
 // that one barrier serves a reduction: a buffer is written again only after
 // the next reduction's barrier, which every reader has reached.
 struct ReduceMem {
-    float4 warp[2][4][4];                  // [sum][warps by fours]; warps that are not there stay 0
-    float4 cta[2][4];                      // [sum], a CTA of the cluster to a component
+    float4 warp[2][4];                     // [sum], a warp to a component; warps that are not there stay 0
+    float4 cta[2][4][2];                   // [sum], a CTA of the cluster to a component; the same
 };
 
-__device__ __forceinline__ void clear(ReduceMem& m)
+__device__ __forceinline__ void clear(ReduceMem& m, int cluster)
 {
     float* f = reinterpret_cast<float*>(&m);
     for (int k = threadIdx.x; k < (int)(sizeof(ReduceMem) / 4); k += blockDim.x) f[k] = 0.0f;
-    __syncthreads();
+    if (cluster > 1) cg::this_cluster().sync();            // before another CTA writes here
+    else __syncthreads();
 }
 
 // N sums of a warp: halves of it take over half of the sums each, so that 4
@@ -271,31 +373,26 @@ __device__ __forceinline__ void team_sum(float (&v)[N], ReduceMem& m, int cluste
     } else {
         const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
         const float r = warp_sums(v, lane);
-        if (lane % (32 / N) == 0) reinterpret_cast<float*>(&m.warp[phase][lane * N / 32][0])[warp] = r;
+        if (lane % (32 / N) == 0) reinterpret_cast<float*>(&m.warp[phase][lane * N / 32])[warp] = r;
         __syncthreads();
-        const int fours = (int)(blockDim.x + 127) / 128;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            float4 q = m.warp[phase][k][0];
-            for (int w = 1; w < fours; ++w) {
-                const float4 t = m.warp[phase][k][w];
-                q = make_float4(q.x + t.x, q.y + t.y, q.z + t.z, q.w + t.w);
-            }
+            const float4 q = m.warp[phase][k];
             v[k] = (q.x + q.y) + (q.z + q.w);
         }
         if (cluster > 1) {
             cg::cluster_group cl = cg::this_cluster();
             const unsigned rank = cl.block_rank();
             if ((int)threadIdx.x < cluster) {
-                float* to = cl.map_shared_rank(reinterpret_cast<float*>(&m.cta[phase][0]), threadIdx.x);
+                float* to = cl.map_shared_rank(reinterpret_cast<float*>(&m.cta[phase][0][0]), threadIdx.x);
 #pragma unroll
-                for (int k = 0; k < N; ++k) to[4 * k + rank] = v[k];
+                for (int k = 0; k < N; ++k) to[8 * k + rank] = v[k];
             }
             cl.sync();
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                const float4 q = m.cta[phase][k];
-                v[k] = (q.x + q.y) + (q.z + q.w);
+                const float4 q = m.cta[phase][k][0], u = m.cta[phase][k][1];
+                v[k] = ((q.x + q.y) + (q.z + q.w)) + ((u.x + u.y) + (u.z + u.w));
             }
         }
         phase ^= 1;
@@ -303,190 +400,207 @@ __device__ __forceinline__ void team_sum(float (&v)[N], ReduceMem& m, int cluste
 }
 
 // g becomes act(g), and da its derivative where it is asked for.
-template <bool DERIVATIVE>
-__device__ __forceinline__ void activation(int act, float (&g)[8], float (&da)[8])
+template <bool DERIVATIVE, int N>
+__device__ __forceinline__ void activation(int act, F2 (&g)[N], F2 (&da)[N])
 {
     if (act == MRU_ACT_SILU) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float c = logit(g[e]);
+        for (int j = 0; j < N; ++j) {
+            const F2 c = {logit(g[j].x), logit(g[j].y)};
             if constexpr (DERIVATIVE) {
-                float s, ns;
+                F2 s, ns;
                 sigmoid2(c, s, ns);
-                da[e] = s * fmaf(c, ns, 1.0f);
-                g[e] = c * s;
+                da[j] = s * fma2(c, ns, both(1.0f));
+                g[j] = c * s;
             } else {
-                g[e] = c * sigmoid(c);
+                g[j] = c * sigmoid(c);
             }
         }
     } else if (act == MRU_ACT_SIGMOID) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float s, ns;
-            sigmoid2(g[e], s, ns);
-            if constexpr (DERIVATIVE) da[e] = s * ns;
-            g[e] = s;
+        for (int j = 0; j < N; ++j) {
+            F2 s, ns;
+            sigmoid2(g[j], s, ns);
+            if constexpr (DERIVATIVE) da[j] = s * ns;
+            g[j] = s;
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            g[e] = 1.0f;
-            if constexpr (DERIVATIVE) da[e] = 0.0f;
+        for (int j = 0; j < N; ++j) {
+            g[j] = both(1.0f);
+            if constexpr (DERIVATIVE) da[j] = both(0.0f);
         }
     }
 }
 
 // v - mean (layer norm) and 1 / sqrt(mean square + eps) of a row.
-template <int TEAM, bool VEC>
-__device__ __forceinline__ float normalise(const BArgs& p, const Cols<VEC>& c, float (&v)[8], ReduceMem& m, int& phase)
+template <int TEAM, int NV, Lay LAY>
+__device__ __forceinline__ float normalise(const BArgs& p, const Cols<NV, LAY>& c, F2 (&v)[NV][4], ReduceMem& m, int& phase)
 {
     const float inv_d = 1.0f / (float)p.D;
-    float s[1];
+    float s[1] = {0.0f};
     if (p.norm == MRU_NORM_LAYER) {
-        s[0] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[0] += v[e];
+        for (int k = 0; k < NV; ++k) s[0] += total(v[k]);
         team_sum<TEAM>(s, m, p.cluster, phase);
-        const float mean = s[0] * inv_d;
+        const F2 mean = both(-s[0] * inv_d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c.ok(e) ? v[e] - mean : 0.0f;
+        for (int k = 0; k < NV; ++k) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[k][j] = v[k][j] + mean;
+            mask(c, k, v[k]);
+        }
+        s[0] = 0.0f;
     }
-    s[0] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s[0] = fmaf(v[e], v[e], s[0]);
+    for (int k = 0; k < NV; ++k) s[0] += dot(v[k], v[k]);
     team_sum<TEAM>(s, m, p.cluster, phase);
     return inv_root(fmaf(s[0], inv_d, p.eps));
 }
 
-// The thread's place: team (row within the CTA's rows) and columns.
-template <int TEAM, bool VEC>
-__device__ __forceinline__ Cols<VEC> place(const BArgs& p, int64_t& row, int64_t& step)
+// The thread's place: team (row within the CTA's rows), columns, and the
+// first column and the number of columns of its CTA.
+template <int TEAM, int NV, Lay LAY>
+__device__ __forceinline__ Cols<NV, LAY> place(const BArgs& p, int64_t& row, int64_t& step, int& first, int& cols)
 {
-    Cols<VEC> c;
+    Cols<NV, LAY> c;
     c.D = p.D;
     if constexpr (TEAM > 0) {
         const int teams = blockDim.x / TEAM;
         row = (int64_t)blockIdx.x * teams + threadIdx.x / TEAM;
         step = (int64_t)gridDim.x * teams;
         c.step = TEAM;
-        c.c0 = (threadIdx.x % TEAM) * (VEC ? 8 : 1);
+        c.c0 = (threadIdx.x % TEAM) * 8;
+        first = 0;
+        cols = p.D;
     } else {
         row = blockIdx.x / p.cluster;
         step = gridDim.x / p.cluster;
         c.step = blockDim.x;
-        c.c0 = (blockIdx.x % p.cluster) * blockDim.x * 8 + threadIdx.x * (VEC ? 8 : 1);
+        first = (blockIdx.x % p.cluster) * blockDim.x * (8 * NV);
+        cols = max(0, min((int)blockDim.x * (8 * NV), p.D - first));
+        c.c0 = first + threadIdx.x * (LAY ? 8 : 1);
     }
     return c;
 }
 
-template <typename T, int TEAM, bool VEC, bool PACK>
-__global__ void __launch_bounds__(TEAM ? 256 : 512, TEAM ? 4 : 2) k_block(BArgs p)
+template <typename T, int TEAM, int NV, Lay LAY, bool PACK>
+__global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs p)
 {
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ ReduceMem mem;
-    constexpr int STAGES = stages_of<T>(3, 0), PLANE = plane_bytes<T>();
-    int phase = 0;
-    if (TEAM == 0) clear(mem);
+    constexpr int STAGES = stages_of<T>(3, 0);
+    int phase = 0, first, cols;
+    if (TEAM == 0) clear(mem, p.cluster);
     int64_t row, step;
-    const Cols<VEC> c = place<TEAM, VEC>(p, row, step);
+    const Cols<NV, LAY> c = place<TEAM, NV, LAY>(p, row, step, first, cols);
     // teams of a warp take their shuffles together: rows past the end go through the motions
     const int64_t last = TEAM ? (p.rows + step - 1) / step * step : p.rows;
     const bool gate = p.has_y && p.act != MRU_ACT_NONE;
-    auto slot = [&](int k) { return Slot<T>{ring + (size_t)k * 3 * PLANE * blockDim.x}; };
-    auto fill = [&](int64_t to, int k) {
-        if (to < p.rows && c.c0 < p.D) {
-            const Slot<T> s = slot(k);
-            s.fill(0, (const T*)p.r + to * p.D + c.c0);
-            if (p.has_y) s.fill(PLANE, (const T*)p.y + to * p.ldy + c.c0);
-            if (gate) s.fill(2 * PLANE, (const T*)p.g + to * p.ldg + c.c0);
+    const unsigned plane = NV * 8 * sizeof(T) * blockDim.x + (LAY ? 0 : kMargin), stage_size = 3 * plane;
+    const unsigned base = (unsigned)__cvta_generic_to_shared(ring);
+    const int start = LAY ? c.c0 : first;
+    Feed<T, NV, LAY> fr(p.r, row, step, p.D, p.rows, p.D, start), fy(p.y, row, step, p.ldy, p.rows, p.D, start),
+        fg(p.g, row, step, p.ldg, p.rows, p.D, start);
+    int64_t coming = row;
+    unsigned to = 0, from = 0;                             // stages to fill and to read next, in bytes
+    auto fill = [&]() {
+        if (coming < p.rows) {
+            fr.copy(base + to, 0, c, cols);
+            if (p.has_y) fy.copy(base + to, plane, c, cols);
+            if (gate) fg.copy(base + to, 2 * plane, c, cols);
         }
+        coming += step;
+        to = to == (STAGES - 1) * stage_size ? 0 : to + stage_size;
         copy_commit();
     };
-    int stage = 0;
-    if constexpr (VEC) {
 #pragma unroll
-        for (int k = 0; k < STAGES - 1; ++k) fill(row + k * step, k);
-    }
+    for (int k = 0; k < STAGES - 1; ++k) fill();
     for (; row < last; row += step) {
         const bool live = row < p.rows;
         const int64_t rr = live ? row : 0;
-        Cols<VEC> cc = c;
-        if (!live) cc.D = 0;
-        const Cols<VEC> pc = live ? c : Cols<VEC>{c.D, c.step, c.D};   // the 8-bit copies' columns
-        float r[8], y[8], g[8];
-        if constexpr (VEC) {
-            fill(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
-            copy_wait<STAGES - 1>();
-            if (cc.c0 < cc.D) {
-                const Slot<T> s = slot(stage);
-                s.read(0, r);
-                if (p.has_y) s.read(PLANE, y);
-                if (gate) s.read(2 * PLANE, g);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) r[e] = y[e] = g[e] = 0.0f;
-            }
-            stage = stage == STAGES - 1 ? 0 : stage + 1;
+        Cols<NV, LAY> cc = c;
+        if (TEAM && !live) cc.D = 0;
+        if constexpr (LAY == kSingle) {
+            copy_wait<STAGES - 2>();
+            __syncthreads();                               // every thread's pieces; the last row's stage is free
+            fill();
         } else {
-            load8<T, VEC>((const T*)p.r + rr * p.D, cc, r);
-            if (p.has_y) load8<T, VEC>((const T*)p.y + rr * p.ldy, cc, y);
-            if (gate) load8<T, VEC>((const T*)p.g + rr * p.ldg, cc, g);
+            fill();
+            copy_wait<STAGES - 1>();
         }
+        const unsigned char* stage = ring + from;
+        from = from == (STAGES - 1) * stage_size ? 0 : from + stage_size;
+        F2 r[NV][4], y[NV][4];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) fr.read(stage, 0, cc, k, r[k]);
         if (p.has_y) {
-            float w[8], b[8];
-            if constexpr (PACK && VEC) {
-                store_packed(p.y8, rr, pc, y);
-                if (gate) store_packed(p.g8, rr, pc, g);
-            }
-            const float rstd = normalise<TEAM, VEC>(p, cc, y, mem, phase);
-            load_param<VEC>(p.prm.w_y, 1.0f, cc, w);
-            load_param<VEC>(p.prm.b_y, 0.0f, cc, b);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e] * rstd, w[e], b[e]);
-            load_param<VEC>(p.prm.s, 1.0f, cc, w);
-            activation<false>(p.act, g, b);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                r[e] = fmaf(p.rs * w[e] * g[e], y[e], r[e]);
-                if (!VEC && !cc.ok(e)) r[e] = 0.0f;
+            for (int k = 0; k < NV; ++k) {
+                fy.read(stage, plane, cc, k, y[k]);
+                if constexpr (PACK && LAY != kSingle) store_packed(p.y8, rr, p.D, cc, k, y[k]);
             }
-            if (VEC && cc.c0 >= cc.D) {
+            const float rstd = normalise<TEAM>(p, cc, y, mem, phase);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) r[e] = 0.0f;
+            for (int k = 0; k < NV; ++k) {
+                F2 w[4], b[4], g[4];
+                load_param(p.prm.w_y, 1.0f, cc, k, w);
+                load_param(p.prm.b_y, 0.0f, cc, k, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[k][j] = fma2(y[k][j] * both(rstd), w[j], b[j]);
+                if (gate) fg.read(stage, 2 * plane, cc, k, g);
+                if constexpr (PACK && LAY != kSingle) {
+                    if (gate) store_packed(p.g8, rr, p.D, cc, k, g);
+                }
+                load_param(p.prm.s, 1.0f, cc, k, w);
+                activation<false>(p.act, g, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[k][j] = fma2(w[j] * both(p.rs) * g[j], y[k][j], r[k][j]);
+                mask(cc, k, r[k]);
+                store_eight((T*)p.r_out + rr * p.D, cc, k, r[k]);
             }
-            store8<T, VEC>((T*)p.r_out + rr * p.D, cc, r);
         }
-        if constexpr (PACK && VEC) {
-            float h[8];
+        fr.done();
+        fy.done();
+        fg.done();
+        if constexpr (PACK && LAY != kSingle) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[e] = to_f32(from_f32<T>(r[e]));
-            store_packed(p.r8, rr, pc, h);
+            for (int k = 0; k < NV; ++k) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[k][j] = F2{to_f32(from_f32<T>(r[k][j].x)), to_f32(from_f32<T>(r[k][j].y))};
+                store_packed(p.r8, rr, p.D, cc, k, y[k]);
+            }
         }
         if (p.has_z) {
-            float w[8], b[8];
-            const float rstd = normalise<TEAM, VEC>(p, cc, r, mem, phase);
-            load_param<VEC>(p.prm.w_z, 1.0f, cc, w);
-            load_param<VEC>(p.prm.b_z, 0.0f, cc, b);
+            const float rstd = normalise<TEAM>(p, cc, r, mem, phase);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[e] = fmaf(r[e] * rstd, w[e], b[e]);
-            store8<T, VEC>((T*)p.z + rr * p.D, cc, r);
+            for (int k = 0; k < NV; ++k) {
+                F2 w[4], b[4];
+                load_param(p.prm.w_z, 1.0f, cc, k, w);
+                load_param(p.prm.b_z, 0.0f, cc, k, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[k][j] = fma2(r[k][j] * both(rstd), w[j], b[j]);
+                store_eight((T*)p.z + rr * p.D, cc, k, r[k]);
+            }
         }
     }
     if (TEAM == 0 && p.cluster > 1) cg::this_cluster().sync();     // peers may still write this CTA's sums
 }
 
 // A CTA's (cluster's) sums over its rows of one parameter's gradient.
-template <int TEAM, bool VEC>
-__device__ __forceinline__ void write_part(const BArgs& p, const Cols<VEC>& c, int which, const float (&acc)[8],
-                                           float* sums)
+template <int TEAM, int NV, Lay LAY>
+__device__ __forceinline__ void write_part(const BArgs& p, const Cols<NV, LAY>& c, int which, const F2 (&acc)[NV][4], float* sums)
 {
     float* to = p.part + ((int64_t)which * p.parts + blockIdx.x / p.cluster) * p.D;
     if constexpr (TEAM > 0) {
+        static_assert(NV == 1, "teams of a warp hold 8 columns to a thread");
         const int teams = blockDim.x / TEAM, cols = TEAM * 8;
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            sums[(threadIdx.x / TEAM) * cols + (threadIdx.x % TEAM) * 8 + e] = acc[e];
+        for (int j = 0; j < 4; ++j) {
+            sums[(threadIdx.x / TEAM) * cols + (threadIdx.x % TEAM) * 8 + 2 * j] = acc[0][j].x;
+            sums[(threadIdx.x / TEAM) * cols + (threadIdx.x % TEAM) * 8 + 2 * j + 1] = acc[0][j].y;
+        }
         __syncthreads();
         for (int k = threadIdx.x; k < cols && k < p.D; k += blockDim.x) {
             float s = 0.0f;
@@ -494,177 +608,211 @@ __device__ __forceinline__ void write_part(const BArgs& p, const Cols<VEC>& c, i
             to[k] = s;
         }
     } else {
-        store8<float, false>(to, Cols<false>{c.c0, VEC ? 1 : c.step, p.D}, acc);
+#pragma unroll
+        for (int e = 0; e < 8 * NV; ++e)
+            if (c.ok(e)) to[c.at(e)] = e % 2 ? acc[e / 8][e % 8 / 2].y : acc[e / 8][e % 8 / 2].x;
     }
 }
 
-// FULL: layer norm, or sums for the biases.
-template <typename T, int TEAM, bool VEC, bool PACKED, bool FULL>
-__global__ void __launch_bounds__(TEAM ? 256 : 512) k_block_bwd(BArgs p)
+// FULL: layer norm, or sums for the biases.  The inputs are read from their
+// stage where they are used, twice where that is cheaper than holding them:
+// only what the second reduction has to wait for stays in registers.
+template <typename T, int TEAM, int NV, Lay LAY, bool PACKED, bool FULL>
+__global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BArgs p)
 {
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ ReduceMem mem;
     __shared__ float sums[TEAM ? 2048 : 1];
-    constexpr int STAGES = stages_of<T>(PACKED ? 2 : 5, PACKED ? 3 : 0), PLANE = plane_bytes<T>();
-    constexpr int STAGE = stage_bytes<T>(PACKED ? 2 : 5, PACKED ? 3 : 0);
-    constexpr int R8 = 2 * PLANE, NEXT = PACKED ? 12 : PLANE;      // planes: dr', dz, r', y, g
-    int phase = 0;
-    if (TEAM == 0) clear(mem);
+    constexpr int PLAIN = PACKED ? 2 : 5, HELD = PACKED ? 3 : 0, STAGES = stages_of<T>(PLAIN, HELD);
+    int phase = 0, first, cols;
+    if (TEAM == 0) clear(mem, p.cluster);
     int64_t row, step;
-    const Cols<VEC> c = place<TEAM, VEC>(p, row, step);
+    const Cols<NV, LAY> c = place<TEAM, NV, LAY>(p, row, step, first, cols);
     const int64_t last = TEAM ? (p.rows + step - 1) / step * step : p.rows;
     const float inv_d = 1.0f / (float)p.D;
-    const bool layer = FULL && p.norm == MRU_NORM_LAYER;
-    float dwy[8], ds[8], dwz[8], dby[8], dbz[8];
+    const bool layer = FULL && p.norm == MRU_NORM_LAYER, gate = p.has_y && p.act != MRU_ACT_NONE;
+    F2 dwy[NV][4], ds[NV][4], dwz[NV][4], dby[FULL ? NV : 1][4], dbz[FULL ? NV : 1][4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dwy[e] = ds[e] = dwz[e] = dby[e] = dbz[e] = 0.0f;
-    const bool gate = p.has_y && p.act != MRU_ACT_NONE;
-    auto slot = [&](int k) { return Slot<T>{ring + (size_t)k * STAGE * blockDim.x}; };
-    auto fill = [&](int64_t to, int k) {
-        if (to < p.rows && c.c0 < p.D) {
-            const Slot<T> s = slot(k);
-            if (p.dro) s.fill(0, (const T*)p.dro + to * p.D + c.c0);
-            if (p.has_z) s.fill(PLANE, (const T*)p.dz + to * p.D + c.c0);
-            if constexpr (PACKED) {
-                if (p.has_z) s.fill8(R8, p.r8, to, c.c0, p.D);
-                if (p.has_y) s.fill8(R8 + NEXT, p.y8, to, c.c0, p.D);
-                if (gate) s.fill8(R8 + 2 * NEXT, p.g8, to, c.c0, p.D);
-            } else {
-                if (p.has_z) s.fill(R8, (const T*)p.r + to * p.D + c.c0);
-                if (p.has_y) s.fill(R8 + NEXT, (const T*)p.y + to * p.ldy + c.c0);
-                if (gate) s.fill(R8 + 2 * NEXT, (const T*)p.g + to * p.ldg + c.c0);
-            }
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            dwy[k][j] = ds[k][j] = dwz[k][j] = both(0.0f);
+            if (FULL) dby[k][j] = dbz[k][j] = both(0.0f);
         }
+    // a stage: dr', dz, then r', y, g
+    const unsigned plane = NV * 8 * sizeof(T) * blockDim.x + (LAY ? 0 : kMargin);
+    const unsigned next = PACKED ? NV * (LAY ? 12 : 8) * blockDim.x + (LAY ? 0 : kMargin) : plane;
+    const unsigned stage_size = 2 * plane + 3 * next, at_r = 2 * plane, at_y = at_r + next, at_g = at_y + next;
+    const unsigned base = (unsigned)__cvta_generic_to_shared(ring);
+    const int start = LAY ? c.c0 : first;
+    using In = typename std::conditional<PACKED, HeldFeed<NV, LAY>, Feed<T, NV, LAY>>::type;
+    Feed<T, NV, LAY> fdr(p.dro, row, step, p.D, p.rows, p.D, start), fdz(p.dz, row, step, p.D, p.rows, p.D, start);
+    auto input = [&](const mru_packed8& h, const void* src, int64_t ld) {
+        if constexpr (PACKED) return In(h, row, step, p.rows, p.D, start);
+        else return In(src, row, step, ld, p.rows, p.D, start);
+    };
+    In fr = input(p.r8, p.r, p.D), fy = input(p.y8, p.y, p.ldy), fg = input(p.g8, p.g, p.ldg);
+    int64_t coming = row;
+    unsigned to = 0, from = 0;
+    auto fill = [&]() {
+        if (coming < p.rows) {
+            if (p.dro) fdr.copy(base + to, 0, c, cols);
+            if (p.has_z) fdz.copy(base + to, plane, c, cols);
+            if (p.has_z) fr.copy(base + to, at_r, c, cols);
+            if (p.has_y) fy.copy(base + to, at_y, c, cols);
+            if (gate) fg.copy(base + to, at_g, c, cols);
+        }
+        coming += step;
+        to = to == (STAGES - 1) * stage_size ? 0 : to + stage_size;
         copy_commit();
     };
-    int stage = 0;
-    if constexpr (VEC) {
 #pragma unroll
-        for (int k = 0; k < STAGES - 1; ++k) fill(row + k * step, k);
-    }
+    for (int k = 0; k < STAGES - 1; ++k) fill();
     for (; row < last; row += step) {
         const bool live = row < p.rows;
         const int64_t rr = live ? row : 0;
-        Cols<VEC> cc = c;
-        if (!live) cc.D = 0;
-        float e_[8], u[8], r[8], y[8], g[8], dz[8], w[8];
-        if constexpr (VEC) {
-            fill(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
-            copy_wait<STAGES - 1>();
-            const Slot<T> s = slot(stage);
-            if (p.dro) s.read(0, e_);
-            if (p.has_z) {
-                s.read(PLANE, dz);
-                if constexpr (PACKED) s.read8(R8, r);
-                else s.read(R8, r);
-            }
-            if (p.has_y) {
-                if constexpr (PACKED) s.read8(R8 + NEXT, y);
-                else s.read(R8 + NEXT, y);
-            }
-            if (gate) {
-                if constexpr (PACKED) s.read8(R8 + 2 * NEXT, g);
-                else s.read(R8 + 2 * NEXT, g);
-            }
-            if (cc.c0 >= cc.D) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) e_[e] = dz[e] = r[e] = y[e] = g[e] = 0.0f;
-            }
-            stage = stage == STAGES - 1 ? 0 : stage + 1;
+        Cols<NV, LAY> cc = c;
+        if (TEAM && !live) cc.D = 0;
+        if constexpr (LAY == kSingle) {
+            copy_wait<STAGES - 2>();
+            __syncthreads();                               // every thread's pieces; the last row's stage is free
+            fill();
         } else {
-            if (p.dro) load8<T, VEC>((const T*)p.dro + rr * p.D, cc, e_);
-            if (p.has_z) {
-                load8<T, VEC>((const T*)p.dz + rr * p.D, cc, dz);
-                if constexpr (PACKED) load_packed(p.r8, rr, cc, r);
-                else load8<T, VEC>((const T*)p.r + rr * p.D, cc, r);
-            }
-            if (p.has_y) {
-                if constexpr (PACKED) load_packed(p.y8, rr, cc, y);
-                else load8<T, VEC>((const T*)p.y + rr * p.ldy, cc, y);
-            }
-            if (gate) {
-                if constexpr (PACKED) load_packed(p.g8, rr, cc, g);
-                else load8<T, VEC>((const T*)p.g + rr * p.ldg, cc, g);
-            }
+            fill();
+            copy_wait<STAGES - 1>();
         }
-        load_param<VEC>(p.prm.w_z, 1.0f, cc, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (!p.dro) e_[e] = 0.0f;
-            if (!p.has_z) dz[e] = r[e] = 0.0f;
-            if (!p.has_y) y[e] = 0.0f;
-            u[e] = dz[e] * w[e];
-        }
+        const unsigned char* stage = ring + from;
+        from = from == (STAGES - 1) * stage_size ? 0 : from + stage_size;
+        float mean_r = 0.0f, mean_y = 0.0f;
         if (layer) {
             float s[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                s[0] += r[e];
-                s[1] += y[e];
+            for (int k = 0; k < NV; ++k) {
+                F2 v[4];
+                if (p.has_z) {
+                    fr.read(stage, at_r, cc, k, v);
+                    s[0] += total(v);
+                }
+                if (p.has_y) {
+                    fy.read(stage, at_y, cc, k, v);
+                    s[1] += total(v);
+                }
             }
             team_sum<TEAM>(s, mem, p.cluster, phase);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                r[e] = cc.ok(e) ? r[e] - s[0] * inv_d : 0.0f;
-                y[e] = cc.ok(e) ? y[e] - s[1] * inv_d : 0.0f;
-            }
+            mean_r = -s[0] * inv_d;
+            mean_y = -s[1] * inv_d;
         }
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};             // r r, u r, y y, u
+        auto centred = [&](const In& f, unsigned at, float mean, int k, F2 (&v)[4]) {
+            f.read(stage, at, cc, k, v);
+            if (layer) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            s[0] = fmaf(r[e], r[e], s[0]);
-            s[1] = fmaf(u[e], r[e], s[1]);
-            s[2] = fmaf(y[e], y[e], s[2]);
-            if (FULL) s[3] += u[e];
+                for (int j = 0; j < 4; ++j) v[j] = v[j] + both(mean);
+                mask(cc, k, v);
+            }
+        };
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};             // r r, u r, y y, u with u = dz w_z
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            F2 r[4], u[4], w[4];
+            if (p.has_y) {
+                centred(fy, at_y, mean_y, k, r);
+                s[2] += dot(r, r);
+            }
+            if (p.has_z) {
+                fdz.read(stage, plane, cc, k, u);
+                centred(fr, at_r, mean_r, k, r);
+                load_param(p.prm.w_z, 1.0f, cc, k, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) u[j] = u[j] * w[j];
+                s[0] += dot(r, r);
+                s[1] += dot(u, r);
+                if (FULL) s[3] += total(u);
+            }
         }
         team_sum<TEAM>(s, mem, p.cluster, phase);
         // a row past the end adds nothing to the sums, whatever eps is
         const float rstd_y = live ? inv_root(fmaf(s[2], inv_d, p.eps)) : 0.0f;
-        if (p.has_z) {
-            const float rstd = live ? inv_root(fmaf(s[0], inv_d, p.eps)) : 0.0f;
-            const float c1 = rstd * s[1] * inv_d, c0 = layer ? s[3] * inv_d : 0.0f;
+        const F2 rstd = both(live ? inv_root(fmaf(s[0], inv_d, p.eps)) : 0.0f);
+        const F2 c1 = both(-rstd.x * s[1] * inv_d), c0 = both(layer ? -s[3] * inv_d : 0.0f);
+        F2 y[NV][4], u[NV][4];                             // N(y) before w_y; dm act(g) w_y
+        float t[2] = {0.0f, 0.0f};                         // u y, u
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float hat = r[e] * rstd;
-                e_[e] = fmaf(rstd, u[e] - c0 - hat * c1, e_[e]);
-                dwz[e] = fmaf(dz[e], hat, dwz[e]);
-                if (FULL) dbz[e] += dz[e];
+        for (int k = 0; k < NV; ++k) {
+            in_turn();
+            F2 e[4], v[4], w[4], n[4], g[4];
+            if (p.dro) {
+                fdr.read(stage, 0, cc, k, e);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) e[j] = both(0.0f);
             }
+            if (p.has_z) {
+                centred(fr, at_r, mean_r, k, v);
+                fdz.read(stage, plane, cc, k, g);
+                load_param(p.prm.w_z, 1.0f, cc, k, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[j] = v[j] * rstd;
+                    F2 d = fma2(v[j], c1, g[j] * w[j]);
+                    if (FULL) d = d + c0;
+                    e[j] = fma2(rstd, d, e[j]);
+                    dwz[k][j] = fma2(g[j], v[j], dwz[k][j]);
+                    if (FULL) dbz[k][j] = dbz[k][j] + g[j];
+                }
+                if (FULL) mask(cc, k, e);
+            }
+            if (p.dr) store_eight((T*)p.dr + rr * p.D, cc, k, e);
+            if (!p.has_y) continue;
+            centred(fy, at_y, mean_y, k, y[k]);
+            load_param(p.prm.w_y, 1.0f, cc, k, w);
+            load_param(p.prm.b_y, 0.0f, cc, k, n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[k][j] = y[k][j] * both(rstd_y);
+                n[j] = fma2(y[k][j], w[j], n[j]);
+            }
+            if (gate) fg.read(stage, at_g, cc, k, g);
+            F2 sc[4];
+            activation<true>(p.act, g, v);                 // v: act'(g)
+            load_param(p.prm.s, 1.0f, cc, k, sc);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const F2 re = e[j] * both(p.rs), dm = re * sc[j], dn = dm * g[j];
+                ds[k][j] = fma2(re * g[j], n[j], ds[k][j]);
+                n[j] = dm * n[j] * v[j];
+                dwy[k][j] = fma2(dn, y[k][j], dwy[k][j]);
+                if (FULL) dby[k][j] = dby[k][j] + dn;
+                u[k][j] = dn * w[j];
+            }
+            if (p.dg) store_eight((T*)p.dg + rr * p.lddg, cc, k, n);
+            t[0] += dot(u[k], y[k]);
+            if (FULL) t[1] += total(u[k]);
         }
-        if (p.dr) store8<T, VEC>((T*)p.dr + rr * p.D, cc, e_);
+        fdr.done();
+        fdz.done();
+        fr.done();
+        fy.done();
+        fg.done();
         if (!p.has_y) continue;
-        float b[8], sc[8];
-        load_param<VEC>(p.prm.w_y, 1.0f, cc, w);
-        load_param<VEC>(p.prm.b_y, 0.0f, cc, b);
-        load_param<VEC>(p.prm.s, 1.0f, cc, sc);
-        float t[2] = {0.0f, 0.0f};                         // q yhat, q
-        activation<true>(p.act, g, dz);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float hat = y[e] * rstd_y, n = fmaf(hat, w[e], b[e]);
-            const float re = !FULL || cc.ok(e) ? p.rs * e_[e] : 0.0f, dm = re * sc[e], dn = dm * g[e];
-            ds[e] = fmaf(re * g[e], n, ds[e]);
-            dwy[e] = fmaf(dn, hat, dwy[e]);
-            if (FULL) dby[e] += dn;
-            g[e] = dm * n * dz[e];
-            u[e] = dn * w[e];
-            y[e] = hat;
-            t[0] = fmaf(u[e], hat, t[0]);
-            if (FULL) t[1] += u[e];
-        }
-        if (p.dg) store8<T, VEC>((T*)p.dg + rr * p.lddg, cc, g);
         team_sum<TEAM>(t, mem, p.cluster, phase);
-        const float t1 = t[0] * inv_d, t0 = layer ? t[1] * inv_d : 0.0f;
+        const F2 t1 = both(-t[0] * inv_d), t0 = both(layer ? -t[1] * inv_d : 0.0f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = rstd_y * (u[e] - t0 - y[e] * t1);
-        store8<T, VEC>((T*)p.dy + rr * p.lddy, cc, u);
+        for (int k = 0; k < NV; ++k) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                u[k][j] = fma2(y[k][j], t1, u[k][j]);
+                if (FULL) u[k][j] = u[k][j] + t0;
+                u[k][j] = u[k][j] * both(rstd_y);
+            }
+            store_eight((T*)p.dy + rr * p.lddy, cc, k, u[k]);
+        }
     }
-    write_part<TEAM, VEC>(p, c, 0, dwy, sums);
-    write_part<TEAM, VEC>(p, c, 1, ds, sums);
-    write_part<TEAM, VEC>(p, c, 2, dwz, sums);
-    if (FULL) {
-        write_part<TEAM, VEC>(p, c, 3, dby, sums);
-        write_part<TEAM, VEC>(p, c, 4, dbz, sums);
+    write_part<TEAM>(p, c, 0, dwy, sums);
+    write_part<TEAM>(p, c, 1, ds, sums);
+    write_part<TEAM>(p, c, 2, dwz, sums);
+    if constexpr (FULL) {
+        write_part<TEAM>(p, c, 3, dby, sums);
+        write_part<TEAM>(p, c, 4, dbz, sums);
     }
     if (TEAM == 0 && p.cluster > 1) cg::this_cluster().sync();
 }
@@ -696,43 +844,54 @@ __global__ void __launch_bounds__(256) k_block_grads(int32_t D, int32_t parts, c
 
 struct Shape {
     int team, cluster, threads;
-    unsigned grid;
+    bool exact;                            // every thread has all of its columns
+    int64_t units;                         // CTAs (clusters) of one row (or team of rows) each
 };
 
 // Teams: 8 lanes up to 64 columns, a warp up to 256, else a CTA of as many
-// warps as the columns need and beyond 4096 columns a cluster of 2 or 4.
-Shape shape_of(int64_t rows, int64_t D, bool vec, int per_sm)
+// warps as the columns need (16 to a thread) and beyond 2048 columns a cluster
+// of 2, 4 or 8.
+Shape shape_of(int64_t rows, int64_t D, bool vec)
 {
     Shape s;
     s.team = !vec ? 0 : D <= 64 ? 8 : D <= 256 ? 32 : 0;
     s.cluster = 1;
-    int64_t units;
     if (s.team) {
         s.threads = 256;
-        units = div_up(rows, 256 / s.team);
+        s.units = div_up(rows, 256 / s.team);
     } else {
         while (s.cluster * kCtaCols < D) s.cluster *= 2;
-        s.threads = (int)(div_up(div_up(D, 8 * s.cluster), 32) * 32);
-        units = rows;
+        s.threads = (int)(div_up(div_up(D, 16 * s.cluster), 32) * 32);
+        s.units = rows;
     }
-    int64_t most = (int64_t)148 * per_sm;
-    if (!s.team) most = most * (512 / s.threads > 4 ? 4 : 512 / s.threads) / s.cluster;
-    s.grid = (unsigned)((units < most ? units : most) * s.cluster);
+    s.exact = !s.team && (int64_t)s.threads * 16 * s.cluster == D;
     return s;
 }
 
-// `per_thread`: bytes of shared memory of a thread's rows on their way.
-template <typename K>
-cudaError_t launch(K kernel, const Shape& sh, const BArgs& p, int per_thread, cudaStream_t s)
+// CTAs (clusters) that stay in the backward, at most: as many rows' sums.
+int64_t most_parts(const Shape& s)
 {
-    const size_t smem = (size_t)per_thread * (size_t)sh.threads;
-    if (smem > 32 * 1024) {                                        // with the static part, beyond the default 48 KB
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const int64_t most = (s.team ? 148 * 2 : 148 * (384 / s.threads)) / s.cluster;
+    return s.units < most ? s.units : most;
+}
+
+// CTAs (clusters) of a kernel that fit the card, found once per device, number
+// of warps and size of cluster.
+struct Fits {
+    std::atomic<int> on[16][9][9];
+};
+
+// `per_thread` bytes of shared memory for a thread's columns of the rows on
+// their way and `extra` besides; most: 0, or as many units at most.  Returns
+// the units launched.
+template <auto KERNEL>
+cudaError_t launch(const Shape& sh, BArgs& p, int per_thread, int extra, int64_t most, cudaStream_t s)
+{
+    static Fits fits;
+    const size_t smem = (size_t)per_thread * (size_t)sh.threads + (size_t)extra;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(sh.grid);
+    cfg.gridDim = dim3((unsigned)sh.cluster);
     cfg.blockDim = dim3((unsigned)sh.threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -743,31 +902,57 @@ cudaError_t launch(K kernel, const Shape& sh, const BArgs& p, int per_thread, cu
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = sh.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    int device = 0, n = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    std::atomic<int>* kept = device < 16 ? &fits.on[device][sh.threads / 32][sh.cluster] : nullptr;
+    if (kept) n = kept->load(std::memory_order_relaxed);
+    if (n == 0) {
+        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+        if (e != cudaSuccess) return e;
+        if (sh.cluster > 1) {
+            e = cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg);
+        } else {
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, sh.threads, smem);
+            n *= 148;
+        }
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        if (kept) kept->store(n, std::memory_order_relaxed);
+    }
+    int64_t units = sh.units < n ? sh.units : n;
+    if (most && units > most) units = most;
+    p.parts = (int32_t)units;
+    cfg.gridDim = dim3((unsigned)(units * sh.cluster));
+    return cudaLaunchKernelEx(&cfg, KERNEL, p);
 }
 
-template <typename T>
-cudaError_t run_forward(const Shape& sh, const BArgs& p, bool vec, bool pack, cudaStream_t s)
+// The column layout's instance: teams of 8 lanes and of a warp, CTAs whose
+// columns may all be there, and the one for rows that cannot be read in
+// aligned pieces of 8 columns.
+template <typename T, bool PACK>
+cudaError_t run_forward(const Shape& sh, BArgs& p, bool vec, cudaStream_t s)
 {
-    constexpr int ring = stages_of<T>(3, 0) * stage_bytes<T>(3, 0);
-    if (!vec) return launch(k_block<T, 0, false, false>, sh, p, 0, s);
-    if (sh.team == 8) return launch(pack ? k_block<T, 8, true, true> : k_block<T, 8, true, false>, sh, p, ring, s);
-    if (sh.team == 32) return launch(pack ? k_block<T, 32, true, true> : k_block<T, 32, true, false>, sh, p, ring, s);
-    return launch(pack ? k_block<T, 0, true, true> : k_block<T, 0, true, false>, sh, p, ring, s);
+    constexpr int n = stages_of<T>(3, 0), one = n * stage_bytes<T>(1, 3, 0), two = n * stage_bytes<T>(2, 3, 0);
+    if (!vec) return launch<k_block<T, 0, 2, kSingle, false>>(sh, p, two, n * 3 * kMargin, 0, s);
+    if (sh.team == 8) return launch<k_block<T, 8, 1, kWide, PACK>>(sh, p, one, 0, 0, s);
+    if (sh.team == 32) return launch<k_block<T, 32, 1, kWide, PACK>>(sh, p, one, 0, 0, s);
+    if (sh.exact) return launch<k_block<T, 0, 2, kExact, PACK>>(sh, p, two, 0, 0, s);
+    return launch<k_block<T, 0, 2, kWide, PACK>>(sh, p, two, 0, 0, s);
 }
 
 template <typename T, bool PACKED, bool FULL>
-cudaError_t run_backward(const Shape& sh, const BArgs& p, bool vec, cudaStream_t s)
+cudaError_t run_backward(const Shape& sh, BArgs& p, bool vec, cudaStream_t s)
 {
-    constexpr int plain = PACKED ? 2 : 5, held = PACKED ? 3 : 0;
-    constexpr int ring = stages_of<T>(plain, held) * stage_bytes<T>(plain, held);
-    if (!vec) return launch(k_block_bwd<T, 0, false, PACKED, FULL>, sh, p, 0, s);
-    if (sh.team == 8) return launch(k_block_bwd<T, 8, true, PACKED, FULL>, sh, p, ring, s);
-    if (sh.team == 32) return launch(k_block_bwd<T, 32, true, PACKED, FULL>, sh, p, ring, s);
-    return launch(k_block_bwd<T, 0, true, PACKED, FULL>, sh, p, ring, s);
+    constexpr int plain = PACKED ? 2 : 5, held = PACKED ? 3 : 0, n = stages_of<T>(plain, held);
+    constexpr int one = n * stage_bytes<T>(1, plain, held), two = n * stage_bytes<T>(2, plain, held);
+    const int64_t most = most_parts(sh);
+    if (!vec) return launch<k_block_bwd<T, 0, 2, kSingle, PACKED, FULL>>(sh, p, two, n * 5 * kMargin, most, s);
+    if (sh.team == 8) return launch<k_block_bwd<T, 8, 1, kWide, PACKED, FULL>>(sh, p, one, 0, most, s);
+    if (sh.team == 32) return launch<k_block_bwd<T, 32, 1, kWide, PACKED, FULL>>(sh, p, one, 0, most, s);
+    if (sh.exact) return launch<k_block_bwd<T, 0, 2, kExact, PACKED, FULL>>(sh, p, two, 0, most, s);
+    return launch<k_block_bwd<T, 0, 2, kWide, PACKED, FULL>>(sh, p, two, 0, most, s);
 }
-
-constexpr int kBwdPerSm = 1, kFwdPerSm = 2;
 
 mru_status check_problem(const mru_block_problem* p)
 {
@@ -850,11 +1035,14 @@ mru_status mru_block_norm(const mru_block_problem* p, const mru_block_params* pr
     a.r = r; a.y = y; a.g = g; a.r_out = r_out; a.z = z;
     a.has_y = has_y; a.has_z = has_z;
     if (saved) { a.r8 = saved->r; a.y8 = saved->y; a.g8 = saved->g; }
-    const Shape sh = shape_of(p->rows, p->D, vec, kFwdPerSm);
+    const Shape sh = shape_of(p->rows, p->D, vec);
     a.cluster = sh.cluster;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = p->dtype == MRU_BF16 ? run_forward<__nv_bfloat16>(sh, a, vec, saved != nullptr, s)
-                                         : run_forward<float>(sh, a, vec, saved != nullptr, s);
+    cudaError_t e;
+    if (p->dtype == MRU_BF16)
+        e = saved ? run_forward<__nv_bfloat16, true>(sh, a, vec, s) : run_forward<__nv_bfloat16, false>(sh, a, vec, s);
+    else
+        e = saved ? run_forward<float, true>(sh, a, vec, s) : run_forward<float, false>(sh, a, vec, s);
     if (e == cudaSuccess && saved && !vec) {
         e = launch_pack8(p->rows, p->D, p->D, p->dtype, has_y ? r_out : r, saved->r, s);
         if (e == cudaSuccess && has_y) e = launch_pack8(p->rows, p->D, a.ldy, p->dtype, y, saved->y, s);
@@ -870,8 +1058,7 @@ size_t mru_block_backward_workspace_size(const mru_block_problem* p)
     // the larger of the two column layouts
     size_t parts = 0;
     for (bool vec : {false, true}) {
-        const Shape sh = shape_of(p->rows, p->D, vec, kBwdPerSm);
-        const size_t n = sh.grid / (size_t)sh.cluster;
+        const size_t n = (size_t)most_parts(shape_of(p->rows, p->D, vec));
         if (n > parts) parts = n;
     }
     return 256 + align256(5 * parts * (size_t)p->D * 4);
@@ -947,9 +1134,8 @@ mru_status mru_block_norm_backward(const mru_block_problem* p, const mru_block_p
     a.dro = dr_out; a.dz = dz; a.dr = dr; a.dy = dy; a.dg = dg;
     a.has_y = has_y; a.has_z = has_z;
     a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + 256);
-    const Shape sh = shape_of(p->rows, p->D, vec, kBwdPerSm);
+    const Shape sh = shape_of(p->rows, p->D, vec);
     a.cluster = sh.cluster;
-    a.parts = (int32_t)(sh.grid / (unsigned)sh.cluster);
     cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(uint32_t), s);
     if (e != cudaSuccess) return MRU_ERR_CUDA;
     const bool full = p->norm == MRU_NORM_LAYER || gr.db_y || gr.db_z, packed = saved != nullptr;

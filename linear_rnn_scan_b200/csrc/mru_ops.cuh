@@ -106,6 +106,44 @@ __device__ __forceinline__ float inv_root(float v)
 }
 constexpr float kLog2e = 1.44269504088896340736f;
 
+// Pairs of floats in the packed fp32 instructions, which take two at the issue
+// cost of one.
+struct alignas(8) F2 {
+    float x, y;
+};
+__device__ __forceinline__ unsigned long long bits(const F2& v)
+{
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
+}
+__device__ __forceinline__ F2 pair(unsigned long long b)
+{
+    F2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 both(float v) { return F2{v, v}; }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return pair(r);
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b)
+{
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return pair(r);
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b)
+{
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return pair(r);
+}
+__device__ __forceinline__ F2 bf16_pair(uint32_t u) { return F2{__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)}; }
+
 // A logit below -80 counts as -80 (s = 2e-35), so that exp(-v) stays finite;
 // NaN stays NaN.
 __device__ __forceinline__ float logit(float v)
@@ -121,6 +159,18 @@ __device__ __forceinline__ void sigmoid2(float v, float& s, float& ns)
     const float e = ex2(-kLog2e * logit(v));
     s = rcp(1.0f + e);
     ns = e * s;
+}
+__device__ __forceinline__ void sigmoid2(F2 v, F2& s, F2& ns)
+{
+    const F2 t = F2{logit(v.x), logit(v.y)} * both(-kLog2e);
+    const F2 e = {ex2(t.x), ex2(t.y)}, d = e + both(1.0f);
+    s = F2{rcp(d.x), rcp(d.y)};
+    ns = e * s;
+}
+__device__ __forceinline__ F2 sigmoid(F2 v)
+{
+    const F2 t = v * both(-kLog2e), d = F2{ex2(t.x), ex2(t.y)} + both(1.0f);
+    return F2{rcp(d.x), rcp(d.y)};
 }
 __device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + ex2(-kLog2e * v)); }
 
