@@ -40,27 +40,31 @@ struct BArgs {
     bool has_y, has_z;
 };
 
-// How a thread's columns lie: NV times 8 in a row (kWide; kExact: every one of
-// them is there), or 8 NV of them a team apart (kSingle).  D counts as 0 for
-// rows past the end.
+// How a thread's columns lie: in pieces of 16 bytes of the rows' type (U = 8 or
+// 4 columns), a team's pieces side by side (kWide; kExact: every one of them
+// is there and the CTA has 128 threads, so that offsets are constants), or one
+// by one (kSingle).  NV eights of columns to a thread; D counts as 0 for rows
+// past the end.
 enum Lay { kSingle, kWide, kExact };
-template <int NV, Lay LAY>
+template <Lay LAY>
+__device__ __forceinline__ unsigned threads() { return LAY == kExact ? 128u : blockDim.x; }
+template <typename T, int NV, Lay LAY>
 struct Cols {
-    int c0, step, D;
-    __device__ __forceinline__ int at(int e) const { return LAY ? c0 + e / 8 * (8 * step) + e % 8 : c0 + e * step; }
+    static constexpr int U = LAY ? 16 / (int)sizeof(T) : 1, N = 8 / U;     // columns of a piece, pieces of an eight
+    int c0, gap, D;
+    __device__ __forceinline__ int step() const { return LAY == kExact ? 128 : gap; }
+    __device__ __forceinline__ int at(int e) const { return c0 + e / U * (U * step()) + e % U; }
     __device__ __forceinline__ bool ok(int e) const { return LAY == kExact || at(e) < D; }
 };
 
-// 8 columns in a row of memory.
-__device__ __forceinline__ void load8(const float* p, F2* v)
+// A piece of a row.
+__device__ __forceinline__ void load_piece(const float* p, F2* v)
 {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    const float4 a = *reinterpret_cast<const float4*>(p);
     v[0] = F2{a.x, a.y};
     v[1] = F2{a.z, a.w};
-    v[2] = F2{b.x, b.y};
-    v[3] = F2{b.z, b.w};
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, F2* v)
+__device__ __forceinline__ void load_piece(const __nv_bfloat16* p, F2* v)
 {
     const uint4 w = *reinterpret_cast<const uint4*>(p);
     v[0] = bf16_pair(w.x);
@@ -68,12 +72,11 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, F2* v)
     v[2] = bf16_pair(w.z);
     v[3] = bf16_pair(w.w);
 }
-__device__ __forceinline__ void store8(float* p, const F2* v)
+__device__ __forceinline__ void store_piece(float* p, const F2* v)
 {
     *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const F2* v)
+__device__ __forceinline__ void store_piece(__nv_bfloat16* p, const F2* v)
 {
     uint32_t u[4];
 #pragma unroll
@@ -84,12 +87,14 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const F2* v)
     *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// 8 of a thread's columns (its k-th eight) from and to a row in memory.
+// The k-th eight of a thread's columns to a row in memory, and of a parameter.
 template <typename T, int NV, Lay LAY>
-__device__ __forceinline__ void store_eight(T* row, const Cols<NV, LAY>& c, int k, const F2 (&v)[4])
+__device__ __forceinline__ void store_eight(T* row, const Cols<T, NV, LAY>& c, int k, const F2 (&v)[4])
 {
     if constexpr (LAY != kSingle) {
-        if (c.ok(8 * k)) store8(row + c.at(8 * k), v);
+#pragma unroll
+        for (int i = 0; i < c.N; ++i)
+            if (c.ok(8 * k + i * c.U)) store_piece(row + c.at(8 * k + i * c.U), v + i * c.U / 2);
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -98,37 +103,42 @@ __device__ __forceinline__ void store_eight(T* row, const Cols<NV, LAY>& c, int 
         }
     }
 }
-template <int NV, Lay LAY>
-__device__ __forceinline__ void load_param(const float* p, float none, const Cols<NV, LAY>& c, int k, F2 (&v)[4])
+template <typename T, int NV, Lay LAY>
+__device__ __forceinline__ void load_param(const float* p, float none, const Cols<T, NV, LAY>& c, int k, F2 (&v)[4])
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = both(none);
     if (!p) return;
     if constexpr (LAY != kSingle) {
-        if (c.ok(8 * k)) load8(p + c.at(8 * k), v);
-    } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (c.ok(8 * k + 2 * j)) v[j].x = p[c.at(8 * k + 2 * j)];
-            if (c.ok(8 * k + 2 * j + 1)) v[j].y = p[c.at(8 * k + 2 * j + 1)];
-        }
+        for (int i = 0; i < c.N; ++i)
+            if (c.ok(8 * k + i * c.U)) {
+#pragma unroll
+                for (int h = 0; h < c.U / 4; ++h)
+                    load_piece(p + (unsigned)(c.at(8 * k + i * c.U) + 4 * h), v + (i * c.U + 4 * h) / 2);
+            }
+    } else {
+        // without a branch to a load: a column that is not there reads the last one
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = F2{p[min(c.at(8 * k + 2 * j), c.D - 1)], p[min(c.at(8 * k + 2 * j + 1), c.D - 1)]};
     }
 }
 // Columns that are not there become zero.
-template <int NV, Lay LAY>
-__device__ __forceinline__ void mask(const Cols<NV, LAY>& c, int k, F2 (&v)[4])
+template <typename T, int NV, Lay LAY>
+__device__ __forceinline__ void mask(const Cols<T, NV, LAY>& c, int k, F2 (&v)[4])
 {
     if constexpr (LAY == kWide) {
-        if (!c.ok(8 * k)) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = both(0.0f);
-        }
+        for (int i = 0; i < c.N; ++i)
+            if (!c.ok(8 * k + i * c.U)) {
+#pragma unroll
+                for (int j = 0; j < c.U / 2; ++j) v[i * c.U / 2 + j] = both(0.0f);
+            }
     } else if constexpr (LAY == kSingle) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (!c.ok(8 * k + 2 * j)) v[j].x = 0.0f;
-            if (!c.ok(8 * k + 2 * j + 1)) v[j].y = 0.0f;
-        }
+        for (int j = 0; j < 4; ++j)
+            v[j] = F2{c.ok(8 * k + 2 * j) ? v[j].x : 0.0f, c.ok(8 * k + 2 * j + 1) ? v[j].y : 0.0f};
     }
 }
 __device__ __forceinline__ float total(const F2 (&v)[4])
@@ -145,27 +155,42 @@ __device__ __forceinline__ float dot(const F2 (&a)[4], const F2 (&b)[4])
 // second, so that their inputs are not all in registers at once.
 __device__ __forceinline__ void in_turn() { asm volatile("" ::: "memory"); }
 
-// Writes a row's 8-bit copy (a run of 64 channels is 8 lanes in a row).  The
+// Writes a row's 8-bit copy.  A run of 64 channels is a piece of 64 / U lanes
+// in a row, or (TEAM 8 with pieces of 4) both pieces of its 8 lanes.  The
 // pitch is `D`; columns that are not there are zero in v and not written.
-template <int NV, Lay LAY>
-__device__ __forceinline__ void store_packed(const mru_packed8& h, int64_t row, int D, const Cols<NV, LAY>& c, int k,
+template <int TEAM, typename T, int NV, Lay LAY>
+__device__ __forceinline__ void store_packed(const mru_packed8& h, int64_t row, int D, const Cols<T, NV, LAY>& c, int k,
                                              const F2 (&v)[4])
 {
-    uint32_t m = 0;
+    constexpr int U = c.U, N = c.N;
+    constexpr bool JOIN = TEAM * U == 32;
+    uint32_t m[N];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m = max(m, max(mag_bits(v[j].x), mag_bits(v[j].y)));
+    for (int i = 0; i < N; ++i) {
+        m[i] = 0;
 #pragma unroll
-    for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(~0u, m, o));
-    if (!c.ok(8 * k)) return;
-    float inv, sc;
-    pack8_factors(__uint_as_float(m), inv, sc);
-    uint32_t w[2] = {0, 0};
+        for (int j = 0; j < U / 2; ++j)
+            m[i] = max(m[i], max(mag_bits(v[i * U / 2 + j].x), mag_bits(v[i * U / 2 + j].y)));
+    }
+    if (JOIN) m[0] = m[N - 1] = max(m[0], m[N - 1]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        w[e / 4] |= (uint32_t)pack8_q(e % 2 ? v[e / 2].y : v[e / 2].x, inv) << (8 * (e % 4));
-    const int col = c.at(8 * k);
-    *reinterpret_cast<uint2*>(h.q + row * D + col) = make_uint2(w[0], w[1]);
-    if (col % 64 == 0) h.scale[row * ((D + 63) / 64) + col / 64] = sc;
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int o = (JOIN ? 8 : 64 / U) / 2; o; o >>= 1) m[i] = max(m[i], __shfl_xor_sync(~0u, m[i], o));
+        if (!c.ok(8 * k + i * U)) continue;
+        float inv, sc;
+        pack8_factors(__uint_as_float(m[i]), inv, sc);
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+            const F2& f = v[(i * U + e) / 2];
+            w[e / 4] |= (uint32_t)pack8_q(e % 2 ? f.y : f.x, inv) << (8 * (e % 4));
+        }
+        const int col = c.at(8 * k + i * U);
+        if constexpr (U == 8) *reinterpret_cast<uint2*>(h.q + row * D + col) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(h.q + row * D + col) = w[0];
+        if (col % 64 == 0) h.scale[row * ((D + 63) / 64) + col / 64] = sc;
+    }
 }
 
 // ------------------------------------------------------- rows on their way ---
@@ -174,9 +199,9 @@ __device__ __forceinline__ void store_packed(const mru_packed8& h, int64_t row, 
 // rows ahead, so that the memory's latency is covered by rows in flight and
 // not by resident warps (whose registers hold whole rows).  kWide, kExact:
 // every thread copies its own columns and reads them back itself, without a
-// barrier, in pieces of 16 bytes (8 and 4 for 8-bit values and their scale),
-// each piece of all threads side by side.  kSingle: a row, wherever it starts,
-// is copied in the aligned 16-byte pieces that hold it by all threads.
+// barrier, each piece of all threads side by side (of 8-bit values too, then
+// their scales).  kSingle: a row, wherever it starts, is copied in the aligned
+// 16-byte pieces that hold it by all threads.
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(unsigned smem, const void* gmem, int bytes = BYTES)
@@ -194,12 +219,14 @@ __device__ __forceinline__ void copy_wait()
 }
 
 // Bytes of a thread's columns in a stage of `plain` inputs and `held` 8-bit
-// ones (with their scales), what a stage has besides (kSingle), and stages: as
-// many as leave an SM its blocks.
+// ones (with a scale to each piece), what a stage has besides (kSingle), and
+// stages: as many as leave an SM its blocks.
+template <typename T>
+__host__ __device__ constexpr int held_bytes() { return 8 + 2 * (int)sizeof(T); }
 template <typename T>
 __host__ __device__ constexpr int stage_bytes(int nv, int plain, int held)
 {
-    return nv * (plain * 8 * (int)sizeof(T) + held * 12);
+    return nv * (plain * 8 * (int)sizeof(T) + held * held_bytes<T>());
 }
 constexpr int kMargin = 32;                // kSingle: the pieces at a row's two ends
 template <typename T>
@@ -209,59 +236,60 @@ __host__ __device__ constexpr int stages_of(int plain, int held)
     return n > 4 ? 4 : n < 2 ? 2 : n;
 }
 
-// One input of the rows: `at` is where it starts in a stage.
-template <typename T, int NV, Lay LAY>
+// One input of the rows.  V: its type in memory; T: the type whose pieces the
+// columns lie in.
+template <typename V, typename T, int NV, Lay LAY>
 struct Feed {
-    const T* next;                         // of the row to copy next, at the CTA's first column
-    const T* now;                          // of the row to read next
+    const V* next;                         // of the row to copy next, at the thread's (kSingle: the CTA's) first column
+    const V* now;                          // of the row to read next
     int64_t jump;                          // to the CTA's next row
     uintptr_t end;                         // behind the last row
     __device__ __forceinline__ Feed(const void* base, int64_t row, int64_t step, int64_t ld, int64_t rows, int D, int c0)
-        : next((const T*)base + row * ld + c0), now(next), jump(step * ld),
-          end(reinterpret_cast<uintptr_t>((const T*)base + (rows - 1) * ld + D))
+        : next((const V*)base + row * ld + c0), now(next), jump(step * ld),
+          end(reinterpret_cast<uintptr_t>((const V*)base + (rows - 1) * ld + D))
     {
     }
-    __device__ __forceinline__ void copy(unsigned stage, unsigned at, const Cols<NV, LAY>& c, int cols)
+    __device__ __forceinline__ void copy(unsigned stage, const Cols<T, NV, LAY>& c, int cols)
     {
+        constexpr int U = c.U, BYTES = U * (int)sizeof(V);
         if constexpr (LAY != kSingle) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-                if (c.ok(8 * k)) {
-#pragma unroll
-                    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-                        copy_async<16>(stage + at + ((k * (int)sizeof(T) / 2 + i) * blockDim.x + threadIdx.x) * 16,
-                                       (const char*)(next + 8 * k * c.step) + 16 * i);
-                }
+            for (int i = 0; i < NV * c.N; ++i)
+                if (c.ok(i * U)) copy_async<BYTES>(stage + (i * threads<LAY>() + threadIdx.x) * BYTES, next + i * U * c.step());
         } else {
             const uintptr_t first = reinterpret_cast<uintptr_t>(next) & ~(uintptr_t)15;
             const uintptr_t last = reinterpret_cast<uintptr_t>(next + cols);
             const int pieces = cols > 0 ? (int)((last - first + 15) / 16) : 0;
             for (int k = threadIdx.x; k < pieces; k += blockDim.x) {
                 const uintptr_t from = first + 16 * (uintptr_t)k;
-                copy_async<16>(stage + at + 16 * k, (const void*)from, end - from < 16 ? (int)(end - from) : 16);
+                copy_async<16>(stage + 16 * k, (const void*)from, end - from < 16 ? (int)(end - from) : 16);
             }
         }
         next += jump;
     }
+    // kSingle: the thread's e-th column of the row to read.
+    __device__ __forceinline__ float one(const unsigned char* stage, const Cols<T, NV, LAY>& c, int e) const
+    {
+        const V* row = reinterpret_cast<const V*>(stage + (reinterpret_cast<uintptr_t>(now) & 15));
+        if constexpr (sizeof(V) == 1) return (float)row[threadIdx.x + e * c.step()];
+        else return to_f32(row[threadIdx.x + e * c.step()]);
+    }
     // The thread's k-th eight columns of the row to read.
-    __device__ __forceinline__ void read(const unsigned char* stage, unsigned at, const Cols<NV, LAY>& c, int k, F2 (&v)[4]) const
+    __device__ __forceinline__ void read(const unsigned char* stage, const Cols<T, NV, LAY>& c, int k, F2 (&v)[4]) const
     {
         if constexpr (LAY == kSingle) {
-            const T* row = reinterpret_cast<const T*>(stage + at + (reinterpret_cast<uintptr_t>(now) & 15));
-            auto one = [&](int e) { return c.ok(e) ? to_f32(row[threadIdx.x + e * c.step]) : 0.0f; };
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = F2{one(8 * k + 2 * j), one(8 * k + 2 * j + 1)};
-        } else if (!c.ok(8 * k)) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = both(0.0f);
-        } else if constexpr (sizeof(T) == 2) {
-            load8(reinterpret_cast<const __nv_bfloat16*>(stage + at + (k * blockDim.x + threadIdx.x) * 16), v);
+            for (int j = 0; j < 4; ++j) v[j] = F2{one(stage, c, 8 * k + 2 * j), one(stage, c, 8 * k + 2 * j + 1)};
+            mask(c, k, v);
         } else {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4 q = *reinterpret_cast<const float4*>(stage + at + ((2 * k + i) * blockDim.x + threadIdx.x) * 16);
-                v[2 * i] = F2{q.x, q.y};
-                v[2 * i + 1] = F2{q.z, q.w};
+            for (int i = 0; i < c.N; ++i) {
+                if (c.ok(8 * k + i * c.U)) {
+                    load_piece(reinterpret_cast<const V*>(stage + ((k * c.N + i) * threads<LAY>() + threadIdx.x) * 16), v + i * c.U / 2);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < c.U / 2; ++j) v[i * c.U / 2 + j] = both(0.0f);
+                }
             }
         }
     }
@@ -269,47 +297,51 @@ struct Feed {
 };
 
 // The same for values held in 8 bits.
-template <int NV, Lay LAY>
+template <typename T, int NV, Lay LAY>
 struct HeldFeed {
-    Feed<int8_t, NV, LAY> q;
+    Feed<int8_t, T, NV, LAY> q;
     const float *next, *now;               // scales of the rows
     int64_t jump;
     __device__ __forceinline__ HeldFeed(const mru_packed8& h, int64_t row, int64_t step, int64_t rows, int D, int c0)
         : q(h.q, row, step, D, rows, D, c0), next(h.scale + row * ((D + 63) / 64)), now(next), jump(step * ((D + 63) / 64))
     {
     }
-    __device__ __forceinline__ void copy(unsigned stage, unsigned at, const Cols<NV, LAY>& c, int cols)
+    __device__ __forceinline__ void copy(unsigned stage, const Cols<T, NV, LAY>& c, int cols)
     {
+        q.copy(stage, c, cols);
         if constexpr (LAY != kSingle) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-                if (c.ok(8 * k)) {
-                    copy_async<8>(stage + at + (k * blockDim.x + threadIdx.x) * 8, q.next + 8 * k * c.step);
-                    copy_async<4>(stage + at + NV * blockDim.x * 8 + (k * blockDim.x + threadIdx.x) * 4, next + c.at(8 * k) / 64);
-                }
-            q.next += q.jump;
+            for (int i = 0; i < NV * c.N; ++i)
+                if (c.ok(i * c.U))
+                    copy_async<4>(stage + NV * threads<LAY>() * 8 + (i * threads<LAY>() + threadIdx.x) * 4,
+                                  next + c.at(i * c.U) / 64);
             next += jump;
-        } else {
-            q.copy(stage, at, c, cols);
         }
     }
-    __device__ __forceinline__ void read(const unsigned char* stage, unsigned at, const Cols<NV, LAY>& c, int k, F2 (&v)[4]) const
+    __device__ __forceinline__ void read(const unsigned char* stage, const Cols<T, NV, LAY>& c, int k, F2 (&v)[4]) const
     {
         if constexpr (LAY == kSingle) {
-            const int8_t* row = reinterpret_cast<const int8_t*>(stage + at + (reinterpret_cast<uintptr_t>(q.now) & 15));
-            auto one = [&](int e) { return c.ok(e) ? (float)row[threadIdx.x + e * c.step] * now[c.at(e) / 64] : 0.0f; };
+            auto one = [&](int e) { return q.one(stage, c, e) * now[min(c.at(e), c.D - 1) / 64]; };
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = F2{one(8 * k + 2 * j), one(8 * k + 2 * j + 1)};
-        } else if (!c.ok(8 * k)) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = both(0.0f);
+            mask(c, k, v);
         } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(stage + at + (k * blockDim.x + threadIdx.x) * 8);
-            const float s = *reinterpret_cast<const float*>(stage + at + NV * blockDim.x * 8 + (k * blockDim.x + threadIdx.x) * 4);
+            constexpr int U = c.U;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t b = (j < 2 ? u.x : u.y) >> (16 * (j % 2));
-                v[j] = F2{(float)(int8_t)b, (float)(int8_t)(b >> 8)} * both(s);
+            for (int i = 0; i < c.N; ++i) {
+                const unsigned at = (k * c.N + i) * threads<LAY>() + threadIdx.x;
+                uint2 u = make_uint2(0, 0);
+                float s = 0.0f;
+                if (c.ok(8 * k + i * U)) {
+                    if constexpr (U == 8) u = *reinterpret_cast<const uint2*>(stage + at * 8);
+                    else u.x = *reinterpret_cast<const uint32_t*>(stage + at * 4);
+                    s = *reinterpret_cast<const float*>(stage + NV * threads<LAY>() * 8 + at * 4);
+                }
+#pragma unroll
+                for (int j = 0; j < U / 2; ++j) {
+                    const uint32_t b = (j < 2 ? u.x : u.y) >> (16 * (j % 2));
+                    v[i * U / 2 + j] = F2{(float)(int8_t)b, (float)(int8_t)(b >> 8)} * both(s);
+                }
             }
         }
     }
@@ -434,8 +466,8 @@ __device__ __forceinline__ void activation(int act, F2 (&g)[N], F2 (&da)[N])
 }
 
 // v - mean (layer norm) and 1 / sqrt(mean square + eps) of a row.
-template <int TEAM, int NV, Lay LAY>
-__device__ __forceinline__ float normalise(const BArgs& p, const Cols<NV, LAY>& c, F2 (&v)[NV][4], ReduceMem& m, int& phase)
+template <int TEAM, typename T, int NV, Lay LAY>
+__device__ __forceinline__ float normalise(const BArgs& p, const Cols<T, NV, LAY>& c, F2 (&v)[NV][4], ReduceMem& m, int& phase)
 {
     const float inv_d = 1.0f / (float)p.D;
     float s[1] = {0.0f};
@@ -460,26 +492,26 @@ __device__ __forceinline__ float normalise(const BArgs& p, const Cols<NV, LAY>& 
 
 // The thread's place: team (row within the CTA's rows), columns, and the
 // first column and the number of columns of its CTA.
-template <int TEAM, int NV, Lay LAY>
-__device__ __forceinline__ Cols<NV, LAY> place(const BArgs& p, int64_t& row, int64_t& step, int& first, int& cols)
+template <int TEAM, typename T, int NV, Lay LAY>
+__device__ __forceinline__ Cols<T, NV, LAY> place(const BArgs& p, int64_t& row, int64_t& step, int& first, int& cols)
 {
-    Cols<NV, LAY> c;
+    Cols<T, NV, LAY> c;
     c.D = p.D;
     if constexpr (TEAM > 0) {
         const int teams = blockDim.x / TEAM;
         row = (int64_t)blockIdx.x * teams + threadIdx.x / TEAM;
         step = (int64_t)gridDim.x * teams;
-        c.step = TEAM;
-        c.c0 = (threadIdx.x % TEAM) * 8;
+        c.gap = TEAM;
+        c.c0 = (threadIdx.x % TEAM) * c.U;
         first = 0;
         cols = p.D;
     } else {
         row = blockIdx.x / p.cluster;
         step = gridDim.x / p.cluster;
-        c.step = blockDim.x;
-        first = (blockIdx.x % p.cluster) * blockDim.x * (8 * NV);
-        cols = max(0, min((int)blockDim.x * (8 * NV), p.D - first));
-        c.c0 = first + threadIdx.x * (LAY ? 8 : 1);
+        c.gap = blockDim.x;
+        first = (blockIdx.x % p.cluster) * threads<LAY>() * (8 * NV);
+        cols = max(0, min((int)threads<LAY>() * (8 * NV), p.D - first));
+        c.c0 = first + threadIdx.x * c.U;
     }
     return c;
 }
@@ -493,22 +525,22 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
     int phase = 0, first, cols;
     if (TEAM == 0) clear(mem, p.cluster);
     int64_t row, step;
-    const Cols<NV, LAY> c = place<TEAM, NV, LAY>(p, row, step, first, cols);
+    const Cols<T, NV, LAY> c = place<TEAM, T, NV, LAY>(p, row, step, first, cols);
     // teams of a warp take their shuffles together: rows past the end go through the motions
     const int64_t last = TEAM ? (p.rows + step - 1) / step * step : p.rows;
     const bool gate = p.has_y && p.act != MRU_ACT_NONE;
-    const unsigned plane = NV * 8 * sizeof(T) * blockDim.x + (LAY ? 0 : kMargin), stage_size = 3 * plane;
+    const unsigned plane = NV * 8 * sizeof(T) * threads<LAY>() + (LAY ? 0 : kMargin), stage_size = 3 * plane;
     const unsigned base = (unsigned)__cvta_generic_to_shared(ring);
     const int start = LAY ? c.c0 : first;
-    Feed<T, NV, LAY> fr(p.r, row, step, p.D, p.rows, p.D, start), fy(p.y, row, step, p.ldy, p.rows, p.D, start),
+    Feed<T, T, NV, LAY> fr(p.r, row, step, p.D, p.rows, p.D, start), fy(p.y, row, step, p.ldy, p.rows, p.D, start),
         fg(p.g, row, step, p.ldg, p.rows, p.D, start);
     int64_t coming = row;
     unsigned to = 0, from = 0;                             // stages to fill and to read next, in bytes
     auto fill = [&]() {
         if (coming < p.rows) {
-            fr.copy(base + to, 0, c, cols);
-            if (p.has_y) fy.copy(base + to, plane, c, cols);
-            if (gate) fg.copy(base + to, 2 * plane, c, cols);
+            fr.copy(base + to, c, cols);
+            if (p.has_y) fy.copy(base + to + plane, c, cols);
+            if (gate) fg.copy(base + to + 2 * plane, c, cols);
         }
         coming += step;
         to = to == (STAGES - 1) * stage_size ? 0 : to + stage_size;
@@ -518,8 +550,8 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
     for (int k = 0; k < STAGES - 1; ++k) fill();
     for (; row < last; row += step) {
         const bool live = row < p.rows;
-        const int64_t rr = live ? row : 0;
-        Cols<NV, LAY> cc = c;
+        const int64_t rr = live ? row : 0, here = rr * p.D;
+        Cols<T, NV, LAY> cc = c;
         if (TEAM && !live) cc.D = 0;
         if constexpr (LAY == kSingle) {
             copy_wait<STAGES - 2>();
@@ -533,12 +565,12 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
         from = from == (STAGES - 1) * stage_size ? 0 : from + stage_size;
         F2 r[NV][4], y[NV][4];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) fr.read(stage, 0, cc, k, r[k]);
+        for (int k = 0; k < NV; ++k) fr.read(stage, cc, k, r[k]);
         if (p.has_y) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                fy.read(stage, plane, cc, k, y[k]);
-                if constexpr (PACK && LAY != kSingle) store_packed(p.y8, rr, p.D, cc, k, y[k]);
+                fy.read(stage + plane, cc, k, y[k]);
+                if constexpr (PACK && LAY != kSingle) store_packed<TEAM>(p.y8, rr, p.D, cc, k, y[k]);
             }
             const float rstd = normalise<TEAM>(p, cc, y, mem, phase);
 #pragma unroll
@@ -548,16 +580,16 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
                 load_param(p.prm.b_y, 0.0f, cc, k, b);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) y[k][j] = fma2(y[k][j] * both(rstd), w[j], b[j]);
-                if (gate) fg.read(stage, 2 * plane, cc, k, g);
+                if (gate) fg.read(stage + 2 * plane, cc, k, g);
                 if constexpr (PACK && LAY != kSingle) {
-                    if (gate) store_packed(p.g8, rr, p.D, cc, k, g);
+                    if (gate) store_packed<TEAM>(p.g8, rr, p.D, cc, k, g);
                 }
                 load_param(p.prm.s, 1.0f, cc, k, w);
                 activation<false>(p.act, g, b);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) r[k][j] = fma2(w[j] * both(p.rs) * g[j], y[k][j], r[k][j]);
                 mask(cc, k, r[k]);
-                store_eight((T*)p.r_out + rr * p.D, cc, k, r[k]);
+                store_eight((T*)p.r_out + here, cc, k, r[k]);
             }
         }
         fr.done();
@@ -568,7 +600,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
             for (int k = 0; k < NV; ++k) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) y[k][j] = F2{to_f32(from_f32<T>(r[k][j].x)), to_f32(from_f32<T>(r[k][j].y))};
-                store_packed(p.r8, rr, p.D, cc, k, y[k]);
+                store_packed<TEAM>(p.r8, rr, p.D, cc, k, y[k]);
             }
         }
         if (p.has_z) {
@@ -580,7 +612,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
                 load_param(p.prm.b_z, 0.0f, cc, k, b);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) r[k][j] = fma2(r[k][j] * both(rstd), w[j], b[j]);
-                store_eight((T*)p.z + rr * p.D, cc, k, r[k]);
+                store_eight((T*)p.z + here, cc, k, r[k]);
             }
         }
     }
@@ -588,8 +620,8 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
 }
 
 // A CTA's (cluster's) sums over its rows of one parameter's gradient.
-template <int TEAM, int NV, Lay LAY>
-__device__ __forceinline__ void write_part(const BArgs& p, const Cols<NV, LAY>& c, int which, const F2 (&acc)[NV][4], float* sums)
+template <int TEAM, typename T, int NV, Lay LAY>
+__device__ __forceinline__ void write_part(const BArgs& p, const Cols<T, NV, LAY>& c, int which, const F2 (&acc)[NV][4], float* sums)
 {
     float* to = p.part + ((int64_t)which * p.parts + blockIdx.x / p.cluster) * p.D;
     if constexpr (TEAM > 0) {
@@ -598,8 +630,8 @@ __device__ __forceinline__ void write_part(const BArgs& p, const Cols<NV, LAY>& 
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            sums[(threadIdx.x / TEAM) * cols + (threadIdx.x % TEAM) * 8 + 2 * j] = acc[0][j].x;
-            sums[(threadIdx.x / TEAM) * cols + (threadIdx.x % TEAM) * 8 + 2 * j + 1] = acc[0][j].y;
+            sums[(threadIdx.x / TEAM) * cols + c.at(2 * j)] = acc[0][j].x;
+            sums[(threadIdx.x / TEAM) * cols + c.at(2 * j + 1)] = acc[0][j].y;
         }
         __syncthreads();
         for (int k = threadIdx.x; k < cols && k < p.D; k += blockDim.x) {
@@ -627,7 +659,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
     int phase = 0, first, cols;
     if (TEAM == 0) clear(mem, p.cluster);
     int64_t row, step;
-    const Cols<NV, LAY> c = place<TEAM, NV, LAY>(p, row, step, first, cols);
+    const Cols<T, NV, LAY> c = place<TEAM, T, NV, LAY>(p, row, step, first, cols);
     const int64_t last = TEAM ? (p.rows + step - 1) / step * step : p.rows;
     const float inv_d = 1.0f / (float)p.D;
     const bool layer = FULL && p.norm == MRU_NORM_LAYER, gate = p.has_y && p.act != MRU_ACT_NONE;
@@ -640,13 +672,13 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             if (FULL) dby[k][j] = dbz[k][j] = both(0.0f);
         }
     // a stage: dr', dz, then r', y, g
-    const unsigned plane = NV * 8 * sizeof(T) * blockDim.x + (LAY ? 0 : kMargin);
-    const unsigned next = PACKED ? NV * (LAY ? 12 : 8) * blockDim.x + (LAY ? 0 : kMargin) : plane;
+    const unsigned plane = NV * 8 * sizeof(T) * threads<LAY>() + (LAY ? 0 : kMargin);
+    const unsigned next = PACKED ? NV * (LAY ? held_bytes<T>() : 8) * threads<LAY>() + (LAY ? 0 : kMargin) : plane;
     const unsigned stage_size = 2 * plane + 3 * next, at_r = 2 * plane, at_y = at_r + next, at_g = at_y + next;
     const unsigned base = (unsigned)__cvta_generic_to_shared(ring);
     const int start = LAY ? c.c0 : first;
-    using In = typename std::conditional<PACKED, HeldFeed<NV, LAY>, Feed<T, NV, LAY>>::type;
-    Feed<T, NV, LAY> fdr(p.dro, row, step, p.D, p.rows, p.D, start), fdz(p.dz, row, step, p.D, p.rows, p.D, start);
+    using In = typename std::conditional<PACKED, HeldFeed<T, NV, LAY>, Feed<T, T, NV, LAY>>::type;
+    Feed<T, T, NV, LAY> fdr(p.dro, row, step, p.D, p.rows, p.D, start), fdz(p.dz, row, step, p.D, p.rows, p.D, start);
     auto input = [&](const mru_packed8& h, const void* src, int64_t ld) {
         if constexpr (PACKED) return In(h, row, step, p.rows, p.D, start);
         else return In(src, row, step, ld, p.rows, p.D, start);
@@ -656,11 +688,11 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
     unsigned to = 0, from = 0;
     auto fill = [&]() {
         if (coming < p.rows) {
-            if (p.dro) fdr.copy(base + to, 0, c, cols);
-            if (p.has_z) fdz.copy(base + to, plane, c, cols);
-            if (p.has_z) fr.copy(base + to, at_r, c, cols);
-            if (p.has_y) fy.copy(base + to, at_y, c, cols);
-            if (gate) fg.copy(base + to, at_g, c, cols);
+            if (p.dro) fdr.copy(base + to, c, cols);
+            if (p.has_z) fdz.copy(base + to + plane, c, cols);
+            if (p.has_z) fr.copy(base + to + at_r, c, cols);
+            if (p.has_y) fy.copy(base + to + at_y, c, cols);
+            if (gate) fg.copy(base + to + at_g, c, cols);
         }
         coming += step;
         to = to == (STAGES - 1) * stage_size ? 0 : to + stage_size;
@@ -670,8 +702,8 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
     for (int k = 0; k < STAGES - 1; ++k) fill();
     for (; row < last; row += step) {
         const bool live = row < p.rows;
-        const int64_t rr = live ? row : 0;
-        Cols<NV, LAY> cc = c;
+        const int64_t rr = live ? row : 0, here = rr * p.D;
+        Cols<T, NV, LAY> cc = c;
         if (TEAM && !live) cc.D = 0;
         if constexpr (LAY == kSingle) {
             copy_wait<STAGES - 2>();
@@ -690,11 +722,11 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             for (int k = 0; k < NV; ++k) {
                 F2 v[4];
                 if (p.has_z) {
-                    fr.read(stage, at_r, cc, k, v);
+                    fr.read(stage + at_r, cc, k, v);
                     s[0] += total(v);
                 }
                 if (p.has_y) {
-                    fy.read(stage, at_y, cc, k, v);
+                    fy.read(stage + at_y, cc, k, v);
                     s[1] += total(v);
                 }
             }
@@ -703,7 +735,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             mean_y = -s[1] * inv_d;
         }
         auto centred = [&](const In& f, unsigned at, float mean, int k, F2 (&v)[4]) {
-            f.read(stage, at, cc, k, v);
+            f.read(stage + at, cc, k, v);
             if (layer) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] = v[j] + both(mean);
@@ -719,7 +751,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
                 s[2] += dot(r, r);
             }
             if (p.has_z) {
-                fdz.read(stage, plane, cc, k, u);
+                fdz.read(stage + plane, cc, k, u);
                 centred(fr, at_r, mean_r, k, r);
                 load_param(p.prm.w_z, 1.0f, cc, k, w);
 #pragma unroll
@@ -741,14 +773,14 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             in_turn();
             F2 e[4], v[4], w[4], n[4], g[4];
             if (p.dro) {
-                fdr.read(stage, 0, cc, k, e);
+                fdr.read(stage, cc, k, e);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) e[j] = both(0.0f);
             }
             if (p.has_z) {
                 centred(fr, at_r, mean_r, k, v);
-                fdz.read(stage, plane, cc, k, g);
+                fdz.read(stage + plane, cc, k, g);
                 load_param(p.prm.w_z, 1.0f, cc, k, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -761,7 +793,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
                 }
                 if (FULL) mask(cc, k, e);
             }
-            if (p.dr) store_eight((T*)p.dr + rr * p.D, cc, k, e);
+            if (p.dr) store_eight((T*)p.dr + here, cc, k, e);
             if (!p.has_y) continue;
             centred(fy, at_y, mean_y, k, y[k]);
             load_param(p.prm.w_y, 1.0f, cc, k, w);
@@ -771,7 +803,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
                 y[k][j] = y[k][j] * both(rstd_y);
                 n[j] = fma2(y[k][j], w[j], n[j]);
             }
-            if (gate) fg.read(stage, at_g, cc, k, g);
+            if (gate) fg.read(stage + at_g, cc, k, g);
             F2 sc[4];
             activation<true>(p.act, g, v);                 // v: act'(g)
             load_param(p.prm.s, 1.0f, cc, k, sc);
@@ -821,21 +853,24 @@ struct GradOut {
     float* to[5];
 };
 
-// The parameters' gradients from the CTAs' sums, in the order of the CTAs.
-__global__ void __launch_bounds__(256) k_block_grads(int32_t D, int32_t parts, const float* __restrict__ part, GradOut out)
+// The parameters' gradients from the CTAs' sums, in a fixed order: 16 threads
+// to a column, each over every 16th CTA, then one over theirs.
+__global__ void __launch_bounds__(512) k_block_grads(int32_t D, int32_t parts, const float* __restrict__ part, GradOut out)
 {
     float* to = out.to[blockIdx.y];
     if (!to) return;
-    __shared__ float s[8][33];
-    const int d = blockIdx.x * 32 + threadIdx.x % 32, k = threadIdx.x / 32;
-    const float* from = part + (int64_t)blockIdx.y * parts * D;
+    __shared__ float s[16][33];
+    const int x = threadIdx.x % 32, k = threadIdx.x / 32, d = blockIdx.x * 32 + x;
+    const float* from = part + (int64_t)blockIdx.y * parts * D + d;
     float v = 0.0f;
-    if (d < D)
-        for (int p = k; p < parts; p += 8) v += from[(int64_t)p * D + d];
-    s[k][threadIdx.x % 32] = v;
+    if (d < D) {
+#pragma unroll 8
+        for (int p = k; p < parts; p += 16) v += from[(int64_t)p * D];
+    }
+    s[k][x] = v;
     __syncthreads();
     if (k == 0 && d < D) {
-        for (int j = 1; j < 8; ++j) v += s[j][threadIdx.x % 32];
+        for (int j = 1; j < 16; ++j) v += s[j][x];
         to[d] = v;
     }
 }
@@ -844,7 +879,7 @@ __global__ void __launch_bounds__(256) k_block_grads(int32_t D, int32_t parts, c
 
 struct Shape {
     int team, cluster, threads;
-    bool exact;                            // every thread has all of its columns
+    bool exact;                            // 128 threads, each with all of its columns
     int64_t units;                         // CTAs (clusters) of one row (or team of rows) each
 };
 
@@ -864,7 +899,7 @@ Shape shape_of(int64_t rows, int64_t D, bool vec)
         s.threads = (int)(div_up(div_up(D, 16 * s.cluster), 32) * 32);
         s.units = rows;
     }
-    s.exact = !s.team && (int64_t)s.threads * 16 * s.cluster == D;
+    s.exact = !s.team && s.threads == 128 && (int64_t)kCtaCols * s.cluster == D;
     return s;
 }
 
@@ -1028,10 +1063,11 @@ mru_status mru_block_norm(const mru_block_problem* p, const mru_block_params* pr
                 b.out(v->scale, (size_t)(p->rows * div_up(p->D, 64)) * 4);
             }
     if (b.clash()) return MRU_ERR_INVALID_ARG;
-    // 8 columns to an access: whole runs, everything 16-byte aligned
-    bool vec = p->D % 8 == 0 && (a.ldy * es) % 16 == 0 && (a.ldg * es) % 16 == 0 && params_aligned(a.prm, 16);
+    // pieces of 16 bytes: whole ones in a row, all of them aligned
+    bool vec = p->D % (16 / (int64_t)es) == 0 && (a.ldy * es) % 16 == 0 && (a.ldg * es) % 16 == 0 && params_aligned(a.prm, 16);
     for (const void* v : {r, y, g, (const void*)r_out, (const void*)z}) vec = vec && aligned(v, 16);
-    if (saved) vec = vec && aligned(saved->r.q, 8) && aligned(saved->y.q, 8) && aligned(saved->g.q, 8);
+    if (saved) vec = vec && aligned(saved->r.q, 16 / es) && aligned(saved->y.q, 16 / es) &&
+                     aligned(saved->g.q, 16 / es);
     a.r = r; a.y = y; a.g = g; a.r_out = r_out; a.z = z;
     a.has_y = has_y; a.has_z = has_z;
     if (saved) { a.r8 = saved->r; a.y8 = saved->y; a.g8 = saved->g; }
@@ -1124,11 +1160,12 @@ mru_status mru_block_norm_backward(const mru_block_problem* p, const mru_block_p
     b.out(ws, ws_bytes);
     if (b.clash()) return MRU_ERR_INVALID_ARG;
     if (ws_bytes < mru_block_backward_workspace_size(p)) return MRU_ERR_WORKSPACE;
-    bool vec = p->D % 8 == 0 && (a.ldy * es) % 16 == 0 && (a.ldg * es) % 16 == 0 &&
+    bool vec = p->D % (16 / (int64_t)es) == 0 && (a.ldy * es) % 16 == 0 && (a.ldg * es) % 16 == 0 &&
                (a.lddy * es) % 16 == 0 && (a.lddg * es) % 16 == 0 && params_aligned(a.prm, 16);
     for (const void* v : {r_out, y, g, dr_out, dz, (const void*)dr, (const void*)dy, (const void*)dg})
         vec = vec && aligned(v, 16);
-    if (saved) vec = vec && aligned(saved->r.q, 8) && aligned(saved->y.q, 8) && aligned(saved->g.q, 8);
+    if (saved) vec = vec && aligned(saved->r.q, 16 / es) && aligned(saved->y.q, 16 / es) &&
+                     aligned(saved->g.q, 16 / es);
     a.r = r_out; a.y = y; a.g = g;
     if (saved) { a.r8 = saved->r; a.y8 = saved->y; a.g8 = saved->g; }
     a.dro = dr_out; a.dz = dz; a.dr = dr; a.dy = dy; a.dg = dg;
@@ -1152,7 +1189,7 @@ mru_status mru_block_norm_backward(const mru_block_problem* p, const mru_block_p
     if (e != cudaSuccess) return MRU_ERR_CUDA;
     if (gr.dw_y || gr.db_y || gr.ds || gr.dw_z || gr.db_z) {
         const GradOut out = {{gr.dw_y, gr.ds, gr.dw_z, gr.db_y, gr.db_z}};
-        k_block_grads<<<dim3((unsigned)div_up(p->D, 32), 5), 256, 0, s>>>(a.D, a.parts, a.part, out);
+        k_block_grads<<<dim3((unsigned)div_up(p->D, 32), 5), 512, 0, s>>>(a.D, a.parts, a.part, out);
         e = cudaGetLastError();
     }
     return cuda_status(e);
