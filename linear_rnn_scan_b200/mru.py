@@ -319,62 +319,72 @@ def _ref(v):
     return ctypes.byref(v) if v is not None else None
 
 
+def _loaded():
+    return _lib if _lib is not None else load()
+
+
 def pack8(rows: int, D: int, ld: int, dtype: int, x: int, out: Packed8, stream: int = 0) -> int:
-    return load().mru_pack8(rows, D, ld, dtype, x, _ref(out), stream)
+    return _loaded().mru_pack8(rows, D, ld, dtype, x, _ref(out), stream)
 
 
 def unpack8(rows: int, D: int, ld: int, dtype: int, packed: Packed8, x: int, stream: int = 0) -> int:
-    return load().mru_unpack8(rows, D, ld, dtype, _ref(packed), x, stream)
+    return _loaded().mru_unpack8(rows, D, ld, dtype, _ref(packed), x, stream)
 
 
 def gated_workspace_size(p: GatedProblem) -> int:
-    return int(load().mru_gated_workspace_size(ctypes.byref(p)))
+    return int(_loaded().mru_gated_workspace_size(ctypes.byref(p)))
 
 
 def gated_backward_workspace_size(p: GatedProblem) -> int:
-    return int(load().mru_gated_backward_workspace_size(ctypes.byref(p)))
+    return int(_loaded().mru_gated_backward_workspace_size(ctypes.byref(p)))
 
 
 def gated_scan(p: GatedProblem, inputs: GatedInputs, y: int, h_last: int | None, saved: GatedSavedBuffers | None,
                ws: int, ws_bytes: int, stream: int = 0) -> int:
-    return load().mru_gated_scan(_ref(p), _ref(inputs), y, h_last, _ref(saved), ws, ws_bytes, stream)
+    return _loaded().mru_gated_scan(_ref(p), _ref(inputs), y, h_last, _ref(saved), ws, ws_bytes, stream)
 
 
 def gated_scan_backward(p: GatedProblem, inputs: GatedInputs, saved: GatedSavedBuffers, dy: int,
                         dh_last: int | None, dx: int, df: int, di: int | None, dlam: int | None, dh0: int | None,
                         ws: int, ws_bytes: int, stream: int = 0) -> int:
-    return load().mru_gated_scan_backward(_ref(p), _ref(inputs), _ref(saved), dy, dh_last, dx, df, di, dlam, dh0,
+    return _loaded().mru_gated_scan_backward(_ref(p), _ref(inputs), _ref(saved), dy, dh_last, dx, df, di, dlam, dh0,
                                           ws, ws_bytes, stream)
 
 
 def debug_stall_next_gated(ms: int) -> None:
     """Testing hook: the next launch of the recurrence with more than 64 tokens
     withholds its first tile's map and bounds its waits by `ms` milliseconds."""
-    load().mru_debug_stall_next_gated(int(ms))
+    _loaded().mru_debug_stall_next_gated(int(ms))
 
 
 def block_norm(p: BlockProblem, prm: BlockParams | None, r: int, y: int | None, g: int | None, r_out: int | None,
                z: int | None, saved: BlockSavedBuffers | None = None, stream: int = 0) -> int:
-    return load().mru_block_norm(_ref(p), _ref(prm), r, y, g, r_out, z, _ref(saved), stream)
+    return _loaded().mru_block_norm(_ref(p), _ref(prm), r, y, g, r_out, z, _ref(saved), stream)
 
 
 def block_backward_workspace_size(p: BlockProblem) -> int:
-    return int(load().mru_block_backward_workspace_size(ctypes.byref(p)))
+    return int(_loaded().mru_block_backward_workspace_size(ctypes.byref(p)))
 
 
 def block_norm_backward(p: BlockProblem, prm: BlockParams | None, r_out: int | None, y: int | None, g: int | None,
                         saved: BlockSavedBuffers | None, dr_out: int | None, dz: int | None, dr: int | None,
                         dy: int | None, dg: int | None, grads: BlockGradBuffers | None, ws: int, ws_bytes: int,
                         stream: int = 0) -> int:
-    return load().mru_block_norm_backward(_ref(p), _ref(prm), r_out, y, g, _ref(saved), dr_out, dz, dr, dy, dg,
+    return _loaded().mru_block_norm_backward(_ref(p), _ref(prm), r_out, y, g, _ref(saved), dr_out, dz, dr, dy, dg,
                                           _ref(grads), ws, ws_bytes, stream)
 
 
 # --------------------------------------------------------- tensor level ---
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream):
@@ -573,26 +583,38 @@ def _launching(device, stream):
             yield st.cuda_stream
 
 
+def _on(device, stream, call, *args):
+    """call(raw stream, *args) with `device` current and the call's stream."""
+    cuda = _torch().cuda
+    if device.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    if stream is None and device.index == cuda.current_device():      # the usual case, without context managers
+        return call(cuda.current_stream().cuda_stream, *args)
+    with _launching(device, stream) as s:
+        return call(s, *args)
+
+
 def _tensor(t, name, shape, dtype, device, contiguous=True):
     """t's device pointer (None for None) after checking what it is."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == device and \
+            (not contiguous or t.is_contiguous()):
+        return t.data_ptr()
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must have dtype {dtype}, not {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _row_stride(t, name):
     """Elements from one row to the next of a tensor whose last dimension is
     contiguous and whose leading ones count rows (a slice of wider rows)."""
     D, ld, rows = t.shape[-1], None, 1
-    if t.numel() == 0:
+    if t.is_contiguous() or t.numel() == 0:
         return D
     for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if size != 1:
@@ -611,6 +633,9 @@ def _row_stride(t, name):
 
 
 def _same_stride(tensors):
+    given = [t for _, t in tensors if t is not None]
+    if all(t.is_contiguous() for t in given):
+        return 0
     lds = {_row_stride(t, n) for n, t in tensors if t is not None}
     if len(lds) > 1:
         raise ValueError(f"{', '.join(n for n, t in tensors if t is not None)} must have the same row stride")
@@ -636,25 +661,28 @@ def _packed_arg(v, name, rows, D, device):
                    _tensor(v.scale, f"{name}.scale", (rows, -(-D // PACK8_GROUP)), torch.float32, device))
 
 
-def _new_workspace(nbytes, ws, device, what):
+def _new_workspace(nbytes, device, what):
     if nbytes == 0:
         raise MruError(ERR_INVALID_ARG, what)
-    return _torch().empty(nbytes, dtype=_torch().uint8, device=device) if ws is None else ws
+    return _torch().empty(nbytes, dtype=_torch().uint8, device=device)
 
 
 def pack8_t(x, *, out=None, stream=None):
     """x [..., D] (float32 or bfloat16) held in 8 bits: Packed(q [rows, D]
     int8, scale [rows, ceil(D / 64)] float32)."""
+    return _on(x.device, stream, _pack8, x, out)
+
+
+def _pack8(s, x, out):
     torch = _torch()
     if x.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("x must be float32 or bfloat16")
     D = x.shape[-1]
     rows = x.numel() // D if D else 0
-    with _launching(x.device, stream) as s:
-        if out is None:
-            out = _new_packed(rows, D, x.device)
-        rc = pack8(rows, D, _row_stride(x, "x"), BF16 if x.dtype == torch.bfloat16 else F32,
-                   _tensor(x, "x", x.shape, x.dtype, x.device, False), _packed_arg(out, "out", rows, D, x.device), s)
+    if out is None:
+        out = _new_packed(rows, D, x.device)
+    rc = pack8(rows, D, _row_stride(x, "x"), BF16 if x.dtype == torch.bfloat16 else F32,
+               _tensor(x, "x", x.shape, x.dtype, x.device, False), _packed_arg(out, "out", rows, D, x.device), s)
     _check(rc, "mru_pack8")
     return out
 
@@ -662,6 +690,10 @@ def pack8_t(x, *, out=None, stream=None):
 def unpack8_t(q, scale, *, dtype=None, out=None, stream=None):
     """The values q [rows, D] and scale [rows, ceil(D / 64)] hold, as dtype
     (float32 when not given)."""
+    return _on(q.device, stream, _unpack8, q, scale, dtype, out)
+
+
+def _unpack8(s, q, scale, dtype, out):
     torch = _torch()
     rows, D = q.shape
     if out is not None and dtype is None:
@@ -669,31 +701,32 @@ def unpack8_t(q, scale, *, dtype=None, out=None, stream=None):
     dtype = dtype or torch.float32
     if dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("dtype must be float32 or bfloat16")
-    with _launching(q.device, stream) as s:
-        if out is None:
-            out = torch.empty((rows, D), dtype=dtype, device=q.device)
-        rc = unpack8(rows, D, _row_stride(out, "out"), BF16 if dtype == torch.bfloat16 else F32,
-                     _packed_arg(Packed(q, scale), "packed", rows, D, q.device),
-                     _tensor(out, "out", (rows, D), dtype, q.device, False), s)
+    if out is None:
+        out = torch.empty((rows, D), dtype=dtype, device=q.device)
+    rc = unpack8(rows, D, _row_stride(out, "out"), BF16 if dtype == torch.bfloat16 else F32,
+                 _packed_arg(Packed(q, scale), "packed", rows, D, q.device),
+                 _tensor(out, "out", (rows, D), dtype, q.device, False), s)
     _check(rc, "mru_unpack8")
     return out
 
 
-def _gated_inputs(p, x, f, i, lam, h0, reset, lens, dev):
+def _gated_inputs(p, shape, dt, x, f, i, lam, h0, reset, lens, dev):
     torch = _torch()
-    dt, shape = _x_dtype(p), (p.B, p.L, p.D)
-    p = GatedProblem(p.B, p.L, p.D, _same_stride([("x", x), ("f", f), ("i", i)]), p.ld_grad, p.dtype, p.gate, p.c)
-    return p, GatedInputs(*[_tensor(t, n, shape, dt, dev, False) for n, t in (("x", x), ("f", f), ("i", i))],
-                          _tensor(lam, "lam", (p.D,), torch.float32, dev),
-                          _tensor(h0, "h0", (p.B, p.D), torch.float32, dev),
-                          _tensor(reset, "reset", (p.B, p.L), torch.uint8, dev),
-                          _tensor(lens, "lens", (p.B,), torch.int32, dev))
+    f32 = torch.float32
+    B, L, D = shape
+    ld = _same_stride((("x", x), ("f", f), ("i", i)))
+    if p.ld != ld:
+        p = GatedProblem(B, L, D, ld, p.ld_grad, p.dtype, p.gate, p.c)
+    return p, GatedInputs(_tensor(x, "x", shape, dt, dev, False), _tensor(f, "f", shape, dt, dev, False),
+                          _tensor(i, "i", shape, dt, dev, False), _tensor(lam, "lam", (D,), f32, dev),
+                          _tensor(h0, "h0", (B, D), f32, dev), _tensor(reset, "reset", (B, L), torch.uint8, dev),
+                          _tensor(lens, "lens", (B,), torch.int32, dev))
 
 
-def _gated_saved(p, saved, dev):
-    K = -(-p.L // GATED_KEEP)
-    return GatedSavedBuffers(_tensor(saved.states, "states", (p.B, K, p.D), _torch().float32, dev),
-                             *[_packed_arg(v, n, p.B * p.L, p.D, dev)
+def _gated_saved(shape, saved, dev):
+    B, L, D = shape
+    return GatedSavedBuffers(_tensor(saved.states, "states", (B, -(-L // GATED_KEEP), D), _torch().float32, dev),
+                             *[_packed_arg(v, n, B * L, D, dev)
                                for n, v in (("x", saved.x), ("f", saved.f), ("i", saved.i))])
 
 
@@ -705,26 +738,28 @@ def gated_scan_t(p: GatedProblem, x, f, *, i=None, lam=None, h0=None, reset=None
     [B, D] float32, saved): saved is None, or with save="full" the states the
     backward needs beside x, f, i, or with save="int8" those and x, f, i in 8
     bits in their place (or pass a GatedSaved of your own to fill)."""
-    torch = _torch()
-    dev = x.device
     if save not in (None, "full", "int8") and not isinstance(save, GatedSaved):
         raise ValueError('save must be None, "full", "int8" or a GatedSaved')
-    with _launching(dev, stream) as s:
-        p, inputs = _gated_inputs(p, x, f, i, lam, h0, reset, lens, dev)
-        if y is None:
-            y = torch.empty((p.B, p.L, p.D), dtype=_x_dtype(p), device=dev)
-        if h_last is None:
-            h_last = torch.empty((p.B, p.D), dtype=torch.float32, device=dev)
-        saved = save if isinstance(save, GatedSaved) else None
-        if isinstance(save, str):
-            packed = [_new_packed(p.B * p.L, p.D, dev) if save == "int8" and t is not None else None
-                      for t in (x, f, i)]
-            saved = GatedSaved(torch.empty((p.B, -(-p.L // GATED_KEEP), p.D), dtype=torch.float32, device=dev),
-                               *packed)
-        ws = _new_workspace(gated_workspace_size(p), ws, dev, "gated_workspace_size")
-        rc = gated_scan(p, inputs, _tensor(y, "y", (p.B, p.L, p.D), _x_dtype(p), dev),
-                        _tensor(h_last, "h_last", (p.B, p.D), torch.float32, dev),
-                        None if saved is None else _gated_saved(p, saved, dev), ws.data_ptr(), ws.numel(), s)
+    return _on(x.device, stream, _gated_scan, p, x, f, i, lam, h0, reset, lens, save, y, h_last, ws)
+
+
+def _gated_scan(s, p, x, f, i, lam, h0, reset, lens, save, y, h_last, ws):
+    torch = _torch()
+    dev, f32, dt = x.device, torch.float32, _x_dtype(p)
+    shape = B, L, D = p.B, p.L, p.D
+    p, inputs = _gated_inputs(p, shape, dt, x, f, i, lam, h0, reset, lens, dev)
+    if y is None:
+        y = torch.empty(shape, dtype=dt, device=dev)
+    if h_last is None:
+        h_last = torch.empty((B, D), dtype=f32, device=dev)
+    saved = save if isinstance(save, GatedSaved) else None
+    if isinstance(save, str):
+        packed = [_new_packed(B * L, D, dev) if save == "int8" and t is not None else None for t in (x, f, i)]
+        saved = GatedSaved(torch.empty((B, -(-L // GATED_KEEP), D), dtype=f32, device=dev), *packed)
+    if ws is None:
+        ws = _new_workspace(gated_workspace_size(p), dev, "gated_workspace_size")
+    rc = gated_scan(p, inputs, _tensor(y, "y", shape, dt, dev), _tensor(h_last, "h_last", (B, D), f32, dev),
+                    None if saved is None else _gated_saved(shape, saved, dev), ws.data_ptr(), ws.numel(), s)
     _check(rc, "mru_gated_scan")
     return y, h_last, saved
 
@@ -734,43 +769,55 @@ def gated_scan_backward_t(p: GatedProblem, dy, saved, *, x=None, f=None, i=None,
     """Gradients of sum <dy, y> + <dh_last, h_last> from what the forward saved
     (and x, f, i when it saved no 8-bit copies): GatedGrads(dx, df, di, dlam,
     dh0), di and dlam None unless the gate is "lru"."""
+    return _on(dy.device, stream, _gated_backward, p, dy, saved, x, f, i, lam, reset, lens, dh_last, dx, df, di, dlam,
+               dh0, ws)
+
+
+def _gated_backward(s, p, dy, saved, x, f, i, lam, reset, lens, dh_last, dx, df, di, dlam, dh0, ws):
     torch = _torch()
-    dev = dy.device
-    dt, shape, lru = _x_dtype(p), (p.B, p.L, p.D), p.gate == GATES["lru"]
+    dev, f32, dt, lru = dy.device, torch.float32, _x_dtype(p), p.gate == GATES["lru"]
+    shape = B, L, D = p.B, p.L, p.D
     if saved.x is not None:
         x = f = i = None
-    elif p.B * p.L * p.D and (x is None or f is None or (lru and i is None)):
+    elif B * L * D and (x is None or f is None or (lru and i is None)):
         raise ValueError("x, f (and i) are needed: the forward saved no 8-bit copies of them")
-    with _launching(dev, stream) as s:
-        p, inputs = _gated_inputs(p, x, f, i, lam, None, reset, lens, dev)
-        dx = torch.empty(shape, dtype=dt, device=dev) if dx is None else dx
-        df = torch.empty(shape, dtype=dt, device=dev) if df is None else df
-        if lru:
-            di = torch.empty(shape, dtype=dt, device=dev) if di is None else di
-            dlam = torch.empty((p.D,), dtype=torch.float32, device=dev) if dlam is None else dlam
-        if dh0 is None:
-            dh0 = torch.empty((p.B, p.D), dtype=torch.float32, device=dev)
-        p.ld_grad = _same_stride([("dx", dx), ("df", df), ("di", di)])
-        ws = _new_workspace(gated_backward_workspace_size(p), ws, dev, "gated_backward_workspace_size")
-        rc = gated_scan_backward(p, inputs, _gated_saved(p, saved, dev), _tensor(dy, "dy", shape, dt, dev),
-                                 _tensor(dh_last, "dh_last", (p.B, p.D), torch.float32, dev),
-                                 *[_tensor(t, n, shape, dt, dev, False)
-                                   for n, t in (("dx", dx), ("df", df), ("di", di))],
-                                 _tensor(dlam, "dlam", (p.D,), torch.float32, dev),
-                                 _tensor(dh0, "dh0", (p.B, p.D), torch.float32, dev), ws.data_ptr(), ws.numel(), s)
+    p, inputs = _gated_inputs(p, shape, dt, x, f, i, lam, None, reset, lens, dev)
+    dx = torch.empty(shape, dtype=dt, device=dev) if dx is None else dx
+    df = torch.empty(shape, dtype=dt, device=dev) if df is None else df
+    if lru:
+        di = torch.empty(shape, dtype=dt, device=dev) if di is None else di
+        dlam = torch.empty((D,), dtype=f32, device=dev) if dlam is None else dlam
+    if dh0 is None:
+        dh0 = torch.empty((B, D), dtype=f32, device=dev)
+    ld = _same_stride((("dx", dx), ("df", df), ("di", di)))
+    if p.ld_grad != ld:
+        p = GatedProblem(B, L, D, p.ld, ld, p.dtype, p.gate, p.c)
+    if ws is None:
+        ws = _new_workspace(gated_backward_workspace_size(p), dev, "gated_backward_workspace_size")
+    rc = gated_scan_backward(p, inputs, _gated_saved(shape, saved, dev), _tensor(dy, "dy", shape, dt, dev),
+                             _tensor(dh_last, "dh_last", (B, D), f32, dev), _tensor(dx, "dx", shape, dt, dev, False),
+                             _tensor(df, "df", shape, dt, dev, False), _tensor(di, "di", shape, dt, dev, False),
+                             _tensor(dlam, "dlam", (D,), f32, dev), _tensor(dh0, "dh0", (B, D), f32, dev),
+                             ws.data_ptr(), ws.numel(), s)
     _check(rc, "mru_gated_scan_backward")
     return GatedGrads(dx, df, di, dlam, dh0)
 
 
-def _block_params(p, dev, w_y, b_y, s, w_z, b_z):
-    return BlockParams(*[_tensor(t, n, (p.D,), _torch().float32, dev)
-                         for n, t in (("w_y", w_y), ("b_y", b_y), ("s", s), ("w_z", w_z), ("b_z", b_z))])
+def _block_params(D, dev, w_y, b_y, s, w_z, b_z):
+    f32 = _torch().float32
+    return BlockParams(_tensor(w_y, "w_y", (D,), f32, dev), _tensor(b_y, "b_y", (D,), f32, dev),
+                       _tensor(s, "s", (D,), f32, dev), _tensor(w_z, "w_z", (D,), f32, dev),
+                       _tensor(b_z, "b_z", (D,), f32, dev))
 
 
-def _block_with(p, **lds):
+def _block_strides(p, y, g, dy=None, dg=None):
+    """p with the row strides of these tensors (0: rows without gaps)."""
+    lds = [0 if t is None or t.is_contiguous() else _row_stride(t, n)
+           for n, t in (("y", y), ("g", g), ("dy", dy), ("dg", dg))]
+    if lds == [p.ld_y, p.ld_g, p.ld_dy, p.ld_dg]:
+        return p
     q = BlockProblem.from_buffer_copy(p)
-    for k, v in lds.items():
-        setattr(q, k, v)
+    q.ld_y, q.ld_g, q.ld_dy, q.ld_dg = lds
     return q
 
 
@@ -781,26 +828,29 @@ def block_norm_t(p: BlockProblem, r, *, y=None, g=None, w_y=None, b_y=None, s=No
     float32 or None.  Returns (r', z, saved): r' is r itself without y, z None
     with norm_after=False, saved a BlockSaved of 8-bit copies with save="int8"
     (or pass a BlockSaved of your own to fill), else None."""
-    torch = _torch()
-    dev, dt = r.device, _x_dtype(p)
     if save not in (None, "int8") and not isinstance(save, BlockSaved):
         raise ValueError('save must be None, "int8" or a BlockSaved')
-    if r.shape[-1] != p.D or r.numel() != p.rows * p.D:
-        raise ValueError(f"r must have {p.rows} rows of {p.D}")
-    with _launching(dev, stream) as st:
-        p = _block_with(p, ld_y=0 if y is None else _row_stride(y, "y"), ld_g=0 if g is None else _row_stride(g, "g"))
-        if y is not None and r_out is None:
-            r_out = torch.empty(r.shape, dtype=dt, device=dev)
-        if norm_after and z is None:
-            z = torch.empty(r.shape, dtype=dt, device=dev)
-        saved = save if isinstance(save, BlockSaved) else None
-        if isinstance(save, str):
-            saved = BlockSaved(*[None if t is None else _new_packed(p.rows, p.D, dev) for t in (r, y, g)])
-        buf = None if saved is None else BlockSavedBuffers(
-            *[_packed_arg(v, n, p.rows, p.D, dev) for n, v in zip(("r", "y", "g"), saved)])
-        rc = block_norm(p, _block_params(p, dev, w_y, b_y, s, w_z, b_z), _tensor(r, "r", r.shape, dt, dev),
-                        _tensor(y, "y", r.shape, dt, dev, False), _tensor(g, "g", r.shape, dt, dev, False),
-                        _tensor(r_out, "r_out", r.shape, dt, dev), _tensor(z, "z", r.shape, dt, dev), buf, st)
+    return _on(r.device, stream, _block_norm, p, r, y, g, (w_y, b_y, s, w_z, b_z), norm_after, save, r_out, z)
+
+
+def _block_norm(st, p, r, y, g, params, norm_after, save, r_out, z):
+    torch = _torch()
+    dev, dt, shape, rows, D = r.device, _x_dtype(p), r.shape, p.rows, p.D
+    if shape[-1] != D or r.numel() != rows * D:
+        raise ValueError(f"r must have {rows} rows of {D}")
+    p = _block_strides(p, y, g)
+    if y is not None and r_out is None:
+        r_out = torch.empty(shape, dtype=dt, device=dev)
+    if norm_after and z is None:
+        z = torch.empty(shape, dtype=dt, device=dev)
+    saved = save if isinstance(save, BlockSaved) else None
+    if isinstance(save, str):
+        saved = BlockSaved(*[None if t is None else _new_packed(rows, D, dev) for t in (r, y, g)])
+    buf = None if saved is None else BlockSavedBuffers(
+        *[_packed_arg(v, n, rows, D, dev) for n, v in zip(("r", "y", "g"), saved)])
+    rc = block_norm(p, _block_params(D, dev, *params), _tensor(r, "r", shape, dt, dev),
+                    _tensor(y, "y", shape, dt, dev, False), _tensor(g, "g", shape, dt, dev, False),
+                    _tensor(r_out, "r_out", shape, dt, dev), _tensor(z, "z", shape, dt, dev), buf, st)
     _check(rc, "mru_block_norm")
     return (r if y is None else r_out), z, saved
 
@@ -811,40 +861,42 @@ def block_norm_backward_t(p: BlockProblem, *, dr_out=None, dz=None, saved=None, 
     stored r', y and g or from the forward's 8-bit copies: BlockGrads(dr, dy,
     dg, dw_y, db_y, ds, dw_z, db_z), None where there is no y, g or z; the
     biases' sums where the norm is "layer" or a b_y was given."""
-    torch = _torch()
     ref = dz if dz is not None else dr_out
     if ref is None:
         raise ValueError("dr_out or dz is needed")
-    dev, dt, shape = ref.device, _x_dtype(p), ref.shape
-    if shape[-1] != p.D or ref.numel() != p.rows * p.D:
-        raise ValueError(f"the gradients must have {p.rows} rows of {p.D}")
+    return _on(ref.device, stream, _block_backward, p, ref, dr_out, dz, saved, r_out, y, g, (w_y, b_y, s, w_z, None),
+               dr, dy, dg, ws)
+
+
+def _block_backward(st, p, ref, dr_out, dz, saved, r_out, y, g, params, dr, dy, dg, ws):
+    torch = _torch()
+    dev, dt, shape, rows, D = ref.device, _x_dtype(p), ref.shape, p.rows, p.D
+    if shape[-1] != D or ref.numel() != rows * D:
+        raise ValueError(f"the gradients must have {rows} rows of {D}")
     if saved is not None:
         r_out = y = g = None
         has_y, gate = saved.y is not None, saved.g is not None
     else:
         has_y, gate = y is not None, g is not None
-    bias = p.norm == NORMS["layer"] or b_y is not None
-    with _launching(dev, stream) as st:
-        dr = torch.empty(shape, dtype=dt, device=dev) if dr is None else dr
-        if has_y and dy is None:
-            dy = torch.empty(shape, dtype=dt, device=dev)
-        if gate and dg is None:
-            dg = torch.empty(shape, dtype=dt, device=dev)
-        p = _block_with(p, **{k: 0 if t is None else _row_stride(t, k[3:])
-                              for k, t in (("ld_y", y), ("ld_g", g), ("ld_dy", dy), ("ld_dg", dg))})
-        want = {"dw_y": has_y, "db_y": has_y and bias, "ds": has_y, "dw_z": dz is not None,
-                "db_z": dz is not None and bias}
-        sums = {k: torch.empty((p.D,), dtype=torch.float32, device=dev) if v else None for k, v in want.items()}
-        buf = None if saved is None else BlockSavedBuffers(
-            *[_packed_arg(v, n, p.rows, p.D, dev) for n, v in zip(("r", "y", "g"), saved)])
-        ws = _new_workspace(block_backward_workspace_size(p), ws, dev, "block_backward_workspace_size")
-        rc = block_norm_backward(p, _block_params(p, dev, w_y, b_y, s, w_z, None),
-                                 _tensor(r_out, "r_out", shape, dt, dev), _tensor(y, "y", shape, dt, dev, False),
-                                 _tensor(g, "g", shape, dt, dev, False), buf,
-                                 _tensor(dr_out, "dr_out", shape, dt, dev), _tensor(dz, "dz", shape, dt, dev),
-                                 _tensor(dr, "dr", shape, dt, dev), _tensor(dy, "dy", shape, dt, dev, False),
-                                 _tensor(dg, "dg", shape, dt, dev, False),
-                                 BlockGradBuffers(*[None if t is None else t.data_ptr() for t in sums.values()]),
-                                 ws.data_ptr(), ws.numel(), st)
+    bias = p.norm == NORMS["layer"] or params[1] is not None
+    dr = torch.empty(shape, dtype=dt, device=dev) if dr is None else dr
+    if has_y and dy is None:
+        dy = torch.empty(shape, dtype=dt, device=dev)
+    if gate and dg is None:
+        dg = torch.empty(shape, dtype=dt, device=dev)
+    p = _block_strides(p, y, g, dy, dg)
+    want = (has_y, has_y and bias, has_y, dz is not None, dz is not None and bias)
+    sums = [torch.empty((D,), dtype=torch.float32, device=dev) if v else None for v in want]
+    buf = None if saved is None else BlockSavedBuffers(
+        *[_packed_arg(v, n, rows, D, dev) for n, v in zip(("r", "y", "g"), saved)])
+    if ws is None:
+        ws = _new_workspace(block_backward_workspace_size(p), dev, "block_backward_workspace_size")
+    rc = block_norm_backward(p, _block_params(D, dev, *params), _tensor(r_out, "r_out", shape, dt, dev),
+                             _tensor(y, "y", shape, dt, dev, False), _tensor(g, "g", shape, dt, dev, False), buf,
+                             _tensor(dr_out, "dr_out", shape, dt, dev), _tensor(dz, "dz", shape, dt, dev),
+                             _tensor(dr, "dr", shape, dt, dev), _tensor(dy, "dy", shape, dt, dev, False),
+                             _tensor(dg, "dg", shape, dt, dev, False),
+                             BlockGradBuffers(*[None if t is None else t.data_ptr() for t in sums]),
+                             ws.data_ptr(), ws.numel(), st)
     _check(rc, "mru_block_norm_backward")
-    return BlockGrads(dr, dy, dg, **sums)
+    return BlockGrads(dr, dy, dg, *sums)
