@@ -398,7 +398,8 @@ size_t mru_gated_backward_workspace_size(const mru_gated_problem* p);
 
 /* y [B, L, D] (contiguous), h_last [B, D] fp32 or NULL: the state after the
  * last token (may not be h0's buffer); saved: NULL, or what to keep.  One
- * token per sequence (L = 1) is the serving step. */
+ * token per sequence (L = 1) is the serving step.  With L <= 64 nothing
+ * waits, and ws may be NULL (no status word then). */
 mru_status mru_gated_scan(const mru_gated_problem* p, const mru_gated_inputs* in, void* y, float* h_last,
                           const mru_gated_saved* saved, void* ws, size_t ws_bytes, void* stream);
 

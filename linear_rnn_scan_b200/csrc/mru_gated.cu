@@ -79,7 +79,7 @@ template <typename T, int GATE>
 __global__ void __launch_bounds__(128) k_gated_short(Args g)
 {
     const int64_t ch = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (ch == 0) *g.status = 0;
+    if (ch == 0 && g.status) *g.status = 0;
     if (ch >= g.B * g.D) return;
     const int64_t b = ch / g.D, d = ch - b * g.D, len = valid_tokens(g, b);
     const float csp = GATE == MRU_GATE_LRU ? g.c * softplus(g.lam[d]) : 0.0f;
@@ -104,7 +104,7 @@ template <typename T, int GATE, bool PACKED>
 __global__ void __launch_bounds__(128) k_gated_short_bwd(Args g)
 {
     const int64_t ch = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (ch == 0) *g.status = 0;
+    if (ch == 0 && g.status) *g.status = 0;
     if (ch >= g.B * g.D) return;
     const int64_t b = ch / g.D, d = ch - b * g.D, len = valid_tokens(g, b);
     const float csp = GATE == MRU_GATE_LRU ? g.c * softplus(g.lam[d]) : 0.0f;
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, C == 4 ? 2 : 3) k_gated_tile(Args g)
         const uint32_t first = g.ticket ? atomicAdd(g.ticket, 1u) : blockIdx.x;
         find_tile<C, false>(g, first, mem.tile[0]);
         find_tile<C, false>(g, draw(g, first), mem.tile[1]);
-        if (!g.ticket && blockIdx.x == 0) *g.status = 0;
+        if (!g.ticket && blockIdx.x == 0 && g.status) *g.status = 0;
     }
     __syncthreads();
     if (mem.tile[0].ticket < g.tiles) {
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_gated_tile_bwd(Args g)
         const uint32_t first = g.ticket ? atomicAdd(g.ticket, 1u) : blockIdx.x;
         find_tile<C, true>(g, first, mem.tile[0]);
         find_tile<C, true>(g, draw(g, first), mem.tile[1]);
-        if (!g.ticket && blockIdx.x == 0) *g.status = 0;
+        if (!g.ticket && blockIdx.x == 0 && g.status) *g.status = 0;
     }
     __syncthreads();
     if (mem.tile[0].ticket < g.tiles) {
@@ -968,7 +968,8 @@ mru_status mru_gated_scan(const mru_gated_problem* p, const mru_gated_inputs* in
 {
     mru_status st = check_problem(p);
     if (st != MRU_OK) return st;
-    if (!in || !ws || !aligned(ws, 16) || !common_inputs_ok(*p, *in)) return MRU_ERR_INVALID_ARG;
+    const bool waits = p->L > kKeep;                                 // else the workspace may be left out
+    if (!in || (waits && !ws) || !aligned(ws, 16) || !common_inputs_ok(*p, *in)) return MRU_ERR_INVALID_ARG;
     const size_t es = elem_size(p->dtype);
     const bool lru = p->gate == MRU_GATE_LRU, any = p->B * p->D > 0, tokens = any && p->L > 0;
     if (lru ? (tokens && !in->i) : (in->i != nullptr)) return MRU_ERR_INVALID_ARG;
@@ -994,7 +995,7 @@ mru_status mru_gated_scan(const mru_gated_problem* p, const mru_gated_inputs* in
     b.in(g.lens, (size_t)g.B * 4);
     b.out(y, (size_t)rows * width);
     b.out(h_last, state);
-    b.out(ws, ws_bytes);
+    b.out(ws, ws ? ws_bytes : 0);
     if (saved) {
         b.out(saved->states, (size_t)(g.B * g.K * g.D) * 4);
         for (const mru_packed8* v : {&saved->x, &saved->f, &saved->i}) {
@@ -1005,10 +1006,10 @@ mru_status mru_gated_scan(const mru_gated_problem* p, const mru_gated_inputs* in
     }
     if (b.clash()) return MRU_ERR_INVALID_ARG;
     const Layout W = layout(*p, false);
-    if (ws_bytes < W.bytes) return MRU_ERR_WORKSPACE;
+    if (ws && ws_bytes < W.bytes) return MRU_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    if (!any || g.K > 1) e = cudaMemsetAsync(ws, 0, W.zeroed, s);   // else the kernel clears the status word
+    if (ws && (!any || g.K > 1)) e = cudaMemsetAsync(ws, 0, W.zeroed, s);   // else the kernel clears the status word
     if (e != cudaSuccess || !any) return cuda_status(e);
     place(g, W, ws);
     take_stall(g);

@@ -585,11 +585,12 @@ def _launching(device, stream):
 
 def _on(device, stream, call, *args):
     """call(raw stream, *args) with `device` current and the call's stream."""
-    cuda = _torch().cuda
+    torch = _torch()
     if device.type != "cuda":
         raise ValueError("tensors must be CUDA tensors")
-    if stream is None and device.index == cuda.current_device():      # the usual case, without context managers
-        return call(cuda.current_stream().cuda_stream, *args)
+    if stream is None and device.index == torch.cuda.current_device():   # the usual case, without context managers
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return call(raw(device.index) if raw else torch.cuda.current_stream().cuda_stream, *args)
     with _launching(device, stream) as s:
         return call(s, *args)
 
@@ -749,17 +750,18 @@ def _gated_scan(s, p, x, f, i, lam, h0, reset, lens, save, y, h_last, ws):
     shape = B, L, D = p.B, p.L, p.D
     p, inputs = _gated_inputs(p, shape, dt, x, f, i, lam, h0, reset, lens, dev)
     if y is None:
-        y = torch.empty(shape, dtype=dt, device=dev)
+        y = torch.empty_like(x) if p.ld == 0 else torch.empty(shape, dtype=dt, device=dev)
     if h_last is None:
-        h_last = torch.empty((B, D), dtype=f32, device=dev)
+        h_last = torch.empty((B, D), dtype=f32, device=dev) if h0 is None else torch.empty_like(h0)
     saved = save if isinstance(save, GatedSaved) else None
     if isinstance(save, str):
         packed = [_new_packed(B * L, D, dev) if save == "int8" and t is not None else None for t in (x, f, i)]
         saved = GatedSaved(torch.empty((B, -(-L // GATED_KEEP), D), dtype=f32, device=dev), *packed)
-    if ws is None:
+    if ws is None and L > GATED_KEEP:                      # up to one piece of tokens nothing waits: no workspace
         ws = _new_workspace(gated_workspace_size(p), dev, "gated_workspace_size")
     rc = gated_scan(p, inputs, _tensor(y, "y", shape, dt, dev), _tensor(h_last, "h_last", (B, D), f32, dev),
-                    None if saved is None else _gated_saved(shape, saved, dev), ws.data_ptr(), ws.numel(), s)
+                    None if saved is None else _gated_saved(shape, saved, dev),
+                    None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s)
     _check(rc, "mru_gated_scan")
     return y, h_last, saved
 
@@ -840,9 +842,9 @@ def _block_norm(st, p, r, y, g, params, norm_after, save, r_out, z):
         raise ValueError(f"r must have {rows} rows of {D}")
     p = _block_strides(p, y, g)
     if y is not None and r_out is None:
-        r_out = torch.empty(shape, dtype=dt, device=dev)
+        r_out = torch.empty_like(r)
     if norm_after and z is None:
-        z = torch.empty(shape, dtype=dt, device=dev)
+        z = torch.empty_like(r)
     saved = save if isinstance(save, BlockSaved) else None
     if isinstance(save, str):
         saved = BlockSaved(*[None if t is None else _new_packed(rows, D, dev) for t in (r, y, g)])
