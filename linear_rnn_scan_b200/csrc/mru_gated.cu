@@ -3,6 +3,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "mru_gated_tile.cuh"
 
@@ -143,23 +144,76 @@ __global__ void __launch_bounds__(128) k_gated_short_bwd(Args g)
 }
 
 // ---------------------------------------------------------------- forward ---
+//
+// A block's warps have two tasks.  Eight compute: each maps its 8 tokens of a
+// tile (decays and inputs stay in registers), and, once the state before them
+// is known, runs the states over them and writes.  Two manage: they draw
+// tiles, start their copies two tiles ahead, compose and publish a tile's map,
+// find its carry and hand every warp its state.  Every input is read once and
+// every output written once, and the instructions of an element are few enough
+// for the memory to set the pace.
 
 // Channels of a lane: tiles of 128 channels in bf16's forward, of 64 elsewhere.
-constexpr int fwd_channels(size_t elem) { return elem == 2 ? 4 : 2; }
+constexpr int fwd_channels(size_t elem, bool vec) { return elem == 2 && vec ? 4 : 2; }
 constexpr int kBwdC = 2;
 
 template <int C>
 struct TileMem {
-    MapRow<C> agg[kWarps];               // the warps' maps
-    Entries<C> ent;
-    float csp[32 * C];                   // c softplus(lam) of the tile's channels
-    Tile tile[3];                        // this one, the next, the one after
+    float2 map[kWarps][32 * C];          // the warps' maps (P, H), by channel
+    float state[kWarps][32 * C];         // and the states before them
+    float csp[2][32 * C];                // c softplus(lam)
+    uint32_t resets[2][2];               // tokens that start anew
+    Tile tile[4];
+    uint64_t full[2];                    // a stage's copies are there
 };
 
-template <int C>
-__device__ __forceinline__ Vec<C> csp_of(const float* csp, int lane)
+// The managers' lane's K channels of a warp's map.
+template <int K>
+__device__ __forceinline__ Map<K> lane_map(const float2* row, int m)
 {
-    return read_row<C>(csp + C * lane);
+    Map<K> r;
+    if constexpr (K == 2) {
+        const float4 v = *reinterpret_cast<const float4*>(row + 2 * m);
+        r.P[0] = v.x; r.H[0] = v.y; r.P[1] = v.z; r.H[1] = v.w;
+    } else {
+        const float2 v = row[m];
+        r.P[0] = v.x; r.H[0] = v.y;
+    }
+    return r;
+}
+template <int C, bool VEC>
+__device__ __forceinline__ void put_map(float2* row, int lane, const Map<C>& m)
+{
+    if constexpr (VEC) {
+#pragma unroll
+        for (int k = 0; k < C / 2; ++k)
+            *reinterpret_cast<float4*>(row + C * lane + 2 * k) = make_float4(m.P[2 * k], m.H[2 * k], m.P[2 * k + 1], m.H[2 * k + 1]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) row[channel<C, VEC>(lane, c)] = make_float2(m.P[c], m.H[c]);
+    }
+}
+template <int K>
+__device__ __forceinline__ void put_states(float* row, int m, const Vec<K>& h)
+{
+#pragma unroll
+    for (int c = 0; c < K; ++c) row[K * m + c] = h.v[c];
+}
+// A manager's channels of a [B, D] array.
+template <int K>
+__device__ __forceinline__ void put_lane(float* to, const Vec<K>& h, int m, int channels)
+{
+#pragma unroll
+    for (int c = 0; c < K; ++c)
+        if (K * m + c < channels) to[K * m + c] = h.v[c];
+}
+template <int K>
+__device__ __forceinline__ Vec<K> get_lane(const float* from, int m, int channels)
+{
+    Vec<K> h;
+#pragma unroll
+    for (int c = 0; c < K; ++c) h.v[c] = from && K * m + c < channels ? from[K * m + c] : 0.0f;
+    return h;
 }
 
 template <int C>
@@ -171,13 +225,14 @@ __device__ __forceinline__ bool all_near(const Vec<C>& csp)
     return __all_sync(~0u, near);
 }
 
-// 8-bit copies of a warp's tokens.  A run of 64 channels is 64 / C lanes of a
-// row; the largest magnitudes of all runs (input, token, half) are found first
-// and a lane takes the factors of one or two of them for all.
-template <typename T, int C, int NIN>
-__device__ __forceinline__ void pack_rows(const Args& g, const Tile& t, int w, int lane, const T* stage, bool wide8)
+// 8-bit copies of a warp's tokens.  A run of 64 channels is the whole row or
+// half a row's lanes; the largest magnitudes of all runs (input, token, half)
+// are found first and a lane takes the factors of one or two of them for all.
+template <typename T, int C, bool VEC, int NIN>
+__device__ __forceinline__ void pack_rows(const Args& g, const Tile& t, int w, int lane,
+                                          const Rows<T, 32 * C, VEC> (&in)[NIN], bool wide8)
 {
-    constexpr int kCh = 32 * C, HALVES = kCh / 64, RUNS = NIN * kStep * HALVES, SETS = (RUNS + 31) / 32;
+    constexpr int HALVES = C / 2, RUNS = NIN * kStep * HALVES, SETS = (RUNS + 31) / 32;
     uint32_t mine[SETS];
 #pragma unroll
     for (int k = 0; k < SETS; ++k) mine[k] = 0;
@@ -185,10 +240,10 @@ __device__ __forceinline__ void pack_rows(const Args& g, const Tile& t, int w, i
     for (int n = 0; n < NIN; ++n)
 #pragma unroll
         for (int s = 0; s < kStep; ++s) {
-            const Vec<C> v = read_row<C>(stage + (n * kTok + w * kStep + s) * kCh + C * lane);
+            const Vec<C> v = read_row<C, VEC>(in[n].row(w * kStep + s), lane);
             uint32_t m = 0;
 #pragma unroll
-            for (int c = 0; c < C; ++c) m = max(m, mag_bits(v.v[c]));
+            for (int c = 0; c < C; ++c) m = max(m, channel<C, VEC>(lane, c) < t.channels ? mag_bits(v.v[c]) : 0u);
 #pragma unroll
             for (int h = 0; h < HALVES; ++h) {
                 const int run = (n * kStep + s) * HALVES + h;
@@ -209,10 +264,9 @@ __device__ __forceinline__ void pack_rows(const Args& g, const Tile& t, int w, i
             to[(row0 + s) * runs + t.d0 / 64 + h] = scale;
         }
     }
-    const int channels = t.channels - C * lane;
 #pragma unroll
     for (int n = 0; n < NIN; ++n) {
-        int8_t* at = (n == 0 ? g.x8.q : n == 1 ? g.f8.q : g.i8.q) + row0 * g.D + t.d0 + C * lane;
+        int8_t* at = (n == 0 ? g.x8.q : n == 1 ? g.f8.q : g.i8.q) + row0 * g.D + t.d0;
 #pragma unroll
         for (int s = 0; s < kStep; ++s, at += g.D) {
             const int run = (n * kStep + s) * HALVES;
@@ -222,19 +276,19 @@ __device__ __forceinline__ void pack_rows(const Args& g, const Tile& t, int w, i
                 if (lane >= 16) k = k1;
             }
             if (s >= left) continue;
-            const Vec<C> v = read_row<C>(stage + (n * kTok + w * kStep + s) * kCh + C * lane);
+            const Vec<C> v = read_row<C, VEC>(in[n].row(w * kStep + s), lane);
             uint32_t q = 0;
 #pragma unroll
             for (int c = 0; c < C; ++c) q |= (uint32_t)pack8_q(v.v[c], k) << (8 * c);
-            if (wide8) {
-                if (channels > 0) {
-                    if constexpr (C == 4) *reinterpret_cast<uint32_t*>(at) = q;
-                    else *reinterpret_cast<uint16_t*>(at) = (uint16_t)q;
+            if (VEC && wide8) {
+                if (C * lane < t.channels) {
+                    if constexpr (C == 4) *reinterpret_cast<uint32_t*>(at + 4 * lane) = q;
+                    else *reinterpret_cast<uint16_t*>(at + 2 * lane) = (uint16_t)q;
                 }
             } else {
 #pragma unroll
                 for (int c = 0; c < C; ++c)
-                    if (c < channels) at[c] = (int8_t)(q >> (8 * c));
+                    if (channel<C, VEC>(lane, c) < t.channels) at[channel<C, VEC>(lane, c)] = (int8_t)(q >> (8 * c));
             }
         }
     }
@@ -242,11 +296,11 @@ __device__ __forceinline__ void pack_rows(const Args& g, const Tile& t, int w, i
 
 // The decays and inputs of a warp's tokens and their map.  SPECIAL: padding
 // (nothing happens) or resets (the state before counts as zero).
-template <typename T, int C, int GATE, bool SPECIAL, bool NEAR>
-__device__ __forceinline__ Map<C> local_map(const T* at, const Vec<C>& csp, int n, uint32_t resets,
-                                            Vec<C> (&a)[kStep], Vec<C> (&b)[kStep])
+template <typename T, int C, bool VEC, int GATE, bool SPECIAL, bool NEAR>
+__device__ __forceinline__ Map<C> local_map(const Rows<T, 32 * C, VEC> (&in)[inputs_of(GATE)], int w, int lane,
+                                            const Vec<C>& csp, int n, uint32_t resets, Vec<C> (&a)[kStep],
+                                            Vec<C> (&b)[kStep])
 {
-    constexpr int kCh = 32 * C, kIn = kTok * kCh;
     Map<C> m = Map<C>::of(1.0f);
 #pragma unroll
     for (int s = 0; s < kStep; ++s) {
@@ -258,9 +312,10 @@ __device__ __forceinline__ Map<C> local_map(const T* at, const Vec<C>& csp, int 
             }
             continue;
         }
-        const Vec<C> x = read_row<C>(at + s * kCh), f = read_row<C>(at + kIn + s * kCh);
+        const int r = w * kStep + s;
+        const Vec<C> x = read_row<C, VEC>(in[0].row(r), lane), f = read_row<C, VEC>(in[1].row(r), lane);
         Vec<C> i = x;
-        if (GATE == MRU_GATE_LRU) i = read_row<C>(at + 2 * kIn + s * kCh);
+        if constexpr (GATE == MRU_GATE_LRU) i = read_row<C, VEC>(in[2].row(r), lane);
         if (SPECIAL && (resets >> s & 1)) m = Map<C>::of(0.0f);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -273,9 +328,9 @@ __device__ __forceinline__ Map<C> local_map(const T* at, const Vec<C>& csp, int 
     return m;
 }
 
-template <typename T, int C, int GATE, bool SPECIAL>
-__device__ __forceinline__ void run_states(T* y, int64_t D, int left, Vec<C> h, int n, uint32_t resets,
-                                           const Vec<C> (&a)[kStep], const Vec<C> (&b)[kStep], const Put& put)
+template <typename T, int C, bool VEC, int GATE, bool SPECIAL>
+__device__ __forceinline__ void run_states(T* y, int64_t D, int left, int lane, Vec<C> h, int n, uint32_t resets,
+                                           const Vec<C> (&a)[kStep], const Vec<C> (&b)[kStep], bool whole, int channels)
 {
 #pragma unroll
     for (int s = 0; s < kStep; ++s, y += D) {
@@ -286,198 +341,201 @@ __device__ __forceinline__ void run_states(T* y, int64_t D, int left, Vec<C> h, 
                                             : fmaf(a[s].v[c], h.v[c], b[s].v[c]);
         Vec<C> out = h;
         if (SPECIAL && s >= n) out = Vec<C>{};
-        if (!SPECIAL || s < left) write_row<C>(y, out, put);
+        if (!SPECIAL || s < left) write_row<C, VEC>(y, out, lane, whole, channels);
     }
 }
 
-template <typename T, int C, int GATE>
+template <typename T, int C, bool VEC, int GATE>
 constexpr size_t forward_stage_bytes()
 {
-    return (size_t)inputs_of(GATE) * kTok * 32 * C * sizeof(T);
+    return (size_t)inputs_of(GATE) * kTok * Rows<T, 32 * C, VEC>::kPitch;
+}
+
+// A token's rows of the gate's inputs, by one thread.
+template <typename T, int C, bool VEC, int GATE>
+__device__ __forceinline__ void copy_inputs(const Args& g, const Tile& t, int m, unsigned char* stage, uint64_t* full)
+{
+    constexpr int kPitch = Rows<T, 32 * C, VEC>::kPitch;
+#pragma unroll
+    for (int n = 0; n < inputs_of(GATE); ++n) {
+        const T* base = (const T*)(n == 0 ? g.x : n == 1 ? g.f : g.i);
+        copy_row<T, VEC>(base + (t.row + m) * g.ld + t.d0, t.channels, base + (g.B * g.L - 1) * g.ld + g.D,
+                         stage + (n * kTok + m) * kPitch, full);
+    }
+}
+
+// c softplus(lam) of a manager's channels, and the tokens that start anew,
+// from values it has loaded.
+template <int K, int GATE, typename M>
+__device__ __forceinline__ void put_tile_data(const Args& g, M& mem, int st, const Tile& t, int m, const Vec<K>& lam,
+                                              bool reset)
+{
+    if (GATE == MRU_GATE_LRU) {
+#pragma unroll
+        for (int c = 0; c < K; ++c) mem.csp[st][K * m + c] = K * m + c < t.channels ? g.c * softplus(lam.v[c]) : 0.0f;
+    }
+    const uint32_t bits = __ballot_sync(~0u, reset && m < t.valid);
+    if (m % 32 == 0) mem.resets[st][m / 32] = bits;
+}
+
+template <typename T, int C, int GATE, bool VEC, bool PACK>
+__device__ __forceinline__ void forward_compute(const Args& g, TileMem<C>& mem, const unsigned char* stages)
+{
+    constexpr int NIN = inputs_of(GATE), CH = 32 * C;
+    constexpr size_t kBytes = forward_stage_bytes<T, C, VEC, GATE>();
+    const int lane = threadIdx.x & 31, w = threadIdx.x / 32;
+    const bool whole = g.D % C == 0 && aligned(g.y, C * sizeof(T));
+    const bool wide8 = PACK && g.D % C == 0 && aligned(g.x8.q, C) && aligned(g.f8.q, C) &&
+                       (GATE != MRU_GATE_LRU || aligned(g.i8.q, C));
+    for (uint32_t it = 0;; ++it) {
+        const int st = it & 1;
+        barrier_wait(g, &mem.full[st], it >> 1 & 1);
+        const Tile& t = mem.tile[it & 3];
+        if (t.ticket >= g.tiles) return;
+        const int n = min(max(t.valid - w * kStep, 0), kStep), left = t.tokens - w * kStep, channels = t.channels;
+        const uint32_t resets = mem.resets[st][w / 4] >> (w % 4 * kStep) & 0xffu;
+        const unsigned char* stage = stages + st * kBytes;
+        Rows<T, CH, VEC> in[NIN];
+        in[0] = Rows<T, CH, VEC>(stage, g.x, g.ld, t);
+        in[1] = Rows<T, CH, VEC>(stage + kTok * Rows<T, CH, VEC>::kPitch, g.f, g.ld, t);
+        if constexpr (NIN == 3) in[2] = Rows<T, CH, VEC>(stage + 2 * kTok * Rows<T, CH, VEC>::kPitch, g.i, g.ld, t);
+        if constexpr (PACK) pack_rows<T, C, VEC, NIN>(g, t, w, lane, in, wide8);
+        Vec<C> csp = {};
+        if (GATE == MRU_GATE_LRU) csp = read_row<C, VEC>(&mem.csp[st][0], lane);
+        const bool special = n < kStep || resets;
+        Vec<C> a[kStep], b[kStep];
+        Map<C> own;
+        if (special) own = local_map<T, C, VEC, GATE, true, false>(in, w, lane, csp, n, resets, a, b);
+        else if (GATE == MRU_GATE_LRU && all_near<C>(csp))
+            own = local_map<T, C, VEC, GATE, false, GATE == MRU_GATE_LRU>(in, w, lane, csp, n, resets, a, b);
+        else own = local_map<T, C, VEC, GATE, false, false>(in, w, lane, csp, n, resets, a, b);
+        put_map<C, VEC>(mem.map[w], lane, own);
+        T* y = (T*)g.y + (t.row + w * kStep) * g.D + t.d0;
+        meet_arrive<kMaps>();
+        meet<kCarry>();
+        const Vec<C> h = read_row<C, VEC>(&mem.state[w][0], lane);
+        if (special) run_states<T, C, VEC, GATE, true>(y, g.D, left, lane, h, n, resets, a, b, whole, channels);
+        else run_states<T, C, VEC, GATE, false>(y, g.D, left, lane, h, n, resets, a, b, whole, channels);
+    }
 }
 
 template <typename T, int C, int GATE, bool VEC>
-__device__ __forceinline__ void load_inputs(const Args& g, const Tile& t, T* to)
+__device__ __forceinline__ void forward_manage(const Args& g, TileMem<C>& mem, unsigned char* stages)
 {
-    constexpr int kIn = kTok * 32 * C;
-    load_tile<T, C, VEC>(t, g.x, g.ld, to);
-    load_tile<T, C, VEC>(t, g.f, g.ld, to + kIn);
-    if (GATE == MRU_GATE_LRU) load_tile<T, C, VEC>(t, g.i, g.ld, to + 2 * kIn);
+    constexpr int CH = 32 * C, K = CH / 64;
+    constexpr size_t kBytes = forward_stage_bytes<T, C, VEC, GATE>();
+    constexpr bool lru = GATE == MRU_GATE_LRU;
+    const int m = threadIdx.x - 32 * kWarps;
+    if (m == 0) {
+        uint32_t ticket = g.ticket ? atomicAdd(g.ticket, 1u) : blockIdx.x;
+        for (int k = 0; k < 3; ++k) {
+            find_tile<CH, false>(g, ticket, mem.tile[k]);
+            ticket = k < 2 ? draw(g, ticket) : ticket;
+        }
+    }
+    meet_managers();
+    auto reset_of = [&](const Tile& t) { return g.reset && t.ticket < g.tiles && m < t.tokens && g.reset[t.row + m]; };
+    auto lam_of = [&](const Tile& t) { return get_lane<K>(lru && t.ticket < g.tiles ? g.lam + t.d0 : nullptr, m, t.channels); };
+    auto copies = [&](const Tile& t, int st) {
+        if (t.ticket < g.tiles && m < t.tokens) copy_inputs<T, C, VEC, GATE>(g, t, m, stages + st * kBytes, &mem.full[st]);
+    };
+    for (int k = 0; k < 2; ++k) {
+        const Tile& t = mem.tile[k];
+        copies(t, k);
+        put_tile_data<K, GATE>(g, mem, k, t, m, lam_of(t), reset_of(t));
+        barrier_arrive(&mem.full[k]);
+    }
+    for (uint32_t it = 0;; ++it) {
+        const int st = it & 1;
+        const Tile& t = mem.tile[it & 3];
+        if (t.ticket >= g.tiles) return;
+        const Tile& coming = mem.tile[(it + 2) & 3];
+        // what can be asked for before the tile's maps are there
+        Search<CH> search(g, t, m);
+        Lookup<K> near, far;
+        near.ask(search.old_tiles(), search.j, CH);
+        far.ask(search.old_groups(), search.group, CH);
+        uint32_t drawn = 0;
+        if (m == 0) drawn = draw(g, coming.ticket);
+        const Vec<K> lam = lam_of(coming);
+        const bool reset = reset_of(coming);
+        const Vec<K> start = get_lane<K>(g.h0 && search.block == 0 ? g.h0 + t.b * g.D + t.d0 : nullptr, m, t.channels);
+        meet<kMaps>();
+        copies(coming, st);                                // the stage has been read
+        Map<K> own = Map<K>::of(1.0f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) own = lane_map<K>(mem.map[w], m).after(own);
+        if (!t.last && !(g.withhold && t.ticket == 0)) search.publish_tile(own);
+        const Vec<K> carry = search.carry(g, near, far, start);
+        Vec<K> h = carry;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            put_states<K>(mem.state[w], m, h);
+            h = lane_map<K>(mem.map[w], m)(h);
+        }
+        meet_arrive<kCarry>();
+        if (!t.last) search.publish_up(near, own, h);
+        else if (g.h_last) put_lane<K>(g.h_last + t.b * g.D + t.d0, h, m, t.channels);
+        if (g.states) put_lane<K>(g.states + t.k * g.D + t.d0, carry, m, t.channels);
+        put_tile_data<K, GATE>(g, mem, st, coming, m, lam, reset);
+        if (m == 0) find_tile<CH, false>(g, drawn, mem.tile[(it + 3) & 3]);
+        meet_managers();
+        barrier_arrive(&mem.full[st]);
+    }
 }
 
-// Forward: every input is read once and every output written once.  Blocks
-// stay and draw tiles in the order of the scan; the next tile's inputs are on
-// their way while one is worked on.  Per tile: each warp maps its 8 tokens,
-// the maps meet in shared memory, the tile's map is published, the carry is
-// fetched (by then the tiles before have published theirs), and the states
-// are run again from it over decays and inputs that stayed in registers.
 template <typename T, int C, int GATE, bool VEC, bool PACK>
-__global__ void __launch_bounds__(kThreads, C == 4 ? 2 : 3) k_gated_tile(Args g)
+__global__ void __launch_bounds__(kThreads, 2) k_gated_tile(Args g)
 {
     extern __shared__ __align__(16) unsigned char stages[];
-    __shared__ TileMem<C> mem;
-    constexpr int NIN = inputs_of(GATE), kCh = 32 * C, kElems = NIN * kTok * kCh;
-    constexpr bool lru = GATE == MRU_GATE_LRU;
-    T* stage = reinterpret_cast<T*>(stages);
-    const int tid = threadIdx.x, lane = tid & 31, w = tid / 32;
-    const bool whole = g.D % C == 0 && aligned(g.y, C * sizeof(T));
-    const bool wide8 = PACK && g.D % C == 0 && aligned(g.x8.q, C) && aligned(g.f8.q, C) && (!lru || aligned(g.i8.q, C));
-    if (tid == 0) {
-        const uint32_t first = g.ticket ? atomicAdd(g.ticket, 1u) : blockIdx.x;
-        find_tile<C, false>(g, first, mem.tile[0]);
-        find_tile<C, false>(g, draw(g, first), mem.tile[1]);
+    __shared__ __align__(16) TileMem<C> mem;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < 2; ++k) barrier_init(&mem.full[k], 32 * kManagers);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         if (!g.ticket && blockIdx.x == 0 && g.status) *g.status = 0;
     }
     __syncthreads();
-    if (mem.tile[0].ticket < g.tiles) {
-        const Tile& t = mem.tile[0];
-        load_inputs<T, C, GATE, VEC>(g, t, stage);
-        if (lru && tid < kCh) mem.csp[tid] = tid < t.channels ? g.c * softplus(g.lam[t.d0 + tid]) : 0.0f;
-    }
-    cp_commit();
-    for (int st = 0, now = 0; mem.tile[now].ticket < g.tiles; st ^= 1) {
-        const int then = now == 2 ? 0 : now + 1, later = then == 2 ? 0 : then + 1;
-        const Tile& t = mem.tile[now];
-        uint32_t drawn = 0;
-        float lam = 0.0f;
-        if (tid == 0) drawn = draw(g, mem.tile[then].ticket);
-        if (mem.tile[then].ticket < g.tiles) {
-            const Tile& u = mem.tile[then];
-            load_inputs<T, C, GATE, VEC>(g, u, stage + (st ^ 1) * kElems);
-            if (lru && tid < u.channels) lam = g.lam[u.d0 + tid];
-        }
-        cp_commit();
-        int n;
-        uint32_t resets;
-        warp_masks(g, t, w, lane, n, resets);
-        cp_wait<1>();
-        __syncthreads();
-        const T* in = stage + st * kElems;
-        if constexpr (PACK) pack_rows<T, C, NIN>(g, t, w, lane, in, wide8);
-        Vec<C> csp = {};
-        if (lru) csp = csp_of<C>(mem.csp, lane);
-        const bool special = n < kStep || resets;
-        Vec<C> a[kStep], b[kStep];
-        const T* rows = in + w * kStep * kCh + C * lane;
-        Map<C> own;
-        if (special) own = local_map<T, C, GATE, true, false>(rows, csp, n, resets, a, b);
-        else if (lru && all_near<C>(csp)) own = local_map<T, C, GATE, false, lru>(rows, csp, n, resets, a, b);
-        else own = local_map<T, C, GATE, false, false>(rows, csp, n, resets, a, b);
-        mem.agg[w].put(lane, own);
-        __syncthreads();
-        Map<C> pre = Map<C>::of(1.0f);
-        for (int v = 0; v < w; ++v) pre = mem.agg[v].get(lane).after(pre);
-        if (w == kWarps - 1) {
-            own = own.after(pre);                          // the tile's map
-            if (!t.last && !(g.withhold && t.ticket == 0)) publish<C>(tile_words<C>(g, t, t.order), lane, own);
-        }
-        mem.ent.fetch(g, t, w, lane, g.h0);
-        if (tid == 0) find_tile<C, false>(g, drawn, mem.tile[later]);
-        __syncthreads();
-        const Vec<C> carry = mem.ent.carry(t, lane);
-        const int channels = t.channels - C * lane;
-        if (w == kWarps - 1) {
-            mem.ent.publish_up(g, t, lane, own, carry);
-            if (t.last && g.h_last) write_state<C>(g.h_last + t.b * g.D + t.d0 + C * lane, own(carry), channels);
-        }
-        if (w == 0 && g.states) write_state<C>(g.states + t.k * g.D + t.d0 + C * lane, carry, channels);
-        T* y = (T*)g.y + (t.row + w * kStep) * g.D + t.d0 + C * lane;
-        const Put put = {whole && channels > 0, channels};
-        const int left = t.tokens - w * kStep;
-        if (special) run_states<T, C, GATE, true>(y, g.D, left, pre(carry), n, resets, a, b, put);
-        else run_states<T, C, GATE, false>(y, g.D, left, pre(carry), n, resets, a, b, put);
-        if (lru && tid < kCh) mem.csp[tid] = g.c * softplus(lam);
-        now = then;
-    }
+    if (threadIdx.x < 32 * kWarps) forward_compute<T, C, GATE, VEC, PACK>(g, mem, stages);
+    else forward_manage<T, C, GATE, VEC>(g, mem, stages);
 }
 
 // --------------------------------------------------------------- backward ---
 
 template <int C>
 struct BackMem {
-    MapRow<C> agg[kWarps];               // the warps' maps of states
-    MapRow<C> back[kWarps];              // and of gradients
-    Entries<C> ent;
+    float2 map[kWarps][32 * C];          // the warps' maps, of states and then of gradients
+    float state[kWarps][32 * C];         // the states before them, then the gradients behind them
     float dlam[kWarps][32 * C];
-    float csp[32 * C];
-    float state[2][32 * C];              // the kept state before the tile
+    float csp[2][32 * C];
     float scale[2][3][kTok];             // 8-bit copies: the scale of a token's run
-    Tile tile[3];
+    uint32_t resets[2][2];
+    Tile tile[4];
+    uint64_t full[2];
 };
 
-template <typename T, int C, int GATE, bool PACKED>
-constexpr size_t backward_stage_bytes()
-{
-    return (size_t)kTok * 32 * C * (inputs_of(GATE) * (PACKED ? 1 : sizeof(T)) + sizeof(T));
-}
-// Two stages where two blocks of them fit an SM's 227 KB, else one.
-template <typename T, int C, int GATE, bool PACKED>
-constexpr int backward_stages()
-{
-    return backward_stage_bytes<T, C, GATE, PACKED>() <= 48 * 1024 ? 2 : 1;
-}
+// A stage: dy, then the inputs.
+template <typename T, int C, bool VEC, bool PACKED>
+struct BackStage {
+    using V = typename std::conditional<PACKED, int8_t, T>::type;
+    static constexpr int CH = 32 * C, kDy = kTok * Rows<T, CH, VEC>::kPitch, kIn = kTok * Rows<V, CH, VEC>::kPitch;
+    static constexpr size_t bytes(int inputs) { return (size_t)kDy + (size_t)inputs * kIn; }
+};
 
-template <typename T, int C, int GATE, bool VEC, bool PACKED>
-__device__ __forceinline__ void load_back(const Args& g, const Tile& t, unsigned char* stage, BackMem<C>& mem, int st)
+// A lane's channels of a token's input, at their scale.
+template <int C, bool VEC, bool PACKED, typename R>
+__device__ __forceinline__ Vec<C> input_row(const R& in, const float* scale, int row, int lane)
 {
-    static_assert(!PACKED || C == 2, "a tile's row is one run of 64 channels");
-    constexpr int NIN = inputs_of(GATE), kCh = 32 * C;
-    T* dy = reinterpret_cast<T*>(stage);
-    load_tile<T, C, VEC>(t, g.dy, g.D, dy);
-    const int tid = threadIdx.x;
+    Vec<C> v = read_row<C, VEC>(in.row(row), lane);
     if constexpr (PACKED) {
-        int8_t* q = reinterpret_cast<int8_t*>(dy + kTok * kCh);
-        const int64_t runs = g.cgs;
 #pragma unroll
-        for (int n = 0; n < NIN; ++n) {
-            const mru_packed8& h = n == 0 ? g.x8 : n == 1 ? g.f8 : g.i8;
-            const int8_t* src = h.q + t.row * g.D + t.d0;
-            if constexpr (VEC) {
-                constexpr int chunks = kCh / 16;
-                for (int k = tid; k < kTok * chunks; k += kThreads) {
-                    const int row = k / chunks, c = k % chunks * 16;
-                    const bool in = row < t.tokens && c < t.channels;
-                    cp_async(q + (n * kTok + row) * kCh + c, in ? src + row * g.D + c : h.q, in ? 16 : 0);
-                }
-            } else {
-                for (int k = tid; k < kTok * kCh; k += kThreads) {
-                    const int row = k / kCh, c = k % kCh;
-                    q[n * kTok * kCh + k] = row < t.tokens && c < t.channels ? src[row * g.D + c] : (int8_t)0;
-                }
-            }
-            if (tid < kTok) {
-                const bool in = tid < t.tokens;
-                cp_async4(&mem.scale[st][n][tid], in ? h.scale + (t.row + tid) * runs + t.d0 / 64 : h.scale, in ? 4 : 0);
-            }
-        }
-    } else {
-        load_inputs<T, C, GATE, VEC>(g, t, dy + kTok * kCh);
+        for (int c = 0; c < C; ++c) v.v[c] *= scale[row];
     }
-    if (tid < kCh) {
-        const bool in = tid < t.channels;
-        cp_async4(&mem.state[st][tid], in ? g.states + t.k * g.D + t.d0 + tid : g.states, in ? 4 : 0);
-    }
-}
-
-// A lane's channels of a token's input n, from the stage.
-template <typename T, int C, bool PACKED>
-__device__ __forceinline__ Vec<C> input_row(const unsigned char* stage, const float (&scale)[3][kTok], int n, int row,
-                                            int lane)
-{
-    constexpr int kCh = 32 * C;
-    const unsigned char* in = stage + kTok * kCh * sizeof(T);
-    if constexpr (PACKED) {
-        const char2 q = *reinterpret_cast<const char2*>(in + (n * kTok + row) * kCh + C * lane);
-        const float k = scale[n][row];
-        return Vec<C>{(float)(signed char)q.x * k, (float)(signed char)q.y * k};
-    } else {
-        return read_row<C>(reinterpret_cast<const T*>(in) + (n * kTok + row) * kCh + C * lane);
-    }
+    return v;
 }
 
 // The map of a warp's tokens; a and, for the sigmoid gate, cx = 1 - a stay.
-template <typename T, int C, int GATE, bool PACKED, bool NEAR>
-__device__ __forceinline__ Map<C> back_map(const unsigned char* stage, const float (&scale)[3][kTok], int w, int lane,
+template <int C, bool VEC, int GATE, bool PACKED, bool NEAR, typename R>
+__device__ __forceinline__ Map<C> back_map(const R (&in)[inputs_of(GATE)], const float (&scale)[3][kTok], int w, int lane,
                                            const Vec<C>& csp, int n, uint32_t resets, Vec<C> (&a)[kStep],
                                            Vec<C> (&cx)[kStep])
 {
@@ -491,10 +549,10 @@ __device__ __forceinline__ Map<C> back_map(const unsigned char* stage, const flo
         }
         if (s >= n) continue;
         const int row = w * kStep + s;
-        const Vec<C> x = input_row<T, C, PACKED>(stage, scale, 0, row, lane);
-        const Vec<C> f = input_row<T, C, PACKED>(stage, scale, 1, row, lane);
+        const Vec<C> x = input_row<C, VEC, PACKED>(in[0], scale[0], row, lane);
+        const Vec<C> f = input_row<C, VEC, PACKED>(in[1], scale[1], row, lane);
         Vec<C> i = x;
-        if (GATE == MRU_GATE_LRU) i = input_row<T, C, PACKED>(stage, scale, 2, row, lane);
+        if constexpr (GATE == MRU_GATE_LRU) i = input_row<C, VEC, PACKED>(in[2], scale[2], row, lane);
         if (resets >> s & 1) m = Map<C>::of(0.0f);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -506,7 +564,7 @@ __device__ __forceinline__ Map<C> back_map(const unsigned char* stage, const flo
                 gates<GATE, NEAR>(x.v[c], f.v[c], i.v[c], csp.v[c], a[s].v[c], b);
             }
             m.P[c] *= a[s].v[c];
-            m.H[c] = carry_in(a[s].v[c], m.H[c]) + b;
+            m.H[c] = GATE == MRU_GATE_DECAY ? carry_in(a[s].v[c], m.H[c]) + b : fmaf(a[s].v[c], m.H[c], b);
         }
     }
     return m;
@@ -515,25 +573,24 @@ __device__ __forceinline__ Map<C> back_map(const unsigned char* stage, const flo
 // A warp's tokens: states from h, the factors of the gradients, and the map of
 // gradients e -> P e + E from the token after the last to before the first.
 // dl: sum q d and sum q dd/de (for lam) at e = 0, without the first token where
-// it is a piece's edge (k_gated_edge counts it).  h: the state after the last.
-template <typename T, int C, int GATE, bool PACKED, bool NEAR>
-__device__ __forceinline__ Map<C> back_factors(const unsigned char* stage, const float (&scale)[3][kTok], int w,
-                                               int lane, const Vec<C>& csp, Vec<C>& h, int n, uint32_t resets,
-                                               bool edge, Vec<C> (&a)[kStep], Vec<C> (&cx)[kStep],
+// it is a piece's edge (k_gated_edge counts it).
+template <typename T, int C, bool VEC, int GATE, bool PACKED, bool NEAR, typename R>
+__device__ __forceinline__ Map<C> back_factors(const R (&in)[inputs_of(GATE)], const Rows<T, 32 * C, VEC>& dys,
+                                               const float (&scale)[3][kTok], int w, int lane, const Vec<C>& csp, Vec<C> h,
+                                               int n, uint32_t resets, bool edge, Vec<C> (&a)[kStep], Vec<C> (&cx)[kStep],
                                                Vec<C> (&cf)[kStep], Vec<C> (&ci)[kStep], Vec<C>& dl0, Vec<C>& dl1)
 {
-    constexpr int kCh = 32 * C;
     Vec<C> q[kStep];
 #pragma unroll
     for (int s = 0; s < kStep; ++s) {
         cf[s] = ci[s] = q[s] = Vec<C>{};
         if (s >= n) continue;
         const int row = w * kStep + s;
-        const Vec<C> x = input_row<T, C, PACKED>(stage, scale, 0, row, lane);
+        const Vec<C> x = input_row<C, VEC, PACKED>(in[0], scale[0], row, lane);
         Vec<C> f = x, i = x;
-        if (GATE == MRU_GATE_LRU) {
-            f = input_row<T, C, PACKED>(stage, scale, 1, row, lane);
-            i = input_row<T, C, PACKED>(stage, scale, 2, row, lane);
+        if constexpr (GATE == MRU_GATE_LRU) {
+            f = input_row<C, VEC, PACKED>(in[1], scale[1], row, lane);
+            i = input_row<C, VEC, PACKED>(in[2], scale[2], row, lane);
         }
         const bool reset = resets >> s & 1;
         if (reset) h = Vec<C>{};
@@ -543,14 +600,16 @@ __device__ __forceinline__ Map<C> back_factors(const unsigned char* stage, const
             if (GATE == MRU_GATE_DECAY) {
                 b = x.v[c];
                 cf[s].v[c] = h.v[c];
+                h.v[c] = carry_in(a[s].v[c], h.v[c]) + b;
             } else if (GATE == MRU_GATE_SIGMOID) {
                 b = cx[s].v[c] * x.v[c];
                 cf[s].v[c] = a[s].v[c] * cx[s].v[c] * (h.v[c] - x.v[c]);
+                h.v[c] = fmaf(a[s].v[c], h.v[c], b);
             } else {
                 gradient_factors<GATE, NEAR>(x.v[c], f.v[c], i.v[c], csp.v[c], h.v[c], a[s].v[c], b, cx[s].v[c],
                                              cf[s].v[c], ci[s].v[c], q[s].v[c]);
+                h.v[c] = fmaf(a[s].v[c], h.v[c], b);
             }
-            h.v[c] = carry_in(a[s].v[c], h.v[c]) + b;
             if (reset) a[s].v[c] = 0.0f;
         }
     }
@@ -560,7 +619,7 @@ __device__ __forceinline__ Map<C> back_factors(const unsigned char* stage, const
 #pragma unroll
     for (int s = kStep - 1; s >= 0; --s) {
         if (s >= n) continue;
-        const Vec<C> dy = read_row<C>(reinterpret_cast<const T*>(stage) + (w * kStep + s) * kCh + C * lane);
+        const Vec<C> dy = read_row<C, VEC>(dys.row(w * kStep + s), lane);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const float d = m.H[c] + dy.v[c];
@@ -575,134 +634,210 @@ __device__ __forceinline__ Map<C> back_factors(const unsigned char* stage, const
     return m;
 }
 
-// Backward, tiles from the last to the first: the states of the tile again
-// from its kept state, the factors of the gradients, then the gradient's own
-// recurrence with its carry from the later tiles, as the forward's.
 template <typename T, int C, int GATE, bool VEC, bool PACKED>
-__global__ void __launch_bounds__(kThreads, 2) k_gated_tile_bwd(Args g)
+__device__ __forceinline__ void backward_compute(const Args& g, BackMem<C>& mem, const unsigned char* stages)
 {
-    extern __shared__ __align__(16) unsigned char stages[];
-    __shared__ BackMem<C> mem;
-    constexpr int kCh = 32 * C;
-    constexpr size_t kBytes = backward_stage_bytes<T, C, GATE, PACKED>();
-    constexpr int STAGES = backward_stages<T, C, GATE, PACKED>();
+    using Stage = BackStage<T, C, VEC, PACKED>;
+    using V = typename Stage::V;
+    constexpr int NIN = inputs_of(GATE), CH = 32 * C;
     constexpr bool lru = GATE == MRU_GATE_LRU;
-    const int tid = threadIdx.x, lane = tid & 31, w = tid / 32;
+    const int lane = threadIdx.x & 31, w = threadIdx.x / 32;
     const bool whole = g.D % C == 0 && g.ldg % C == 0 && aligned(g.dx, C * sizeof(T)) && aligned(g.df, C * sizeof(T)) &&
                        (!lru || aligned(g.di, C * sizeof(T)));
-    if (tid == 0) {
-        const uint32_t first = g.ticket ? atomicAdd(g.ticket, 1u) : blockIdx.x;
-        find_tile<C, true>(g, first, mem.tile[0]);
-        find_tile<C, true>(g, draw(g, first), mem.tile[1]);
-        if (!g.ticket && blockIdx.x == 0 && g.status) *g.status = 0;
-    }
-    __syncthreads();
-    if (mem.tile[0].ticket < g.tiles) {
-        const Tile& t = mem.tile[0];
-        if (STAGES == 2) load_back<T, C, GATE, VEC, PACKED>(g, t, stages, mem, 0);
-        if (lru && tid < kCh) mem.csp[tid] = tid < t.channels ? g.c * softplus(g.lam[t.d0 + tid]) : 0.0f;
-    }
-    cp_commit();
-    for (int st = 0, now = 0; mem.tile[now].ticket < g.tiles; st ^= 1) {
-        const int then = now == 2 ? 0 : now + 1, later = then == 2 ? 0 : then + 1;
-        const Tile& t = mem.tile[now];
-        unsigned char* stage = stages + (STAGES == 2 ? st * kBytes : 0);
-        uint32_t drawn = 0;
-        float lam = 0.0f;
-        if (tid == 0) drawn = draw(g, mem.tile[then].ticket);
-        if (STAGES == 1) load_back<T, C, GATE, VEC, PACKED>(g, t, stage, mem, st);
-        if (mem.tile[then].ticket < g.tiles) {
-            const Tile& u = mem.tile[then];
-            if (STAGES == 2) load_back<T, C, GATE, VEC, PACKED>(g, u, stages + (st ^ 1) * kBytes, mem, st ^ 1);
-            if (lru && tid < u.channels) lam = g.lam[u.d0 + tid];
-        }
-        cp_commit();
-        int n;
-        uint32_t resets;
-        warp_masks(g, t, w, lane, n, resets);
-        cp_wait<STAGES - 1>();
-        __syncthreads();
+    const int64_t ld = PACKED ? g.D : g.ld;
+    for (uint32_t it = 0;; ++it) {
+        const int st = it & 1;
+        barrier_wait(g, &mem.full[st], it >> 1 & 1);
+        const Tile& t = mem.tile[it & 3];
+        if (t.ticket >= g.tiles) break;
+        const int n = min(max(t.valid - w * kStep, 0), kStep), left = t.tokens - w * kStep, channels = t.channels;
+        const uint32_t resets = mem.resets[st][w / 4] >> (w % 4 * kStep) & 0xffu;
+        const bool edge = PACKED && w == 0 && t.row % g.L > 0;
+        const unsigned char* stage = stages + st * Stage::bytes(NIN);
+        const Rows<T, CH, VEC> dys(stage, g.dy, g.D, t);
+        const void *px = PACKED ? (const void*)g.x8.q : g.x, *pf = PACKED ? (const void*)g.f8.q : g.f;
+        Rows<V, CH, VEC> in[NIN];
+        in[0] = Rows<V, CH, VEC>(stage + Stage::kDy, px, ld, t);
+        in[1] = Rows<V, CH, VEC>(stage + Stage::kDy + Stage::kIn, pf, ld, t);
+        if constexpr (NIN == 3)
+            in[2] = Rows<V, CH, VEC>(stage + Stage::kDy + 2 * Stage::kIn, PACKED ? (const void*)g.i8.q : g.i, ld, t);
         Vec<C> csp = {};
-        if (lru) csp = csp_of<C>(mem.csp, lane);
+        if (lru) csp = read_row<C, VEC>(&mem.csp[st][0], lane);
         const bool near = lru && all_near<C>(csp);
-        Vec<C> a[kStep], cx[kStep], cf[kStep], ci[kStep];
-        mem.agg[w].put(lane, near ? back_map<T, C, GATE, PACKED, lru>(stage, mem.scale[st], w, lane, csp, n, resets, a, cx)
-                                  : back_map<T, C, GATE, PACKED, false>(stage, mem.scale[st], w, lane, csp, n, resets, a,
-                                                                        cx));
-        __syncthreads();
-        Vec<C> h = read_row<C>(&mem.state[st][C * lane]), dl0, dl1;
-        for (int v = 0; v < w; ++v) h = mem.agg[v].get(lane)(h);
-        const bool edge = PACKED && w == 0 && t.k % g.K > 0;
-        Map<C> own = near ? back_factors<T, C, GATE, PACKED, lru>(stage, mem.scale[st], w, lane, csp, h, n, resets, edge,
-                                                                  a, cx, cf, ci, dl0, dl1)
-                          : back_factors<T, C, GATE, PACKED, false>(stage, mem.scale[st], w, lane, csp, h, n, resets,
-                                                                    edge, a, cx, cf, ci, dl0, dl1);
-        mem.back[w].put(lane, own);
-        __syncthreads();
-        Map<C> post = Map<C>::of(1.0f);
-        for (int v = kWarps - 1; v > w; --v) post = mem.back[v].get(lane).after(post);
-        if (w == 0) {
-            own = own.after(post);                         // the tile's map
-            if (!t.last && !(g.withhold && t.ticket == 0)) publish<C>(tile_words<C>(g, t, t.order), lane, own);
-        }
-        mem.ent.fetch(g, t, w, lane, g.dh_last);
-        if (tid == 0) find_tile<C, true>(g, drawn, mem.tile[later]);
-        __syncthreads();
-        const Vec<C> carry = mem.ent.carry(t, lane);
-        const int channels = t.channels - C * lane;
-        if (w == 0) {
-            mem.ent.publish_up(g, t, lane, own, carry);
-            if (t.last && g.dh0) write_state<C>(g.dh0 + t.b * g.D + t.d0 + C * lane, own(carry), channels);
-        }
-        if (PACKED && g.edge_h && w == kWarps - 1 && t.order > 0)
-            write_state<C>(g.edge_h + (t.k + 1) * g.D + t.d0 + C * lane, h, channels);
-        Vec<C> e = post(carry);
+        Vec<C> a[kStep], cx[kStep], cf[kStep], ci[kStep], dl0, dl1;
+        put_map<C, VEC>(mem.map[w], lane,
+                        near ? back_map<C, VEC, GATE, PACKED, lru>(in, mem.scale[st], w, lane, csp, n, resets, a, cx)
+                             : back_map<C, VEC, GATE, PACKED, false>(in, mem.scale[st], w, lane, csp, n, resets, a, cx));
+        meet_arrive<kMaps>();
+        meet<kStates>();
+        const Vec<C> h = read_row<C, VEC>(&mem.state[w][0], lane);
+        put_map<C, VEC>(mem.map[w], lane,
+                        near ? back_factors<T, C, VEC, GATE, PACKED, lru>(in, dys, mem.scale[st], w, lane, csp, h, n, resets,
+                                                                          edge, a, cx, cf, ci, dl0, dl1)
+                             : back_factors<T, C, VEC, GATE, PACKED, false>(in, dys, mem.scale[st], w, lane, csp, h, n, resets,
+                                                                            edge, a, cx, cf, ci, dl0, dl1));
+        int64_t at = (t.row + w * kStep + kStep - 1) * g.ldg + t.d0;
+        const int64_t edge_at = t.k * g.D + t.d0;
+        meet_arrive<kBack>();
+        meet<kCarry>();
+        Vec<C> e = read_row<C, VEC>(&mem.state[w][0], lane);
         if (lru) {
 #pragma unroll
-            for (int c = 0; c < C; ++c) mem.dlam[w][C * lane + c] = fmaf(dl1.v[c], e.v[c], dl0.v[c]);
+            for (int c = 0; c < C; ++c) mem.dlam[w][channel<C, VEC>(lane, c)] = fmaf(dl1.v[c], e.v[c], dl0.v[c]);
         }
-        const int left = t.tokens - w * kStep;
-        const Put put = {whole && channels > 0, channels};
-        int64_t at = (t.row + w * kStep + kStep - 1) * g.ldg + t.d0 + C * lane;
 #pragma unroll
         for (int s = kStep - 1; s >= 0; --s, at -= g.ldg) {
             if (s >= left) continue;
-            Vec<C> d = {};
+            Vec<C> d = {}, o;
             if (s < n) {
-                d = read_row<C>(reinterpret_cast<const T*>(stage) + (w * kStep + s) * kCh + C * lane);
+                d = read_row<C, VEC>(dys.row(w * kStep + s), lane);
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     d.v[c] += e.v[c];
                     e.v[c] = carry_in(a[s].v[c], d.v[c]);
                 }
             }
-            if (PACKED && s == 0 && edge) write_state<C>(g.edge_d + t.k * g.D + t.d0 + C * lane, d, channels);
-            Vec<C> o;
-            if (GATE == MRU_GATE_DECAY) {
-                write_row<C>((T*)g.dx + at, d, put);
-            } else {
+            if (PACKED && s == 0 && edge) write_row<C, VEC>(g.edge_d + edge_at, d, lane, false, channels);
 #pragma unroll
-                for (int c = 0; c < C; ++c) o.v[c] = cx[s].v[c] * d.v[c];
-                write_row<C>((T*)g.dx + at, o, put);
-            }
+            for (int c = 0; c < C; ++c) o.v[c] = GATE == MRU_GATE_DECAY ? d.v[c] : cx[s].v[c] * d.v[c];
+            write_row<C, VEC>((T*)g.dx + at, o, lane, whole, channels);
 #pragma unroll
             for (int c = 0; c < C; ++c) o.v[c] = cf[s].v[c] * d.v[c];
-            write_row<C>((T*)g.df + at, o, put);
+            write_row<C, VEC>((T*)g.df + at, o, lane, whole, channels);
             if (lru) {
 #pragma unroll
                 for (int c = 0; c < C; ++c) o.v[c] = ci[s].v[c] * d.v[c];
-                write_row<C>((T*)g.di + at, o, put);
+                write_row<C, VEC>((T*)g.di + at, o, lane, whole, channels);
             }
         }
-        if (lru && tid < kCh) mem.csp[tid] = g.c * softplus(lam);
-        __syncthreads();                                   // the stage may be filled again
-        if (lru && g.dlam_part && tid < t.channels) {
-            float s = 0.0f;
-            for (int v = 0; v < kWarps; ++v) s += mem.dlam[v][tid];
-            g.dlam_part[t.k * g.D + t.d0 + tid] = s;
-        }
-        now = then;
     }
+    meet_arrive<kMaps>();                                  // the last tile's part of dlam is there
+}
+
+template <typename T, int C, int GATE, bool VEC, bool PACKED>
+__device__ __forceinline__ void backward_manage(const Args& g, BackMem<C>& mem, unsigned char* stages)
+{
+    using Stage = BackStage<T, C, VEC, PACKED>;
+    constexpr int NIN = inputs_of(GATE), CH = 32 * C, K = CH / 64;
+    static_assert(!PACKED || C == 2, "a tile's row is one run of 64 channels");
+    constexpr bool lru = GATE == MRU_GATE_LRU;
+    const int m = threadIdx.x - 32 * kWarps;
+    if (m == 0) {
+        const uint32_t ticket = g.ticket ? atomicAdd(g.ticket, 1u) : blockIdx.x;
+        find_tile<CH, true>(g, ticket, mem.tile[0]);
+        find_tile<CH, true>(g, draw(g, ticket), mem.tile[1]);
+    }
+    meet_managers();
+    auto valid = [&](const Tile& t) { return t.ticket < g.tiles; };
+    auto reset_of = [&](const Tile& t) { return g.reset && valid(t) && m < t.tokens && g.reset[t.row + m]; };
+    auto lam_of = [&](const Tile& t) { return get_lane<K>(lru && valid(t) ? g.lam + t.d0 : nullptr, m, t.channels); };
+    auto state_of = [&](const Tile& t) {
+        return get_lane<K>(valid(t) ? g.states + t.k * g.D + t.d0 : nullptr, m, t.channels);
+    };
+    auto scale_of = [&](const Tile& t, int n) {
+        const mru_packed8& h = n == 0 ? g.x8 : n == 1 ? g.f8 : g.i8;
+        return PACKED && valid(t) && m < t.tokens ? h.scale[(t.row + m) * (int64_t)g.cgs + t.d0 / 64] : 0.0f;
+    };
+    auto copies = [&](const Tile& t, int st) {
+        if (!valid(t) || m >= t.tokens) return;
+        unsigned char* stage = stages + st * Stage::bytes(NIN);
+        const T* dy = (const T*)g.dy;
+        copy_row<T, VEC>(dy + (t.row + m) * g.D + t.d0, t.channels, dy + g.B * g.L * g.D,
+                         stage + m * Rows<T, CH, VEC>::kPitch, &mem.full[st]);
+        if constexpr (PACKED) {
+#pragma unroll
+            for (int n = 0; n < NIN; ++n) {
+                const int8_t* q = n == 0 ? g.x8.q : n == 1 ? g.f8.q : g.i8.q;
+                copy_row<int8_t, VEC>(q + (t.row + m) * g.D + t.d0, t.channels, q + g.B * g.L * g.D,
+                                      stage + Stage::kDy + n * Stage::kIn + m * Rows<int8_t, CH, VEC>::kPitch, &mem.full[st]);
+            }
+        } else {
+            copy_inputs<T, C, VEC, GATE>(g, t, m, stage + Stage::kDy, &mem.full[st]);
+        }
+    };
+    copies(mem.tile[0], 0);
+    put_tile_data<K, GATE>(g, mem, 0, mem.tile[0], m, lam_of(mem.tile[0]), reset_of(mem.tile[0]));
+#pragma unroll
+    for (int n = 0; n < NIN; ++n) mem.scale[0][n][m] = scale_of(mem.tile[0], n);
+    Vec<K> state = state_of(mem.tile[0]);
+    barrier_arrive(&mem.full[0]);
+    // the sums over a tile's warps for dlam, once its compute warps are through
+    auto flush = [&](const Tile& t) {
+        if (!lru || !g.dlam_part) return;
+        Vec<K> s = {};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+            for (int c = 0; c < K; ++c) s.v[c] += mem.dlam[w][K * m + c];
+        put_lane<K>(g.dlam_part + t.k * g.D + t.d0, s, m, t.channels);
+    };
+    uint32_t it = 0;
+    for (;; ++it) {
+        const int st = (it + 1) & 1;                       // the next tile's stage
+        const Tile& t = mem.tile[it & 3];
+        if (t.ticket >= g.tiles) break;
+        const Tile& coming = mem.tile[(it + 1) & 3];
+        Search<CH> search(g, t, m);
+        Lookup<K> near, far;
+        near.ask(search.old_tiles(), search.j, CH);
+        far.ask(search.old_groups(), search.group, CH);
+        uint32_t drawn = 0;
+        if (m == 0) drawn = draw(g, coming.ticket);
+        const Vec<K> lam = lam_of(coming), next = state_of(coming);
+        const bool reset = reset_of(coming);
+        float scale[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int n = 0; n < NIN; ++n) scale[n] = scale_of(coming, n);
+        const Vec<K> start = get_lane<K>(g.dh_last && search.block == 0 ? g.dh_last + t.b * g.D + t.d0 : nullptr, m, t.channels);
+        meet<kMaps>();                                     // the tile before is through
+        copies(coming, st);
+        if (it > 0) flush(mem.tile[(it - 1) & 3]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            put_states<K>(mem.state[w], m, state);
+            state = lane_map<K>(mem.map[w], m)(state);
+        }
+        meet_arrive<kStates>();
+        if (PACKED && g.edge_h && t.order > 0) put_lane<K>(g.edge_h + (t.k + 1) * g.D + t.d0, state, m, t.channels);
+        put_tile_data<K, GATE>(g, mem, st, coming, m, lam, reset);
+#pragma unroll
+        for (int n = 0; n < NIN; ++n) mem.scale[st][n][m] = scale[n];
+        state = next;
+        meet<kBack>();
+        Map<K> own = Map<K>::of(1.0f);
+#pragma unroll
+        for (int w = kWarps - 1; w >= 0; --w) own = lane_map<K>(mem.map[w], m).after(own);
+        if (!t.last && !(g.withhold && t.ticket == 0)) search.publish_tile(own);
+        Vec<K> e = search.carry(g, near, far, start);
+#pragma unroll
+        for (int w = kWarps - 1; w >= 0; --w) {
+            put_states<K>(mem.state[w], m, e);
+            e = lane_map<K>(mem.map[w], m)(e);
+        }
+        meet_arrive<kCarry>();
+        if (!t.last) search.publish_up(near, own, e);
+        else if (g.dh0) put_lane<K>(g.dh0 + t.b * g.D + t.d0, e, m, t.channels);
+        if (m == 0) find_tile<CH, true>(g, drawn, mem.tile[(it + 2) & 3]);
+        meet_managers();
+        barrier_arrive(&mem.full[st]);
+    }
+    meet<kMaps>();
+    if (it > 0) flush(mem.tile[(it - 1) & 3]);
+}
+
+template <typename T, int C, int GATE, bool VEC, bool PACKED>
+__global__ void __launch_bounds__(kThreads, 2) k_gated_tile_bwd(Args g)
+{
+    extern __shared__ __align__(16) unsigned char stages[];
+    __shared__ __align__(16) BackMem<C> mem;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < 2; ++k) barrier_init(&mem.full[k], 32 * kManagers);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (!g.ticket && blockIdx.x == 0 && g.status) *g.status = 0;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32 * kWarps) backward_compute<T, C, GATE, VEC, PACKED>(g, mem, stages);
+    else backward_manage<T, C, GATE, VEC, PACKED>(g, mem, stages);
 }
 
 // With 8-bit copies the states run in pieces of 64 tokens from the kept states,
@@ -810,9 +945,9 @@ struct Layout {
     uint32_t tiles, cols, cgs, groups, blocks;
 };
 constexpr size_t kControl = 256;
-Layout layout(const mru_gated_problem& p, bool backward)
+Layout layout(const mru_gated_problem& p, bool backward, bool vec)
 {
-    const int64_t kCh = 32 * (backward ? kBwdC : fwd_channels(elem_size(p.dtype)));
+    const int64_t kCh = 32 * (backward ? kBwdC : fwd_channels(elem_size(p.dtype), vec));
     Layout W;
     memset(&W, 0, sizeof W);
     const int64_t K = div_up(p.L, kKeep);
@@ -908,14 +1043,14 @@ struct Forward {
             k_gated_short<T, GATE><<<(unsigned)div_up(g.B * g.D, 128), 128, 0, s>>>(g);
             return cudaGetLastError();
         }
-        constexpr int C = fwd_channels(sizeof(T));
-        constexpr size_t smem = 2 * forward_stage_bytes<T, C, GATE>();
         static Fits fits[4];
+        constexpr int C = fwd_channels(sizeof(T), true);
+        constexpr size_t smem = 2 * forward_stage_bytes<T, C, true, GATE>(), odd = 2 * forward_stage_bytes<T, 2, false, GATE>();
         if (vec)
             return pack ? launch_tiles(k_gated_tile<T, C, GATE, true, true>, fits[0], g, smem, s)
                         : launch_tiles(k_gated_tile<T, C, GATE, true, false>, fits[1], g, smem, s);
-        return pack ? launch_tiles(k_gated_tile<T, C, GATE, false, true>, fits[2], g, smem, s)
-                    : launch_tiles(k_gated_tile<T, C, GATE, false, false>, fits[3], g, smem, s);
+        return pack ? launch_tiles(k_gated_tile<T, 2, GATE, false, true>, fits[2], g, odd, s)
+                    : launch_tiles(k_gated_tile<T, 2, GATE, false, false>, fits[3], g, odd, s);
     }
 };
 
@@ -930,11 +1065,13 @@ struct Backward {
             k_gated_short_bwd<T, GATE, PACKED><<<(unsigned)div_up(g.B * g.D, 128), 128, 0, s>>>(g);
             return cudaGetLastError();
         }
-        constexpr int C = kBwdC;
-        constexpr size_t smem = backward_stages<T, C, GATE, PACKED>() * backward_stage_bytes<T, C, GATE, PACKED>();
+        constexpr int C = kBwdC, NIN = inputs_of(GATE);
         static Fits fits[2];
-        const cudaError_t e = vec ? launch_tiles(k_gated_tile_bwd<T, C, GATE, true, PACKED>, fits[0], g, smem, s)
-                                  : launch_tiles(k_gated_tile_bwd<T, C, GATE, false, PACKED>, fits[1], g, smem, s);
+        const cudaError_t e =
+            vec ? launch_tiles(k_gated_tile_bwd<T, C, GATE, true, PACKED>, fits[0], g,
+                               2 * BackStage<T, C, true, PACKED>::bytes(NIN), s)
+                : launch_tiles(k_gated_tile_bwd<T, C, GATE, false, PACKED>, fits[1], g,
+                               2 * BackStage<T, C, false, PACKED>::bytes(NIN), s);
         if (e != cudaSuccess || !g.edge_h) return e;
         k_gated_edge<T, GATE><<<(unsigned)div_up(g.B * (g.K - 1) * g.D, 128), 128, 0, s>>>(g);
         return cudaGetLastError();
@@ -955,12 +1092,15 @@ extern "C" {
 
 size_t mru_gated_workspace_size(const mru_gated_problem* p)
 {
-    return check_problem(p) == MRU_OK ? layout(*p, false).bytes : 0;
+    if (check_problem(p) != MRU_OK) return 0;
+    // for either column layout
+    const size_t a = layout(*p, false, false).bytes, b = layout(*p, false, true).bytes;
+    return a > b ? a : b;
 }
 
 size_t mru_gated_backward_workspace_size(const mru_gated_problem* p)
 {
-    return check_problem(p) == MRU_OK ? layout(*p, true).bytes : 0;
+    return check_problem(p) == MRU_OK ? layout(*p, true, true).bytes : 0;
 }
 
 mru_status mru_gated_scan(const mru_gated_problem* p, const mru_gated_inputs* in, void* y, float* h_last,
@@ -1005,8 +1145,9 @@ mru_status mru_gated_scan(const mru_gated_problem* p, const mru_gated_inputs* in
         }
     }
     if (b.clash()) return MRU_ERR_INVALID_ARG;
-    const Layout W = layout(*p, false);
-    if (ws && ws_bytes < W.bytes) return MRU_ERR_WORKSPACE;
+    const bool vec = width % 16 == 0 && pitch % 16 == 0 && aligned(g.x, 16) && aligned(g.f, 16) && aligned(g.i, 16);
+    const Layout W = layout(*p, false, vec);
+    if (ws && ws_bytes < mru_gated_workspace_size(p)) return MRU_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     if (ws && (!any || g.K > 1)) e = cudaMemsetAsync(ws, 0, W.zeroed, s);   // else the kernel clears the status word
@@ -1018,7 +1159,6 @@ mru_status mru_gated_scan(const mru_gated_problem* p, const mru_gated_inputs* in
     g.states = saved ? saved->states : nullptr;
     const bool here = pack && p->L > kShort;                        // copies in the same pass
     if (here) { g.x8 = saved->x; g.f8 = saved->f; g.i8 = saved->i; }
-    const bool vec = pitch % 16 == 0 && aligned(g.x, 16) && aligned(g.f, 16) && aligned(g.i, 16);
     e = by_type(p->dtype, p->gate, Forward{g, vec, here, s});
     if (e != cudaSuccess || !pack || !tokens || here) return cuda_status(e);
     e = launch_pack8(rows, g.D, g.ld, p->dtype, g.x, saved->x, s);
@@ -1071,7 +1211,7 @@ mru_status mru_gated_scan_backward(const mru_gated_problem* p, const mru_gated_i
     b.out(dh0, state);
     b.out(ws, ws_bytes);
     if (b.clash()) return MRU_ERR_INVALID_ARG;
-    const Layout W = layout(*p, true);
+    const Layout W = layout(*p, true, true);
     if (ws_bytes < W.bytes) return MRU_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;

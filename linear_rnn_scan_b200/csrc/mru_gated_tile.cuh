@@ -12,7 +12,8 @@ using namespace ops;
 constexpr int kTok = MRU_GATED_KEEP;     // tokens of a tile: a kept state per tile
 constexpr int kWarps = 8;
 constexpr int kStep = kTok / kWarps;     // tokens of a warp
-constexpr int kThreads = 32 * kWarps;
+constexpr int kManagers = 2;             // warps that load, and find carries
+constexpr int kThreads = 32 * (kWarps + kManagers);
 constexpr int kFan = 8;                  // tiles of a group, groups of a block of the carry's tree
 
 struct Args {
@@ -72,12 +73,17 @@ __device__ __forceinline__ void gates(float x, float f, float i, float csp, floa
     }
 }
 
-// The states of a lane's C channels, and the map h -> P h + H of a run of
-// tokens on them.
+// C channels of a lane: adjacent ones (VEC: 16-byte rows), or 32 apart.
 template <int C>
 struct Vec {
     float v[C];
 };
+template <int C, bool VEC>
+__device__ __forceinline__ int channel(int lane, int c)
+{
+    return VEC ? C * lane + c : lane + 32 * c;
+}
+// The map h -> P h + H of a run of tokens on them.
 template <int C>
 struct Map {
     float P[C], H[C];
@@ -110,30 +116,6 @@ struct Map {
         return r;
     }
 };
-// A row of maps in shared memory, (P, H, P, H) of two channels to 16 bytes.
-template <int C>
-struct MapRow {
-    float4 q[C / 2][32];
-    __device__ __forceinline__ void put(int lane, const Map<C>& m)
-    {
-#pragma unroll
-        for (int k = 0; k < C / 2; ++k)
-            q[k][lane] = make_float4(m.P[2 * k], m.H[2 * k], m.P[2 * k + 1], m.H[2 * k + 1]);
-    }
-    __device__ __forceinline__ Map<C> get(int lane) const
-    {
-        Map<C> m;
-#pragma unroll
-        for (int k = 0; k < C / 2; ++k) {
-            const float4 v = q[k][lane];
-            m.P[2 * k] = v.x;
-            m.H[2 * k] = v.y;
-            m.P[2 * k + 1] = v.z;
-            m.H[2 * k + 1] = v.w;
-        }
-        return m;
-    }
-};
 
 // ------------------------------------------------------------------ tiles ---
 
@@ -147,18 +129,18 @@ struct Tile {
     int32_t last;                        // nothing is carried out of it
 };
 
-template <int C, bool REVERSE>
+template <int CH, bool REVERSE>
 __device__ __forceinline__ void find_tile(const Args& g, uint32_t ticket, Tile& t)
 {
     t.ticket = ticket;
     if (ticket >= g.tiles) return;
     const uint32_t order = ticket / g.cols, col = ticket - order * g.cols, b = col / g.cgs;
     const int64_t t0 = (REVERSE ? g.K - 1 - (int64_t)order : (int64_t)order) * kTok;
-    const int64_t d0 = (int64_t)(col - b * g.cgs) * (32 * C), left = valid_tokens(g, b) - t0;
+    const int64_t d0 = (int64_t)(col - b * g.cgs) * CH, left = valid_tokens(g, b) - t0;
     t.order = order;
     t.col = col;
     t.tokens = (int32_t)(g.L - t0 < kTok ? g.L - t0 : kTok);
-    t.channels = (int32_t)(g.D - d0 < 32 * C ? g.D - d0 : 32 * C);
+    t.channels = (int32_t)(g.D - d0 < CH ? g.D - d0 : CH);
     t.valid = left <= 0 ? 0 : left < kTok ? (int32_t)left : kTok;
     t.row = b * g.L + t0;
     t.b = b;
@@ -175,12 +157,76 @@ __device__ __forceinline__ uint32_t draw(const Args& g, uint32_t before)
     return g.ticket ? atomicAdd(g.ticket, 1u) : before + gridDim.x;
 }
 
-// A warp's tokens that are not padding, and which of them start anew.
-__device__ __forceinline__ void warp_masks(const Args& g, const Tile& t, int w, int lane, int& n, uint32_t& resets)
+// ---------------------------------------------------------------- waiting ---
+
+// Meeting points of the warps that compute and the managers (hardware named
+// barriers; 0 is __syncthreads).  arrive: without waiting.
+enum Meet { kMaps = 1, kCarry = 2, kMgr = 3, kStates = 4, kBack = 5 };
+template <int ID>
+__device__ __forceinline__ void meet_arrive()
 {
-    n = min(max(t.valid - w * kStep, 0), kStep);
-    resets = 0;
-    if (g.reset) resets = __ballot_sync(~0u, lane < n && g.reset[t.row + w * kStep + lane] != 0);
+    __syncwarp();
+    asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(kThreads) : "memory");
+}
+template <int ID>
+__device__ __forceinline__ void meet()
+{
+    __syncwarp();
+    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(kThreads) : "memory");
+}
+__device__ __forceinline__ void meet_managers()
+{
+    __syncwarp();
+    asm volatile("bar.sync %0, %1;" ::"n"((int)kMgr), "n"(32 * kManagers) : "memory");
+}
+
+__device__ __forceinline__ unsigned shared_address(const void* p) { return (unsigned)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void barrier_init(uint64_t* b, int count)
+{
+    asm volatile("mbarrier.init.shared.b64 [%0], %1;" ::"r"(shared_address(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint64_t* b, int bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(shared_address(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(uint64_t* b)
+{
+    asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(shared_address(b)) : "memory");
+}
+__device__ __forceinline__ bool barrier_try(uint64_t* b, unsigned parity)
+{
+    unsigned done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done)
+                 : "r"(shared_address(b)), "r"(parity)
+                 : "memory");
+    return done;
+}
+__device__ __forceinline__ uint64_t now_ns()
+{
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// Records that a wait gave up.  g.abort is missing where no tile waits.
+__device__ __forceinline__ void give_up(const Args& g)
+{
+    if (g.status) atomicOr(g.status, (uint32_t)STATUS_TIMEOUT);
+    if (g.abort) atomicExch(g.abort, 1u);
+}
+// Waits for a stage's copies, for a limited time.
+__device__ __forceinline__ void barrier_wait(const Args& g, uint64_t* b, unsigned parity)
+{
+    uint64_t t0 = 0;
+    for (int n = 0; !barrier_try(b, parity); ++n) {
+        if ((n & 255) != 255) continue;
+        const uint64_t t = now_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > 2000000000ull) {
+            if ((threadIdx.x & 31) == 0) give_up(g);
+            return;
+        }
+    }
 }
 
 // ------------------------------------------------------------------ carry ---
@@ -192,7 +238,8 @@ __device__ __forceinline__ void warp_masks(const Args& g, const Tile& t, int w, 
 // channel is one 64-bit word, complemented so that zeroed memory reads as "not
 // there yet" (no pair is all ones: such a NaN is published as another NaN):
 // word and flag arrive together, which saves a fence before the flag and a
-// round trip after it.
+// round trip after it.  A manager's lane holds the CH / 64 channels from
+// CH / 64 times its index.
 
 __device__ __forceinline__ uint64_t pair_word(float P, float H)
 {
@@ -200,288 +247,265 @@ __device__ __forceinline__ uint64_t pair_word(float P, float H)
     if (p == 0xffffffffu) p = 0x7fffffffu;
     return ~(((uint64_t)p << 32) | __float_as_uint(H));
 }
+__device__ __forceinline__ float word_P(uint64_t u) { return __uint_as_float((uint32_t)(~u >> 32)); }
+__device__ __forceinline__ float word_H(uint64_t u) { return __uint_as_float((uint32_t)~u); }
 
-template <int C>
-__device__ __forceinline__ uint64_t* tile_words(const Args& g, const Tile& t, uint32_t order)
+template <int K>
+__device__ __forceinline__ void publish(uint64_t* at, const Map<K>& m)
 {
-    return g.a0 + ((uint64_t)t.col * (uint64_t)g.K + order) * (32 * C);
-}
-template <int C>
-__device__ __forceinline__ uint64_t* group_words(const Args& g, const Tile& t, uint32_t group)
-{
-    return g.a1 + ((uint64_t)t.col * g.groups + group) * (32 * C);
-}
-template <int C>
-__device__ __forceinline__ uint64_t* block_words(const Args& g, const Tile& t, uint32_t block)
-{
-    return g.c2 + ((uint64_t)t.col * g.blocks + block) * (32 * C);
-}
-
-// Words [2 k, lane, 2]: 16 bytes of a lane next to its neighbours'.
-template <int C>
-__device__ __forceinline__ void publish(uint64_t* at, int lane, const Map<C>& m)
-{
-#pragma unroll
-    for (int k = 0; k < C / 2; ++k)
-        asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(at + 64 * k + 2 * lane),
-                     "l"(pair_word(m.P[2 * k], m.H[2 * k])), "l"(pair_word(m.P[2 * k + 1], m.H[2 * k + 1]))
+    if constexpr (K == 2)
+        asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(at), "l"(pair_word(m.P[0], m.H[0])),
+                     "l"(pair_word(m.P[1], m.H[1]))
                      : "memory");
+    else
+        asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(at), "l"(pair_word(m.P[0], m.H[0])) : "memory");
+}
+template <int K>
+__device__ __forceinline__ void peek(const uint64_t* at, uint64_t (&u)[K])
+{
+    if constexpr (K == 2)
+        asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(u[0]), "=l"(u[1]) : "l"(at) : "memory");
+    else
+        asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(u[0]) : "l"(at) : "memory");
 }
 
-__device__ __forceinline__ uint64_t now_ns()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
+// A lane's carry: what it is made of, oldest first, in two lists that are
+// looked up while other work is done.
+template <int K>
+struct Lookup {
+    uint64_t u[kFan][K];
 
-template <int C>
-__device__ __forceinline__ bool peek(const uint64_t* at, int lane, uint64_t (&u)[C])
-{
-    bool there = true;
+    // Asks for `count` maps (at most 8), `gap` words apart.
+    __device__ __forceinline__ void ask(const uint64_t* at, uint32_t count, uint64_t gap)
+    {
 #pragma unroll
-    for (int k = 0; k < C / 2; ++k)
-        asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];"
-                     : "=l"(u[2 * k]), "=l"(u[2 * k + 1])
-                     : "l"(at + 64 * k + 2 * lane)
-                     : "memory");
+        for (int k = 0; k < kFan; ++k) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) there = there && u[c] != 0;
-    return there;
-}
-template <int C>
-__device__ __forceinline__ Map<C> map_of(const uint64_t (&u)[C])
-{
-    Map<C> m;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        m.P[c] = __uint_as_float((uint32_t)(~u[c] >> 32));
-        m.H[c] = __uint_as_float((uint32_t)~u[c]);
+            for (int c = 0; c < K; ++c) u[k][c] = 0;
+            if (k < (int)count) peek<K>(at + k * gap, u[k]);
+        }
     }
-    return m;
-}
-
-// Waits for two published maps (either may be absent: the identity), for a
-// limited time, and composes them, `one` first.
-template <int C>
-__device__ __forceinline__ Map<C> await(const Args& g, const uint64_t* one, const uint64_t* two, int lane)
-{
-    uint64_t u[C], v[C], t0 = 0;
-    for (int n = 0;; ++n) {
-        const bool a = !one || peek<C>(one, lane, u), b = !two || peek<C>(two, lane, v);
-        if (__all_sync(~0u, a && b)) break;
-        if ((n & 63) == 63) {
+    // Waits until they are there, for a limited time; false: it gave up.
+    __device__ __forceinline__ bool await(const Args& g, const uint64_t* at, uint32_t count, uint64_t gap)
+    {
+        uint64_t t0 = 0;
+        for (int n = 0;; ++n) {
+            bool there = true;
+#pragma unroll
+            for (int k = 0; k < kFan; ++k)
+#pragma unroll
+                for (int c = 0; c < K; ++c) there = there && (k >= (int)count || u[k][c] != 0);
+            if (__all_sync(~0u, there)) return true;
+            ask(at, count, gap);
+            if ((n & 63) != 63) continue;
             uint32_t stop;
             asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(stop) : "l"(g.abort) : "memory");
             const uint64_t t = now_ns();
             if (t0 == 0) t0 = t;
-            bool out = false;
-            if (lane == 0 && t - t0 > g.wait_ns) {
-                atomicOr(g.status, (uint32_t)STATUS_TIMEOUT);
-                atomicExch(g.abort, 1u);
-                out = true;
-            }
-            if (__any_sync(~0u, out || stop)) return Map<C>::of(1.0f);
+            const bool out = (threadIdx.x & 31) == 0 && t - t0 > g.wait_ns;
+            if (out) give_up(g);
+            if (__any_sync(~0u, out || stop)) return false;
         }
     }
-    if (!one) return Map<C>::of(1.0f);
-    const Map<C> first = map_of<C>(u);
-    return two ? map_of<C>(v).after(first) : first;
-}
-
-// What a tile's carry is made of, in shared memory: [0 .. 3] the block's carry
-// in and the block's groups before this one, [4 .. 7] the tiles before in the
-// group; two to an entry, so that [0] is the carry in and group 0, [1] groups 1
-// and 2, and so on.
-template <int C>
-struct Entries {
-    MapRow<C> e[8];
-
-    // Warp w fetches entry w.  `start` is the state before the first tile (h0,
-    // or the last state's gradient).
-    __device__ __forceinline__ void fetch(const Args& g, const Tile& t, int w, int lane, const float* start)
+    // Their composition applied to h.
+    __device__ __forceinline__ Vec<K> apply(uint32_t count, Vec<K> h) const
     {
-        const uint32_t block = t.order / (kFan * kFan), group = t.order / kFan % kFan, j = t.order % kFan;
-        if (w >= 4) {
-            const uint32_t k = 2 * (w - 4);
-            if (k < j) {
-                const uint64_t* at = tile_words<C>(g, t, t.order - j + k);
-                e[w].put(lane, await<C>(g, at, k + 1 < j ? at + 32 * C : nullptr, lane));
-            }
-        } else if (w == 0 && block == 0) {
-            Map<C> m = Map<C>::of(0.0f);
-            if (start) {
 #pragma unroll
-                for (int c = 0; c < C; ++c)
-                    if (C * lane + c < t.channels) m.H[c] = start[t.b * g.D + t.d0 + C * lane + c];
-            }
-            e[0].put(lane, group ? await<C>(g, group_words<C>(g, t, 0), nullptr, lane).after(m) : m);
-        } else if (2u * w <= group) {
-            const uint64_t* at = group_words<C>(g, t, block * kFan + 2 * w);
-            e[w].put(lane, await<C>(g, w ? at - 32 * C : block_words<C>(g, t, block), 2u * w < group ? at : nullptr, lane));
-        }
-    }
-    __device__ __forceinline__ Vec<C> carry(const Tile& t, int lane) const
-    {
-        const uint32_t group = t.order / kFan % kFan, j = t.order % kFan;
-        const Map<C> first = e[0].get(lane);
-        Vec<C> h;
+        for (int k = 0; k < kFan; ++k)
+            if (k < (int)count) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) h.v[c] = first.H[c];
-        for (uint32_t k = 1; 2 * k <= group; ++k) h = e[k].get(lane)(h);
-        for (uint32_t k = 0; 2 * k < j; ++k) h = e[4 + k].get(lane)(h);
+                for (int c = 0; c < K; ++c) h.v[c] = carry_in(word_P(u[k][c]), h.v[c]) + word_H(u[k][c]);
+            }
         return h;
     }
-    // After the carry is known: the group's map (last tile of a group) and the
-    // next block's carry (last tile of a block), by one warp.
-    __device__ __forceinline__ void publish_up(const Args& g, const Tile& t, int lane, const Map<C>& own,
-                                               const Vec<C>& carry) const
+    __device__ __forceinline__ Map<K> compose(Map<K> m) const
     {
-        if (t.last || t.order % kFan != kFan - 1) return;
-        const uint32_t group = t.order / kFan;
-        Map<C> m;
-        if (group % kFan != kFan - 1) {
-            m = e[4].get(lane);
-            for (int k = 5; k < 8; ++k) m = e[k].get(lane).after(m);
-            publish<C>(group_words<C>(g, t, group), lane, own.after(m));
-        } else {
-            const Vec<C> h = own(carry);
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                m.P[c] = 0.0f;
-                m.H[c] = h.v[c];
+        for (int k = kFan - 2; k >= 0; --k)
+#pragma unroll
+            for (int c = 0; c < K; ++c) {
+                // m after the k-th
+                m.H[c] = carry_in(m.P[c], word_H(u[k][c])) + m.H[c];
+                m.P[c] *= word_P(u[k][c]);
             }
-            publish<C>(block_words<C>(g, t, group / kFan + 1), lane, m);
+        return m;
+    }
+};
+
+// A manager's search for its tile's carry.
+template <int CH>
+struct Search {
+    static constexpr int K = CH / 64;
+    uint64_t *tiles, *groups, *blocks;   // the column's words, at the lane's channels
+    uint32_t block, group, j;            // place of the tile: block, group in it, tile in the group
+
+    __device__ __forceinline__ Search(const Args& g, const Tile& t, int m)
+        : tiles(g.a0 + (uint64_t)t.col * (uint64_t)g.K * CH + K * m), groups(g.a1 + (uint64_t)t.col * g.groups * CH + K * m),
+          blocks(g.c2 + (uint64_t)t.col * g.blocks * CH + K * m), block(t.order / (kFan * kFan)),
+          group(t.order / kFan % kFan), j(t.order % kFan)
+    {
+    }
+    __device__ __forceinline__ uint32_t order() const { return (block * kFan + group) * kFan + j; }
+    __device__ __forceinline__ const uint64_t* old_tiles() const { return tiles + (uint64_t)(order() - j) * CH; }
+    __device__ __forceinline__ const uint64_t* old_groups() const { return groups + (uint64_t)(block * kFan) * CH; }
+    __device__ __forceinline__ void publish_tile(const Map<K>& own) { publish<K>(tiles + (uint64_t)order() * CH, own); }
+    // The state before the tile.  `start`: before the first one (h0, or the
+    // last state's gradient).
+    __device__ __forceinline__ Vec<K> carry(const Args& g, Lookup<K>& near, Lookup<K>& far, const Vec<K>& start)
+    {
+        Vec<K> h = start;
+        bool fine = true;
+        if (block) {
+            Lookup<K> one;
+            one.ask(blocks + (uint64_t)block * CH, 1, CH);
+            fine = one.await(g, blocks + (uint64_t)block * CH, 1, CH);
+            h = one.apply(1, h);
+        }
+        if (group) {
+            fine = far.await(g, old_groups(), group, CH) && fine;
+            h = far.apply(group, h);
+        }
+        if (j) {
+            fine = near.await(g, old_tiles(), j, CH) && fine;
+            h = near.apply(j, h);
+        }
+        return fine ? h : start;
+    }
+    // After the carry is known: the group's map (last tile of a group) and the
+    // next block's carry (last tile of a block).
+    __device__ __forceinline__ void publish_up(const Lookup<K>& near, const Map<K>& own, const Vec<K>& after)
+    {
+        if (j != kFan - 1) return;
+        Map<K> m;
+        if (group != kFan - 1) {
+            publish<K>(groups + (uint64_t)(block * kFan + group) * CH, near.compose(own));
+        } else {
+#pragma unroll
+            for (int c = 0; c < K; ++c) {
+                m.P[c] = 0.0f;
+                m.H[c] = after.v[c];
+            }
+            publish<K>(blocks + (uint64_t)(block + 1) * CH, m);
         }
     }
 };
 
 // ------------------------------------------------------- loads and stores ---
 
-__device__ __forceinline__ void cp_async(void* smem, const void* gmem, int bytes16)
+// A row's piece of an input into shared memory (16-byte aligned, pitch bytes
+// apart), by one thread.  VEC: rows start on 16 bytes and hold whole pieces of
+// them; else the aligned pieces that hold the row, except where they would end
+// behind the last row: that row goes element by element.  Returns the bytes
+// under way.
+template <typename V, bool VEC>
+__device__ __forceinline__ int copy_row(const V* from, int channels, const V* end, unsigned char* to, uint64_t* full)
 {
-    const unsigned s = (unsigned)__cvta_generic_to_shared(smem);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(gmem), "r"(bytes16) : "memory");
-}
-__device__ __forceinline__ void cp_async4(void* smem, const void* gmem, int bytes4)
-{
-    const unsigned s = (unsigned)__cvta_generic_to_shared(smem);
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(s), "l"(gmem), "r"(bytes4) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// A tile of one input into shared memory [64][32 C], zeros past the last token
-// or channel.  VEC: rows start on 16 bytes; else element by element.
-template <typename T, int C, bool VEC>
-__device__ __forceinline__ void load_tile(const Tile& t, const void* from, int64_t ld, T* to)
-{
-    constexpr int kCh = 32 * C;
-    const T* src = (const T*)from + t.row * ld + t.d0;
-    if constexpr (VEC) {
-        constexpr int per = 16 / sizeof(T), chunks = kCh / per, rows = kThreads / chunks;
-        const int row = threadIdx.x / chunks, c = threadIdx.x % chunks * per;
-        const T* at = src + row * ld + c;
-        T* put = to + row * kCh + c;
-        const int bytes = c >= t.channels ? 0 : t.channels - c >= per ? 16 : (t.channels - c) * (int)sizeof(T);
-        const int64_t jump = rows * ld;
-#pragma unroll
-        for (int k = 0; k < kTok / rows; ++k) {
-            const bool in = row + k * rows < t.tokens && bytes > 0;
-            cp_async(put + k * rows * kCh, in ? at : src, in ? bytes : 0);
-            at += jump;
-        }
-    } else {
-        for (int k = threadIdx.x; k < kTok * kCh; k += kThreads) {
-            const int row = k / kCh, c = k % kCh;
-            const bool in = row < t.tokens && c < t.channels;
-            const T* at = in ? src + row * ld + c : src;
-            if constexpr (sizeof(T) == 4) cp_async4(to + k, at, in ? 4 : 0);
-            else to[k] = in ? *at : from_f32<T>(0.0f);
+    uintptr_t first = reinterpret_cast<uintptr_t>(from);
+    int bytes = channels * (int)sizeof(V);
+    if constexpr (!VEC) {
+        const unsigned off = (unsigned)(first & 15);
+        first -= off;
+        bytes = (bytes + (int)off + 15) & ~15;
+        if (first + (uintptr_t)bytes > reinterpret_cast<uintptr_t>(end)) {
+            V* put = reinterpret_cast<V*>(to + off);
+            for (int c = 0; c < channels; ++c) put[c] = from[c];
+            return 0;
         }
     }
+    barrier_expect(full, bytes);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     shared_address(to)),
+                 "l"(first), "r"(bytes), "r"(shared_address(full))
+                 : "memory");
+    return bytes;
 }
 
-// C adjacent channels of a row.
-template <int C>
-__device__ __forceinline__ Vec<C> read_row(const float* p)
-{
-    Vec<C> r;
-    if constexpr (C == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        r.v[0] = v.x; r.v[1] = v.y; r.v[2] = v.z; r.v[3] = v.w;
-    } else {
-        const float2 v = *reinterpret_cast<const float2*>(p);
-        r.v[0] = v.x; r.v[1] = v.y;
+// Where an input's rows lie in a stage: pitch, and (not VEC) how far a row
+// starts behind its 16 bytes.
+template <typename V, int CH, bool VEC>
+struct Rows {
+    static constexpr int kPitch = CH * (int)sizeof(V) + (VEC ? 0 : 32);
+    const unsigned char* base;
+    unsigned off, step;                  // of the tile's first row, and of a row to the next, modulo 16
+    Rows() = default;
+    __device__ __forceinline__ Rows(const unsigned char* b, const void* from, int64_t ld, const Tile& t) : base(b)
+    {
+        off = VEC ? 0 : (unsigned)(reinterpret_cast<uintptr_t>((const V*)from + t.row * ld + t.d0) & 15);
+        step = VEC ? 0 : (unsigned)((ld * (int64_t)sizeof(V)) & 15);
     }
-    return r;
-}
-template <int C>
-__device__ __forceinline__ Vec<C> read_row(const __nv_bfloat16* p)
-{
-    Vec<C> r;
-    uint32_t u[C / 2];
-    if constexpr (C == 4) {
-        const uint2 v = *reinterpret_cast<const uint2*>(p);
-        u[0] = v.x; u[1] = v.y;
-    } else {
-        u[0] = *reinterpret_cast<const uint32_t*>(p);
+    __device__ __forceinline__ const V* row(int r) const
+    {
+        return reinterpret_cast<const V*>(base + r * kPitch + (VEC ? 0 : (off + r * step) & 15));
     }
-#pragma unroll
-    for (int k = 0; k < C / 2; ++k) {
-        r.v[2 * k] = __uint_as_float(u[k] << 16);
-        r.v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-    }
-    return r;
-}
-
-// Whether rows of C channels can be written in one piece, and how many
-// channels of the lane there are otherwise.
-struct Put {
-    bool whole;
-    int channels;
 };
-template <int C>
-__device__ __forceinline__ void write_row(float* p, const Vec<C>& r, const Put& put)
+
+__device__ __forceinline__ float value(float v) { return v; }
+__device__ __forceinline__ float value(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float value(int8_t v) { return (float)v; }
+
+// A lane's channels of a row in shared memory.
+template <int C, bool VEC, typename V>
+__device__ __forceinline__ Vec<C> read_row(const V* row, int lane)
 {
-    if (put.whole) {
-        if constexpr (C == 4) *reinterpret_cast<float4*>(p) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-        else *reinterpret_cast<float2*>(p) = make_float2(r.v[0], r.v[1]);
-        return;
-    }
+    Vec<C> r;
+    if constexpr (!VEC) {
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-        if (c < put.channels) p[c] = r.v[c];
-}
-template <int C>
-__device__ __forceinline__ void write_row(__nv_bfloat16* p, const Vec<C>& r, const Put& put)
-{
-    if (put.whole) {
+        for (int c = 0; c < C; ++c) r.v[c] = value(row[channel<C, VEC>(lane, c)]);
+    } else if constexpr (sizeof(V) == 4) {
+        if constexpr (C == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(row + 4 * lane);
+            r.v[0] = v.x; r.v[1] = v.y; r.v[2] = v.z; r.v[3] = v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2*>(row + 2 * lane);
+            r.v[0] = v.x; r.v[1] = v.y;
+        }
+    } else if constexpr (sizeof(V) == 2) {
         uint32_t u[C / 2];
+        if constexpr (C == 4) {
+            const uint2 v = *reinterpret_cast<const uint2*>(row + 4 * lane);
+            u[0] = v.x; u[1] = v.y;
+        } else {
+            u[0] = *reinterpret_cast<const uint32_t*>(row + 2 * lane);
+        }
 #pragma unroll
         for (int k = 0; k < C / 2; ++k) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(r.v[2 * k], r.v[2 * k + 1]);
-            u[k] = *reinterpret_cast<const uint32_t*>(&h);
+            r.v[2 * k] = __uint_as_float(u[k] << 16);
+            r.v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
         }
-        if constexpr (C == 4) *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
-        else *reinterpret_cast<uint32_t*>(p) = u[0];
+    } else {
+        static_assert(C == 2, "8-bit rows: two channels to a lane");
+        const char2 q = *reinterpret_cast<const char2*>(row + 2 * lane);
+        r.v[0] = (float)(signed char)q.x;
+        r.v[1] = (float)(signed char)q.y;
+    }
+    return r;
+}
+
+// Writes a lane's channels of a row in memory (row: at the tile's first one).
+// whole: in one piece; else those of the tile's channels that there are.
+template <int C, bool VEC, typename T>
+__device__ __forceinline__ void write_row(T* row, const Vec<C>& r, int lane, bool whole, int channels)
+{
+    if (VEC && whole) {
+        if (C * lane >= channels) return;
+        if constexpr (sizeof(T) == 4) {
+            if constexpr (C == 4) *reinterpret_cast<float4*>(row + 4 * lane) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+            else *reinterpret_cast<float2*>(row + 2 * lane) = make_float2(r.v[0], r.v[1]);
+        } else {
+            uint32_t u[C / 2];
+#pragma unroll
+            for (int k = 0; k < C / 2; ++k) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(r.v[2 * k], r.v[2 * k + 1]);
+                u[k] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            if constexpr (C == 4) *reinterpret_cast<uint2*>(row + 4 * lane) = make_uint2(u[0], u[1]);
+            else *reinterpret_cast<uint32_t*>(row + 2 * lane) = u[0];
+        }
         return;
     }
 #pragma unroll
     for (int c = 0; c < C; ++c)
-        if (c < put.channels) p[c] = __float2bfloat16_rn(r.v[c]);
-}
-// fp32 rows of one value per channel ([B, D] arrays).
-template <int C>
-__device__ __forceinline__ void write_state(float* p, const Vec<C>& r, int channels)
-{
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-        if (c < channels) p[c] = r.v[c];
+        if (channel<C, VEC>(lane, c) < channels) row[channel<C, VEC>(lane, c)] = from_f32<T>(r.v[c]);
 }
 
 }  // namespace gated
