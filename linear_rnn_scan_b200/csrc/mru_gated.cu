@@ -351,16 +351,31 @@ constexpr size_t forward_stage_bytes()
     return (size_t)inputs_of(GATE) * kTok * Rows<T, 32 * C, VEC>::kPitch;
 }
 
-// A token's rows of the gate's inputs, by one thread.
-template <typename T, int C, bool VEC, int GATE>
-__device__ __forceinline__ void copy_inputs(const Args& g, const Tile& t, int m, unsigned char* stage, uint64_t* full)
+// Starts the copies of a tile's inputs (V: their type in memory) by the
+// managers: the copy engine's own tiles by the first of them, or a token's rows
+// by each.
+template <typename V, int C, bool VEC, int NIN>
+__device__ __forceinline__ void copy_inputs(const Args& g, const Maps& maps, const Tile& t, int m, unsigned char* stage,
+                                            uint64_t* full)
 {
-    constexpr int kPitch = Rows<T, 32 * C, VEC>::kPitch;
+    constexpr int CH = 32 * C, kPitch = Rows<V, CH, VEC>::kPitch;
+    if constexpr (VEC) {
+        if (m != 0) return;
+        barrier_expect(full, NIN * kTok * kPitch);
 #pragma unroll
-    for (int n = 0; n < inputs_of(GATE); ++n) {
-        const T* base = (const T*)(n == 0 ? g.x : n == 1 ? g.f : g.i);
-        copy_row<T, VEC>(base + (t.row + m) * g.ld + t.d0, t.channels, base + (g.B * g.L - 1) * g.ld + g.D,
-                         stage + (n * kTok + m) * kPitch, full);
+        for (int n = 0; n < NIN; ++n)
+            copy_tile(&maps.in[n], (int)t.d0, (int)(t.row - t.b * g.L), (int)t.b, stage + n * kTok * kPitch, full);
+    } else {
+        if (m >= t.tokens) return;
+        constexpr bool held = sizeof(V) == 1;
+        const int64_t ld = held ? g.D : g.ld;
+#pragma unroll
+        for (int n = 0; n < NIN; ++n) {
+            const V* base = (const V*)(held ? (const void*)(n == 0 ? g.x8.q : n == 1 ? g.f8.q : g.i8.q)
+                                            : n == 0 ? g.x : n == 1 ? g.f : g.i);
+            copy_row<V>(base + (t.row + m) * ld + t.d0, t.channels, base + (g.B * g.L - 1) * ld + g.D,
+                        stage + (n * kTok + m) * kPitch, full);
+        }
     }
 }
 
@@ -420,7 +435,7 @@ __device__ __forceinline__ void forward_compute(const Args& g, TileMem<C>& mem, 
 }
 
 template <typename T, int C, int GATE, bool VEC>
-__device__ __forceinline__ void forward_manage(const Args& g, TileMem<C>& mem, unsigned char* stages)
+__device__ __forceinline__ void forward_manage(const Args& g, const Maps& maps, TileMem<C>& mem, unsigned char* stages)
 {
     constexpr int CH = 32 * C, K = CH / 64;
     constexpr size_t kBytes = forward_stage_bytes<T, C, VEC, GATE>();
@@ -437,7 +452,7 @@ __device__ __forceinline__ void forward_manage(const Args& g, TileMem<C>& mem, u
     auto reset_of = [&](const Tile& t) { return g.reset && t.ticket < g.tiles && m < t.tokens && g.reset[t.row + m]; };
     auto lam_of = [&](const Tile& t) { return get_lane<K>(lru && t.ticket < g.tiles ? g.lam + t.d0 : nullptr, m, t.channels); };
     auto copies = [&](const Tile& t, int st) {
-        if (t.ticket < g.tiles && m < t.tokens) copy_inputs<T, C, VEC, GATE>(g, t, m, stages + st * kBytes, &mem.full[st]);
+        if (t.ticket < g.tiles) copy_inputs<T, C, VEC, inputs_of(GATE)>(g, maps, t, m, stages + st * kBytes, &mem.full[st]);
     };
     for (int k = 0; k < 2; ++k) {
         const Tile& t = mem.tile[k];
@@ -461,7 +476,7 @@ __device__ __forceinline__ void forward_manage(const Args& g, TileMem<C>& mem, u
         const bool reset = reset_of(coming);
         const Vec<K> start = get_lane<K>(g.h0 && search.block == 0 ? g.h0 + t.b * g.D + t.d0 : nullptr, m, t.channels);
         meet<kMaps>();
-        copies(coming, st);                                // the stage has been read
+        if (VEC) copies(coming, st);                       // the stage has been read
         Map<K> own = Map<K>::of(1.0f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) own = lane_map<K>(mem.map[w], m).after(own);
@@ -474,6 +489,7 @@ __device__ __forceinline__ void forward_manage(const Args& g, TileMem<C>& mem, u
             h = lane_map<K>(mem.map[w], m)(h);
         }
         meet_arrive<kCarry>();
+        if (!VEC) copies(coming, st);                      // row by row, which takes longer
         if (!t.last) search.publish_up(near, own, h);
         else if (g.h_last) put_lane<K>(g.h_last + t.b * g.D + t.d0, h, m, t.channels);
         if (g.states) put_lane<K>(g.states + t.k * g.D + t.d0, carry, m, t.channels);
@@ -485,9 +501,9 @@ __device__ __forceinline__ void forward_manage(const Args& g, TileMem<C>& mem, u
 }
 
 template <typename T, int C, int GATE, bool VEC, bool PACK>
-__global__ void __launch_bounds__(kThreads, 2) k_gated_tile(Args g)
+__global__ void __launch_bounds__(kThreads, 2) k_gated_tile(Args g, const __grid_constant__ Maps maps)
 {
-    extern __shared__ __align__(16) unsigned char stages[];
+    extern __shared__ __align__(128) unsigned char stages[];
     __shared__ __align__(16) TileMem<C> mem;
     if (threadIdx.x == 0) {
         for (int k = 0; k < 2; ++k) barrier_init(&mem.full[k], 32 * kManagers);
@@ -496,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_gated_tile(Args g)
     }
     __syncthreads();
     if (threadIdx.x < 32 * kWarps) forward_compute<T, C, GATE, VEC, PACK>(g, mem, stages);
-    else forward_manage<T, C, GATE, VEC>(g, mem, stages);
+    else forward_manage<T, C, GATE, VEC>(g, maps, mem, stages);
 }
 
 // --------------------------------------------------------------- backward ---
@@ -534,7 +550,7 @@ __device__ __forceinline__ Vec<C> input_row(const R& in, const float* scale, int
 }
 
 // The map of a warp's tokens; a and, for the sigmoid gate, cx = 1 - a stay.
-template <int C, bool VEC, int GATE, bool PACKED, bool NEAR, typename R>
+template <int C, bool VEC, int GATE, bool PACKED, bool SPECIAL, bool NEAR, typename R>
 __device__ __forceinline__ Map<C> back_map(const R (&in)[inputs_of(GATE)], const float (&scale)[3][kTok], int w, int lane,
                                            const Vec<C>& csp, int n, uint32_t resets, Vec<C> (&a)[kStep],
                                            Vec<C> (&cx)[kStep])
@@ -547,13 +563,13 @@ __device__ __forceinline__ Map<C> back_map(const R (&in)[inputs_of(GATE)], const
             a[s].v[c] = 1.0f;
             cx[s].v[c] = 0.0f;
         }
-        if (s >= n) continue;
+        if (SPECIAL && s >= n) continue;
         const int row = w * kStep + s;
         const Vec<C> x = input_row<C, VEC, PACKED>(in[0], scale[0], row, lane);
         const Vec<C> f = input_row<C, VEC, PACKED>(in[1], scale[1], row, lane);
         Vec<C> i = x;
         if constexpr (GATE == MRU_GATE_LRU) i = input_row<C, VEC, PACKED>(in[2], scale[2], row, lane);
-        if (resets >> s & 1) m = Map<C>::of(0.0f);
+        if (SPECIAL && (resets >> s & 1)) m = Map<C>::of(0.0f);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             float b;
@@ -574,7 +590,7 @@ __device__ __forceinline__ Map<C> back_map(const R (&in)[inputs_of(GATE)], const
 // gradients e -> P e + E from the token after the last to before the first.
 // dl: sum q d and sum q dd/de (for lam) at e = 0, without the first token where
 // it is a piece's edge (k_gated_edge counts it).
-template <typename T, int C, bool VEC, int GATE, bool PACKED, bool NEAR, typename R>
+template <typename T, int C, bool VEC, int GATE, bool PACKED, bool SPECIAL, bool NEAR, typename R>
 __device__ __forceinline__ Map<C> back_factors(const R (&in)[inputs_of(GATE)], const Rows<T, 32 * C, VEC>& dys,
                                                const float (&scale)[3][kTok], int w, int lane, const Vec<C>& csp, Vec<C> h,
                                                int n, uint32_t resets, bool edge, Vec<C> (&a)[kStep], Vec<C> (&cx)[kStep],
@@ -584,7 +600,7 @@ __device__ __forceinline__ Map<C> back_factors(const R (&in)[inputs_of(GATE)], c
 #pragma unroll
     for (int s = 0; s < kStep; ++s) {
         cf[s] = ci[s] = q[s] = Vec<C>{};
-        if (s >= n) continue;
+        if (SPECIAL && s >= n) continue;
         const int row = w * kStep + s;
         const Vec<C> x = input_row<C, VEC, PACKED>(in[0], scale[0], row, lane);
         Vec<C> f = x, i = x;
@@ -592,7 +608,7 @@ __device__ __forceinline__ Map<C> back_factors(const R (&in)[inputs_of(GATE)], c
             f = input_row<C, VEC, PACKED>(in[1], scale[1], row, lane);
             i = input_row<C, VEC, PACKED>(in[2], scale[2], row, lane);
         }
-        const bool reset = resets >> s & 1;
+        const bool reset = SPECIAL && (resets >> s & 1);
         if (reset) h = Vec<C>{};
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -618,7 +634,7 @@ __device__ __forceinline__ Map<C> back_factors(const R (&in)[inputs_of(GATE)], c
     dl0 = dl1 = Vec<C>{};
 #pragma unroll
     for (int s = kStep - 1; s >= 0; --s) {
-        if (s >= n) continue;
+        if (SPECIAL && s >= n) continue;
         const Vec<C> dy = read_row<C, VEC>(dys.row(w * kStep + s), lane);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -628,10 +644,47 @@ __device__ __forceinline__ Map<C> back_factors(const R (&in)[inputs_of(GATE)], c
                 dl1.v[c] = fmaf(q[s].v[c], m.P[c], dl1.v[c]);
             }
             m.P[c] *= a[s].v[c];
-            m.H[c] = carry_in(a[s].v[c], d);
+            m.H[c] = SPECIAL || GATE == MRU_GATE_DECAY ? carry_in(a[s].v[c], d) : a[s].v[c] * d;
         }
     }
     return m;
+}
+
+// The gradients of a warp's tokens, from e behind them; first: where the first
+// token's d goes, if anywhere.
+template <typename T, int C, bool VEC, int GATE, bool SPECIAL>
+__device__ __forceinline__ void write_gradients(const Args& g, const Rows<T, 32 * C, VEC>& dys, int w, int lane, int64_t at,
+                                                Vec<C> e, int n, int left, const Vec<C> (&a)[kStep],
+                                                const Vec<C> (&cx)[kStep], const Vec<C> (&cf)[kStep],
+                                                const Vec<C> (&ci)[kStep], float* first, bool whole, int channels)
+{
+    T *dx = (T*)g.dx + at + (kStep - 1) * g.ldg, *df = (T*)g.df + at + (kStep - 1) * g.ldg;
+    T* di = (T*)g.di + at + (kStep - 1) * g.ldg;
+#pragma unroll
+    for (int s = kStep - 1; s >= 0; --s, dx -= g.ldg, df -= g.ldg, di -= g.ldg) {
+        if (SPECIAL && s >= left) continue;
+        Vec<C> d = {}, o;
+        if (!SPECIAL || s < n) {
+            d = read_row<C, VEC>(dys.row(w * kStep + s), lane);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                d.v[c] += e.v[c];
+                e.v[c] = SPECIAL || GATE == MRU_GATE_DECAY ? carry_in(a[s].v[c], d.v[c]) : a[s].v[c] * d.v[c];
+            }
+        }
+        if (s == 0 && first) write_row<C, VEC>(first, d, lane, false, channels);
+#pragma unroll
+        for (int c = 0; c < C; ++c) o.v[c] = GATE == MRU_GATE_DECAY ? d.v[c] : cx[s].v[c] * d.v[c];
+        write_row<C, VEC>(dx, o, lane, whole, channels);
+#pragma unroll
+        for (int c = 0; c < C; ++c) o.v[c] = cf[s].v[c] * d.v[c];
+        write_row<C, VEC>(df, o, lane, whole, channels);
+        if (GATE == MRU_GATE_LRU) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) o.v[c] = ci[s].v[c] * d.v[c];
+            write_row<C, VEC>(di, o, lane, whole, channels);
+        }
+    }
 }
 
 template <typename T, int C, int GATE, bool VEC, bool PACKED>
@@ -663,59 +716,44 @@ __device__ __forceinline__ void backward_compute(const Args& g, BackMem<C>& mem,
             in[2] = Rows<V, CH, VEC>(stage + Stage::kDy + 2 * Stage::kIn, PACKED ? (const void*)g.i8.q : g.i, ld, t);
         Vec<C> csp = {};
         if (lru) csp = read_row<C, VEC>(&mem.csp[st][0], lane);
-        const bool near = lru && all_near<C>(csp);
+        const bool special = n < kStep || resets, near = lru && !special && all_near<C>(csp);
         Vec<C> a[kStep], cx[kStep], cf[kStep], ci[kStep], dl0, dl1;
-        put_map<C, VEC>(mem.map[w], lane,
-                        near ? back_map<C, VEC, GATE, PACKED, lru>(in, mem.scale[st], w, lane, csp, n, resets, a, cx)
-                             : back_map<C, VEC, GATE, PACKED, false>(in, mem.scale[st], w, lane, csp, n, resets, a, cx));
+        Map<C> own;
+        const float (&scale)[3][kTok] = mem.scale[st];
+        if (special) own = back_map<C, VEC, GATE, PACKED, true, false>(in, scale, w, lane, csp, n, resets, a, cx);
+        else if (near) own = back_map<C, VEC, GATE, PACKED, false, lru>(in, scale, w, lane, csp, n, resets, a, cx);
+        else own = back_map<C, VEC, GATE, PACKED, false, false>(in, scale, w, lane, csp, n, resets, a, cx);
+        put_map<C, VEC>(mem.map[w], lane, own);
         meet_arrive<kMaps>();
         meet<kStates>();
         const Vec<C> h = read_row<C, VEC>(&mem.state[w][0], lane);
-        put_map<C, VEC>(mem.map[w], lane,
-                        near ? back_factors<T, C, VEC, GATE, PACKED, lru>(in, dys, mem.scale[st], w, lane, csp, h, n, resets,
-                                                                          edge, a, cx, cf, ci, dl0, dl1)
-                             : back_factors<T, C, VEC, GATE, PACKED, false>(in, dys, mem.scale[st], w, lane, csp, h, n, resets,
-                                                                            edge, a, cx, cf, ci, dl0, dl1));
-        int64_t at = (t.row + w * kStep + kStep - 1) * g.ldg + t.d0;
-        const int64_t edge_at = t.k * g.D + t.d0;
+        if (special)
+            own = back_factors<T, C, VEC, GATE, PACKED, true, false>(in, dys, scale, w, lane, csp, h, n, resets, edge, a, cx,
+                                                                     cf, ci, dl0, dl1);
+        else if (near)
+            own = back_factors<T, C, VEC, GATE, PACKED, false, lru>(in, dys, scale, w, lane, csp, h, n, resets, edge, a, cx,
+                                                                    cf, ci, dl0, dl1);
+        else
+            own = back_factors<T, C, VEC, GATE, PACKED, false, false>(in, dys, scale, w, lane, csp, h, n, resets, edge, a, cx,
+                                                                      cf, ci, dl0, dl1);
+        put_map<C, VEC>(mem.map[w], lane, own);
+        const int64_t at = (t.row + w * kStep) * g.ldg + t.d0, edge_at = t.k * g.D + t.d0;
         meet_arrive<kBack>();
         meet<kCarry>();
-        Vec<C> e = read_row<C, VEC>(&mem.state[w][0], lane);
+        const Vec<C> e = read_row<C, VEC>(&mem.state[w][0], lane);
         if (lru) {
 #pragma unroll
             for (int c = 0; c < C; ++c) mem.dlam[w][channel<C, VEC>(lane, c)] = fmaf(dl1.v[c], e.v[c], dl0.v[c]);
         }
-#pragma unroll
-        for (int s = kStep - 1; s >= 0; --s, at -= g.ldg) {
-            if (s >= left) continue;
-            Vec<C> d = {}, o;
-            if (s < n) {
-                d = read_row<C, VEC>(dys.row(w * kStep + s), lane);
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    d.v[c] += e.v[c];
-                    e.v[c] = carry_in(a[s].v[c], d.v[c]);
-                }
-            }
-            if (PACKED && s == 0 && edge) write_row<C, VEC>(g.edge_d + edge_at, d, lane, false, channels);
-#pragma unroll
-            for (int c = 0; c < C; ++c) o.v[c] = GATE == MRU_GATE_DECAY ? d.v[c] : cx[s].v[c] * d.v[c];
-            write_row<C, VEC>((T*)g.dx + at, o, lane, whole, channels);
-#pragma unroll
-            for (int c = 0; c < C; ++c) o.v[c] = cf[s].v[c] * d.v[c];
-            write_row<C, VEC>((T*)g.df + at, o, lane, whole, channels);
-            if (lru) {
-#pragma unroll
-                for (int c = 0; c < C; ++c) o.v[c] = ci[s].v[c] * d.v[c];
-                write_row<C, VEC>((T*)g.di + at, o, lane, whole, channels);
-            }
-        }
+        float* first = edge ? g.edge_d + edge_at : nullptr;
+        if (special) write_gradients<T, C, VEC, GATE, true>(g, dys, w, lane, at, e, n, left, a, cx, cf, ci, first, whole, channels);
+        else write_gradients<T, C, VEC, GATE, false>(g, dys, w, lane, at, e, n, left, a, cx, cf, ci, first, whole, channels);
     }
     meet_arrive<kMaps>();                                  // the last tile's part of dlam is there
 }
 
 template <typename T, int C, int GATE, bool VEC, bool PACKED>
-__device__ __forceinline__ void backward_manage(const Args& g, BackMem<C>& mem, unsigned char* stages)
+__device__ __forceinline__ void backward_manage(const Args& g, const Maps& maps, BackMem<C>& mem, unsigned char* stages)
 {
     using Stage = BackStage<T, C, VEC, PACKED>;
     constexpr int NIN = inputs_of(GATE), CH = 32 * C, K = CH / 64;
@@ -739,21 +777,19 @@ __device__ __forceinline__ void backward_manage(const Args& g, BackMem<C>& mem, 
         return PACKED && valid(t) && m < t.tokens ? h.scale[(t.row + m) * (int64_t)g.cgs + t.d0 / 64] : 0.0f;
     };
     auto copies = [&](const Tile& t, int st) {
-        if (!valid(t) || m >= t.tokens) return;
+        if (!valid(t)) return;
         unsigned char* stage = stages + st * Stage::bytes(NIN);
-        const T* dy = (const T*)g.dy;
-        copy_row<T, VEC>(dy + (t.row + m) * g.D + t.d0, t.channels, dy + g.B * g.L * g.D,
-                         stage + m * Rows<T, CH, VEC>::kPitch, &mem.full[st]);
-        if constexpr (PACKED) {
-#pragma unroll
-            for (int n = 0; n < NIN; ++n) {
-                const int8_t* q = n == 0 ? g.x8.q : n == 1 ? g.f8.q : g.i8.q;
-                copy_row<int8_t, VEC>(q + (t.row + m) * g.D + t.d0, t.channels, q + g.B * g.L * g.D,
-                                      stage + Stage::kDy + n * Stage::kIn + m * Rows<int8_t, CH, VEC>::kPitch, &mem.full[st]);
+        if constexpr (VEC) {
+            if (m == 0) {
+                barrier_expect(&mem.full[st], Stage::kDy);
+                copy_tile(&maps.dy, (int)t.d0, (int)(t.row - t.b * g.L), (int)t.b, stage, &mem.full[st]);
             }
-        } else {
-            copy_inputs<T, C, VEC, GATE>(g, t, m, stage + Stage::kDy, &mem.full[st]);
+        } else if (m < t.tokens) {
+            const T* dy = (const T*)g.dy;
+            copy_row<T>(dy + (t.row + m) * g.D + t.d0, t.channels, dy + g.B * g.L * g.D,
+                        stage + m * Rows<T, CH, VEC>::kPitch, &mem.full[st]);
         }
+        copy_inputs<typename Stage::V, C, VEC, NIN>(g, maps, t, m, stage + Stage::kDy, &mem.full[st]);
     };
     copies(mem.tile[0], 0);
     put_tile_data<K, GATE>(g, mem, 0, mem.tile[0], m, lam_of(mem.tile[0]), reset_of(mem.tile[0]));
@@ -790,7 +826,7 @@ __device__ __forceinline__ void backward_manage(const Args& g, BackMem<C>& mem, 
         for (int n = 0; n < NIN; ++n) scale[n] = scale_of(coming, n);
         const Vec<K> start = get_lane<K>(g.dh_last && search.block == 0 ? g.dh_last + t.b * g.D + t.d0 : nullptr, m, t.channels);
         meet<kMaps>();                                     // the tile before is through
-        copies(coming, st);
+        if (VEC) copies(coming, st);
         if (it > 0) flush(mem.tile[(it - 1) & 3]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -798,6 +834,7 @@ __device__ __forceinline__ void backward_manage(const Args& g, BackMem<C>& mem, 
             state = lane_map<K>(mem.map[w], m)(state);
         }
         meet_arrive<kStates>();
+        if (!VEC) copies(coming, st);
         if (PACKED && g.edge_h && t.order > 0) put_lane<K>(g.edge_h + (t.k + 1) * g.D + t.d0, state, m, t.channels);
         put_tile_data<K, GATE>(g, mem, st, coming, m, lam, reset);
 #pragma unroll
@@ -826,9 +863,9 @@ __device__ __forceinline__ void backward_manage(const Args& g, BackMem<C>& mem, 
 }
 
 template <typename T, int C, int GATE, bool VEC, bool PACKED>
-__global__ void __launch_bounds__(kThreads, 2) k_gated_tile_bwd(Args g)
+__global__ void __launch_bounds__(kThreads, 2) k_gated_tile_bwd(Args g, const __grid_constant__ Maps maps)
 {
-    extern __shared__ __align__(16) unsigned char stages[];
+    extern __shared__ __align__(128) unsigned char stages[];
     __shared__ __align__(16) BackMem<C> mem;
     if (threadIdx.x == 0) {
         for (int k = 0; k < 2; ++k) barrier_init(&mem.full[k], 32 * kManagers);
@@ -837,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_gated_tile_bwd(Args g)
     }
     __syncthreads();
     if (threadIdx.x < 32 * kWarps) backward_compute<T, C, GATE, VEC, PACKED>(g, mem, stages);
-    else backward_manage<T, C, GATE, VEC, PACKED>(g, mem, stages);
+    else backward_manage<T, C, GATE, VEC, PACKED>(g, maps, mem, stages);
 }
 
 // With 8-bit copies the states run in pieces of 64 tokens from the kept states,
@@ -1013,7 +1050,7 @@ struct Fits {
 
 // Blocks that stay: as many as fit the card.
 template <typename K>
-cudaError_t launch_tiles(K kernel, Fits& fits, const Args& g, size_t smem, cudaStream_t s)
+cudaError_t launch_tiles(K kernel, Fits& fits, const Args& g, const Maps& maps, size_t smem, cudaStream_t s)
 {
     int device = 0;
     const cudaError_t got = cudaGetDevice(&device);
@@ -1028,9 +1065,43 @@ cudaError_t launch_tiles(K kernel, Fits& fits, const Args& g, size_t smem, cudaS
         if (kept) fits.on[device].store(per, std::memory_order_relaxed);
     }
     const uint32_t most = 148u * (uint32_t)per;
-    kernel<<<g.tiles < most ? g.tiles : most, kThreads, smem, s>>>(g);
+    kernel<<<g.tiles < most ? g.tiles : most, kThreads, smem, s>>>(g, maps);
     return cudaGetLastError();
 }
+
+// cuTensorMapEncodeTiled, asked for by name (the library loads without a
+// driver too).
+decltype(&cuTensorMapEncodeTiled) encoder()
+{
+    static std::atomic<void*> found{nullptr};
+    void* f = found.load(std::memory_order_relaxed);
+    if (!f) {
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            return nullptr;
+        found.store(f, std::memory_order_relaxed);
+    }
+    return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(f);
+}
+
+// A [B, L, D] tensor of `es`-byte elements, rows ld elements apart, in boxes
+// of 64 tokens and `channels` channels.
+bool encode(CUtensorMap& map, const void* base, size_t es, const Args& g, int64_t ld, int channels)
+{
+    const cuuint64_t dims[3] = {(cuuint64_t)g.D, (cuuint64_t)g.L, (cuuint64_t)g.B};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * es, (cuuint64_t)(g.L * ld) * es};
+    const cuuint32_t box[3] = {(cuuint32_t)channels, (cuuint32_t)kTok, 1}, step[3] = {1, 1, 1};
+    const CUtensorMapDataType type = es == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const auto f = encoder();
+    return f && f(&map, type, 3, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Whether the copy engine's strides hold this (below 2^40 bytes).
+bool strides_fit(const Args& g, int64_t ld, size_t es) { return (double)g.L * (double)ld * (double)es < 1099511627776.0; }
 
 struct Forward {
     const Args& g;
@@ -1045,12 +1116,19 @@ struct Forward {
         }
         static Fits fits[4];
         constexpr int C = fwd_channels(sizeof(T), true);
+        Maps maps;
+        memset(&maps, 0, sizeof maps);
+        if (vec) {
+            const void* in[3] = {g.x, g.f, g.i};
+            for (int n = 0; n < inputs_of(GATE); ++n)
+                if (!encode(maps.in[n], in[n], sizeof(T), g, g.ld, 32 * C)) return cudaErrorInvalidValue;
+        }
         constexpr size_t smem = 2 * forward_stage_bytes<T, C, true, GATE>(), odd = 2 * forward_stage_bytes<T, 2, false, GATE>();
         if (vec)
-            return pack ? launch_tiles(k_gated_tile<T, C, GATE, true, true>, fits[0], g, smem, s)
-                        : launch_tiles(k_gated_tile<T, C, GATE, true, false>, fits[1], g, smem, s);
-        return pack ? launch_tiles(k_gated_tile<T, 2, GATE, false, true>, fits[2], g, odd, s)
-                    : launch_tiles(k_gated_tile<T, 2, GATE, false, false>, fits[3], g, odd, s);
+            return pack ? launch_tiles(k_gated_tile<T, C, GATE, true, true>, fits[0], g, maps, smem, s)
+                        : launch_tiles(k_gated_tile<T, C, GATE, true, false>, fits[1], g, maps, smem, s);
+        return pack ? launch_tiles(k_gated_tile<T, 2, GATE, false, true>, fits[2], g, maps, odd, s)
+                    : launch_tiles(k_gated_tile<T, 2, GATE, false, false>, fits[3], g, maps, odd, s);
     }
 };
 
@@ -1067,10 +1145,20 @@ struct Backward {
         }
         constexpr int C = kBwdC, NIN = inputs_of(GATE);
         static Fits fits[2];
+        Maps maps;
+        memset(&maps, 0, sizeof maps);
+        if (vec) {
+            const void* in[3] = {PACKED ? (const void*)g.x8.q : g.x, PACKED ? (const void*)g.f8.q : g.f,
+                                 PACKED ? (const void*)g.i8.q : g.i};
+            if (!encode(maps.dy, g.dy, sizeof(T), g, g.D, 32 * C)) return cudaErrorInvalidValue;
+            for (int n = 0; n < NIN; ++n)
+                if (!encode(maps.in[n], in[n], PACKED ? 1 : sizeof(T), g, PACKED ? g.D : g.ld, 32 * C))
+                    return cudaErrorInvalidValue;
+        }
         const cudaError_t e =
-            vec ? launch_tiles(k_gated_tile_bwd<T, C, GATE, true, PACKED>, fits[0], g,
+            vec ? launch_tiles(k_gated_tile_bwd<T, C, GATE, true, PACKED>, fits[0], g, maps,
                                2 * BackStage<T, C, true, PACKED>::bytes(NIN), s)
-                : launch_tiles(k_gated_tile_bwd<T, C, GATE, false, PACKED>, fits[1], g,
+                : launch_tiles(k_gated_tile_bwd<T, C, GATE, false, PACKED>, fits[1], g, maps,
                                2 * BackStage<T, C, false, PACKED>::bytes(NIN), s);
         if (e != cudaSuccess || !g.edge_h) return e;
         k_gated_edge<T, GATE><<<(unsigned)div_up(g.B * (g.K - 1) * g.D, 128), 128, 0, s>>>(g);
@@ -1145,7 +1233,8 @@ mru_status mru_gated_scan(const mru_gated_problem* p, const mru_gated_inputs* in
         }
     }
     if (b.clash()) return MRU_ERR_INVALID_ARG;
-    const bool vec = width % 16 == 0 && pitch % 16 == 0 && aligned(g.x, 16) && aligned(g.f, 16) && aligned(g.i, 16);
+    const bool vec = width % 16 == 0 && pitch % 16 == 0 && strides_fit(g, g.ld, es) && aligned(g.x, 16) &&
+                     aligned(g.f, 16) && aligned(g.i, 16);
     const Layout W = layout(*p, false, vec);
     if (ws && ws_bytes < mru_gated_workspace_size(p)) return MRU_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -1232,11 +1321,11 @@ mru_status mru_gated_scan_backward(const mru_gated_problem* p, const mru_gated_i
         g.edge_d = reinterpret_cast<float*>(edge + one);
         g.edge_q = reinterpret_cast<float*>(edge + 2 * one);
     }
-    bool vec = width % 16 == 0 && aligned(dy, 16);
+    bool vec = width % 16 == 0 && strides_fit(g, g.D, es) && aligned(dy, 16);
     if (packed)
         vec = vec && g.D % 16 == 0 && aligned(saved->x.q, 16) && aligned(saved->f.q, 16) && aligned(saved->i.q, 16);
     else
-        vec = vec && pitch % 16 == 0 && aligned(g.x, 16) && aligned(g.f, 16) && aligned(g.i, 16);
+        vec = vec && pitch % 16 == 0 && strides_fit(g, g.ld, es) && aligned(g.x, 16) && aligned(g.f, 16) && aligned(g.i, 16);
     e = by_type(p->dtype, p->gate, Backward{g, vec, packed, s});
     if (e == cudaSuccess && dlam) {
         const int64_t parts = g.B * (g.K > 0 ? g.K : 1);

@@ -2,6 +2,8 @@
 // and 64 channels is brought on chip and how its carry is found.
 #pragma once
 
+#include <cuda.h>
+
 #include "mru_ops.cuh"
 
 namespace mru {
@@ -392,32 +394,43 @@ struct Search {
 
 // ------------------------------------------------------- loads and stores ---
 
-// A row's piece of an input into shared memory (16-byte aligned, pitch bytes
-// apart), by one thread.  VEC: rows start on 16 bytes and hold whole pieces of
-// them; else the aligned pieces that hold the row, except where they would end
-// behind the last row: that row goes element by element.  Returns the bytes
-// under way.
-template <typename V, bool VEC>
-__device__ __forceinline__ int copy_row(const V* from, int channels, const V* end, unsigned char* to, uint64_t* full)
+// The tensors that the copy engine reads tiles of (rows that start on 16
+// bytes): [B, L, D], a box of 64 tokens and a tile's channels.
+struct Maps {
+    CUtensorMap dy, in[3];
+};
+
+// A tile of a tensor into shared memory, by one thread, zeros past the last
+// token and channel; t: first token in the sequence.
+__device__ __forceinline__ void copy_tile(const CUtensorMap* map, int d0, int t, int b, unsigned char* to, uint64_t* full)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            shared_address(to)),
+        "l"(map), "r"(d0), "r"(t), "r"(b), "r"(shared_address(full))
+        : "memory");
+}
+
+// A row's piece of an input whose rows start anywhere into shared memory, by
+// one thread: the aligned 16-byte pieces that hold it, except where they would
+// end behind the last row, which goes element by element.
+template <typename V>
+__device__ __forceinline__ void copy_row(const V* from, int channels, const V* end, unsigned char* to, uint64_t* full)
 {
     uintptr_t first = reinterpret_cast<uintptr_t>(from);
-    int bytes = channels * (int)sizeof(V);
-    if constexpr (!VEC) {
-        const unsigned off = (unsigned)(first & 15);
-        first -= off;
-        bytes = (bytes + (int)off + 15) & ~15;
-        if (first + (uintptr_t)bytes > reinterpret_cast<uintptr_t>(end)) {
-            V* put = reinterpret_cast<V*>(to + off);
-            for (int c = 0; c < channels; ++c) put[c] = from[c];
-            return 0;
-        }
+    const unsigned off = (unsigned)(first & 15);
+    first -= off;
+    const int bytes = (channels * (int)sizeof(V) + (int)off + 15) & ~15;
+    if (first + (uintptr_t)bytes > reinterpret_cast<uintptr_t>(end)) {
+        V* put = reinterpret_cast<V*>(to + off);
+        for (int c = 0; c < channels; ++c) put[c] = from[c];
+        return;
     }
     barrier_expect(full, bytes);
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                      shared_address(to)),
                  "l"(first), "r"(bytes), "r"(shared_address(full))
                  : "memory");
-    return bytes;
 }
 
 // Where an input's rows lie in a stage: pitch, and (not VEC) how far a row
