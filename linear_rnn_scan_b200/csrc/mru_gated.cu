@@ -153,8 +153,15 @@ __global__ void __launch_bounds__(128) k_gated_short_bwd(Args g)
 // every output written once, and the instructions of an element are few enough
 // for the memory to set the pace.
 
-// Channels of a lane: tiles of 128 channels in bf16's forward, of 64 elsewhere.
-constexpr int fwd_channels(size_t elem, bool vec) { return elem == 2 && vec ? 4 : 2; }
+// Channels of a lane.  Four (tiles of 128 channels, two blocks to an SM) spare
+// instructions, two (64 channels, three blocks) hide more: B4 L4096 D8192 bf16,
+// sigmoid: 176 us with four, 186 with two; B8 L4096 D2048 bf16, lru: 158 and 149,
+// with 8-bit copies 404 and 346; fp32 rows move twice the bytes per instruction:
+// decay B1 L65536 D2048 423 (two blocks) and 351.
+constexpr int fwd_channels(size_t elem, bool vec, int gate, bool pack)
+{
+    return elem == 2 && vec && gate != MRU_GATE_LRU && !pack ? 4 : 2;
+}
 constexpr int kBwdC = 2;
 
 template <int C>
@@ -468,8 +475,8 @@ __device__ __forceinline__ void forward_manage(const Args& g, const Maps& maps, 
         // what can be asked for before the tile's maps are there
         Search<CH> search(g, t, m);
         Lookup<K> near, far;
-        near.ask(search.old_tiles(), search.j, CH);
-        far.ask(search.old_groups(), search.group, CH);
+        uint64_t before[K];
+        search.ask(before, far, near);
         uint32_t drawn = 0;
         if (m == 0) drawn = draw(g, coming.ticket);
         const Vec<K> lam = lam_of(coming);
@@ -481,7 +488,7 @@ __device__ __forceinline__ void forward_manage(const Args& g, const Maps& maps, 
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) own = lane_map<K>(mem.map[w], m).after(own);
         if (!t.last && !(g.withhold && t.ticket == 0)) search.publish_tile(own);
-        const Vec<K> carry = search.carry(g, near, far, start);
+        const Vec<K> carry = search.carry(g, before, far, near, start);
         Vec<K> h = carry;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -501,7 +508,7 @@ __device__ __forceinline__ void forward_manage(const Args& g, const Maps& maps, 
 }
 
 template <typename T, int C, int GATE, bool VEC, bool PACK>
-__global__ void __launch_bounds__(kThreads, 2) k_gated_tile(Args g, const __grid_constant__ Maps maps)
+__global__ void __launch_bounds__(kThreads, C == 2 ? 3 : 2) k_gated_tile(Args g, const __grid_constant__ Maps maps)
 {
     extern __shared__ __align__(128) unsigned char stages[];
     __shared__ __align__(16) TileMem<C> mem;
@@ -815,8 +822,8 @@ __device__ __forceinline__ void backward_manage(const Args& g, const Maps& maps,
         const Tile& coming = mem.tile[(it + 1) & 3];
         Search<CH> search(g, t, m);
         Lookup<K> near, far;
-        near.ask(search.old_tiles(), search.j, CH);
-        far.ask(search.old_groups(), search.group, CH);
+        uint64_t before[K];
+        search.ask(before, far, near);
         uint32_t drawn = 0;
         if (m == 0) drawn = draw(g, coming.ticket);
         const Vec<K> lam = lam_of(coming), next = state_of(coming);
@@ -845,7 +852,7 @@ __device__ __forceinline__ void backward_manage(const Args& g, const Maps& maps,
 #pragma unroll
         for (int w = kWarps - 1; w >= 0; --w) own = lane_map<K>(mem.map[w], m).after(own);
         if (!t.last && !(g.withhold && t.ticket == 0)) search.publish_tile(own);
-        Vec<K> e = search.carry(g, near, far, start);
+        Vec<K> e = search.carry(g, before, far, near, start);
 #pragma unroll
         for (int w = kWarps - 1; w >= 0; --w) {
             put_states<K>(mem.state[w], m, e);
@@ -982,9 +989,9 @@ struct Layout {
     uint32_t tiles, cols, cgs, groups, blocks;
 };
 constexpr size_t kControl = 256;
-Layout layout(const mru_gated_problem& p, bool backward, bool vec)
+Layout layout(const mru_gated_problem& p, bool backward, int channels)
 {
-    const int64_t kCh = 32 * (backward ? kBwdC : fwd_channels(elem_size(p.dtype), vec));
+    const int64_t kCh = 32 * channels;
     Layout W;
     memset(&W, 0, sizeof W);
     const int64_t K = div_up(p.L, kKeep);
@@ -1115,17 +1122,18 @@ struct Forward {
             return cudaGetLastError();
         }
         static Fits fits[4];
-        constexpr int C = fwd_channels(sizeof(T), true);
+        constexpr int C = fwd_channels(sizeof(T), true, GATE, false), P = fwd_channels(sizeof(T), true, GATE, true);
         Maps maps;
         memset(&maps, 0, sizeof maps);
         if (vec) {
             const void* in[3] = {g.x, g.f, g.i};
             for (int n = 0; n < inputs_of(GATE); ++n)
-                if (!encode(maps.in[n], in[n], sizeof(T), g, g.ld, 32 * C)) return cudaErrorInvalidValue;
+                if (!encode(maps.in[n], in[n], sizeof(T), g, g.ld, 32 * (pack ? P : C))) return cudaErrorInvalidValue;
         }
-        constexpr size_t smem = 2 * forward_stage_bytes<T, C, true, GATE>(), odd = 2 * forward_stage_bytes<T, 2, false, GATE>();
+        constexpr size_t smem = 2 * forward_stage_bytes<T, C, true, GATE>(), packs = 2 * forward_stage_bytes<T, P, true, GATE>();
+        constexpr size_t odd = 2 * forward_stage_bytes<T, 2, false, GATE>();
         if (vec)
-            return pack ? launch_tiles(k_gated_tile<T, C, GATE, true, true>, fits[0], g, maps, smem, s)
+            return pack ? launch_tiles(k_gated_tile<T, P, GATE, true, true>, fits[0], g, maps, packs, s)
                         : launch_tiles(k_gated_tile<T, C, GATE, true, false>, fits[1], g, maps, smem, s);
         return pack ? launch_tiles(k_gated_tile<T, 2, GATE, false, true>, fits[2], g, maps, odd, s)
                     : launch_tiles(k_gated_tile<T, 2, GATE, false, false>, fits[3], g, maps, odd, s);
@@ -1181,14 +1189,14 @@ extern "C" {
 size_t mru_gated_workspace_size(const mru_gated_problem* p)
 {
     if (check_problem(p) != MRU_OK) return 0;
-    // for either column layout
-    const size_t a = layout(*p, false, false).bytes, b = layout(*p, false, true).bytes;
+    // for either width of a tile
+    const size_t a = layout(*p, false, 2).bytes, b = layout(*p, false, 4).bytes;
     return a > b ? a : b;
 }
 
 size_t mru_gated_backward_workspace_size(const mru_gated_problem* p)
 {
-    return check_problem(p) == MRU_OK ? layout(*p, true, true).bytes : 0;
+    return check_problem(p) == MRU_OK ? layout(*p, true, kBwdC).bytes : 0;
 }
 
 mru_status mru_gated_scan(const mru_gated_problem* p, const mru_gated_inputs* in, void* y, float* h_last,
@@ -1235,7 +1243,8 @@ mru_status mru_gated_scan(const mru_gated_problem* p, const mru_gated_inputs* in
     if (b.clash()) return MRU_ERR_INVALID_ARG;
     const bool vec = width % 16 == 0 && pitch % 16 == 0 && strides_fit(g, g.ld, es) && aligned(g.x, 16) &&
                      aligned(g.f, 16) && aligned(g.i, 16);
-    const Layout W = layout(*p, false, vec);
+    const bool here = pack && p->L > kShort;                        // 8-bit copies in the same pass
+    const Layout W = layout(*p, false, fwd_channels(es, vec, p->gate, here));
     if (ws && ws_bytes < mru_gated_workspace_size(p)) return MRU_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
@@ -1246,7 +1255,6 @@ mru_status mru_gated_scan(const mru_gated_problem* p, const mru_gated_inputs* in
     g.y = y;
     g.h_last = h_last;
     g.states = saved ? saved->states : nullptr;
-    const bool here = pack && p->L > kShort;                        // copies in the same pass
     if (here) { g.x8 = saved->x; g.f8 = saved->f; g.i8 = saved->i; }
     e = by_type(p->dtype, p->gate, Forward{g, vec, here, s});
     if (e != cudaSuccess || !pack || !tokens || here) return cuda_status(e);
@@ -1300,7 +1308,7 @@ mru_status mru_gated_scan_backward(const mru_gated_problem* p, const mru_gated_i
     b.out(dh0, state);
     b.out(ws, ws_bytes);
     if (b.clash()) return MRU_ERR_INVALID_ARG;
-    const Layout W = layout(*p, true, true);
+    const Layout W = layout(*p, true, kBwdC);
     if (ws_bytes < W.bytes) return MRU_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;

@@ -271,6 +271,26 @@ __device__ __forceinline__ void peek(const uint64_t* at, uint64_t (&u)[K])
         asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(u[0]) : "l"(at) : "memory");
 }
 
+// A warp waits until every lane finds `there`, asking `again` each time, for a
+// limited time; false: it gave up.
+template <typename There, typename Again>
+__device__ __forceinline__ bool spin(const Args& g, There there, Again again)
+{
+    uint64_t t0 = 0;
+    for (int n = 0; !__all_sync(~0u, there()); ++n) {
+        again();
+        if ((n & 63) != 63) continue;
+        uint32_t stop;
+        asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(stop) : "l"(g.abort) : "memory");
+        const uint64_t t = now_ns();
+        if (t0 == 0) t0 = t;
+        const bool out = (threadIdx.x & 31) == 0 && t - t0 > g.wait_ns;
+        if (out) give_up(g);
+        if (__any_sync(~0u, out || stop)) return false;
+    }
+    return true;
+}
+
 // A lane's carry: what it is made of, oldest first, in two lists that are
 // looked up while other work is done.
 template <int K>
@@ -287,27 +307,19 @@ struct Lookup {
             if (k < (int)count) peek<K>(at + k * gap, u[k]);
         }
     }
+    __device__ __forceinline__ bool there(uint32_t count) const
+    {
+        bool all = true;
+#pragma unroll
+        for (int k = 0; k < kFan; ++k)
+#pragma unroll
+            for (int c = 0; c < K; ++c) all = all && (k >= (int)count || u[k][c] != 0);
+        return all;
+    }
     // Waits until they are there, for a limited time; false: it gave up.
     __device__ __forceinline__ bool await(const Args& g, const uint64_t* at, uint32_t count, uint64_t gap)
     {
-        uint64_t t0 = 0;
-        for (int n = 0;; ++n) {
-            bool there = true;
-#pragma unroll
-            for (int k = 0; k < kFan; ++k)
-#pragma unroll
-                for (int c = 0; c < K; ++c) there = there && (k >= (int)count || u[k][c] != 0);
-            if (__all_sync(~0u, there)) return true;
-            ask(at, count, gap);
-            if ((n & 63) != 63) continue;
-            uint32_t stop;
-            asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(stop) : "l"(g.abort) : "memory");
-            const uint64_t t = now_ns();
-            if (t0 == 0) t0 = t;
-            const bool out = (threadIdx.x & 31) == 0 && t - t0 > g.wait_ns;
-            if (out) give_up(g);
-            if (__any_sync(~0u, out || stop)) return false;
-        }
+        return spin(g, [&]() { return there(count); }, [&]() { ask(at, count, gap); });
     }
     // Their composition applied to h.
     __device__ __forceinline__ Vec<K> apply(uint32_t count, Vec<K> h) const
@@ -351,17 +363,28 @@ struct Search {
     __device__ __forceinline__ const uint64_t* old_tiles() const { return tiles + (uint64_t)(order() - j) * CH; }
     __device__ __forceinline__ const uint64_t* old_groups() const { return groups + (uint64_t)(block * kFan) * CH; }
     __device__ __forceinline__ void publish_tile(const Map<K>& own) { publish<K>(tiles + (uint64_t)order() * CH, own); }
-    // The state before the tile.  `start`: before the first one (h0, or the
-    // last state's gradient).
-    __device__ __forceinline__ Vec<K> carry(const Args& g, Lookup<K>& near, Lookup<K>& far, const Vec<K>& start)
+    // Asks for what the carry is made of: the block's carry in (first), groups
+    // (far) and tiles (near).
+    __device__ __forceinline__ void ask(uint64_t (&first)[K], Lookup<K>& far, Lookup<K>& near) const
+    {
+#pragma unroll
+        for (int c = 0; c < K; ++c) first[c] = 0;
+        if (block) peek<K>(blocks + (uint64_t)block * CH, first);
+        far.ask(old_groups(), group, CH);
+        near.ask(old_tiles(), j, CH);
+    }
+    // The state before the tile, waited for.  `start`: before the first one
+    // (h0, or the last state's gradient).
+    __device__ __forceinline__ Vec<K> carry(const Args& g, uint64_t (&first)[K], Lookup<K>& far, Lookup<K>& near,
+                                            const Vec<K>& start) const
     {
         Vec<K> h = start;
         bool fine = true;
         if (block) {
-            Lookup<K> one;
-            one.ask(blocks + (uint64_t)block * CH, 1, CH);
-            fine = one.await(g, blocks + (uint64_t)block * CH, 1, CH);
-            h = one.apply(1, h);
+            const uint64_t* at = blocks + (uint64_t)block * CH;
+            fine = spin(g, [&]() { return first[0] != 0 && first[K - 1] != 0; }, [&]() { peek<K>(at, first); });
+#pragma unroll
+            for (int c = 0; c < K; ++c) h.v[c] = word_H(first[c]);
         }
         if (group) {
             fine = far.await(g, old_groups(), group, CH) && fine;
