@@ -337,10 +337,12 @@ struct HeldFeed {
                     else u.x = *reinterpret_cast<const uint32_t*>(stage + at * 4);
                     s = *reinterpret_cast<const float*>(stage + NV * threads<LAY>() * 8 + at * 4);
                 }
-#pragma unroll
-                for (int j = 0; j < U / 2; ++j) {
-                    const uint32_t b = (j < 2 ? u.x : u.y) >> (16 * (j % 2));
-                    v[i * U / 2 + j] = F2{(float)(int8_t)b, (float)(int8_t)(b >> 8)} * both(s);
+                const uint32_t lo = flip_bytes(u.x), hi = flip_bytes(u.y);
+                v[i * U / 2] = F2{byte_f32<0>(lo), byte_f32<1>(lo)} * both(s);
+                v[i * U / 2 + 1] = F2{byte_f32<2>(lo), byte_f32<3>(lo)} * both(s);
+                if constexpr (U == 8) {
+                    v[2] = F2{byte_f32<0>(hi), byte_f32<1>(hi)} * both(s);
+                    v[3] = F2{byte_f32<2>(hi), byte_f32<3>(hi)} * both(s);
                 }
             }
         }

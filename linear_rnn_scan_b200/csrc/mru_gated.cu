@@ -232,70 +232,52 @@ __device__ __forceinline__ bool all_near(const Vec<C>& csp)
     return __all_sync(~0u, near);
 }
 
-// 8-bit copies of a warp's tokens.  A run of 64 channels is the whole row or
-// half a row's lanes; the largest magnitudes of all runs (input, token, half)
-// are found first and a lane takes the factors of one or two of them for all.
+// 8-bit copies of a warp's tokens.  A run of 64 channels is a warp's row; the
+// largest magnitudes of all runs (input, token) are found first and a lane
+// takes the factors of one of them for all.
 template <typename T, int C, bool VEC, int NIN>
 __device__ __forceinline__ void pack_rows(const Args& g, const Tile& t, int w, int lane,
                                           const Rows<T, 32 * C, VEC> (&in)[NIN], bool wide8)
 {
-    constexpr int HALVES = C / 2, RUNS = NIN * kStep * HALVES, SETS = (RUNS + 31) / 32;
-    uint32_t mine[SETS];
-#pragma unroll
-    for (int k = 0; k < SETS; ++k) mine[k] = 0;
+    static_assert(C == 2, "a row is one run of 64 channels");
+    static_assert(NIN * kStep <= 32, "a lane to a run");
+    const bool part = t.channels < 64;                       // what lies behind the last channel does not count
+    uint32_t mine = 0;
 #pragma unroll
     for (int n = 0; n < NIN; ++n)
 #pragma unroll
         for (int s = 0; s < kStep; ++s) {
-            const Vec<C> v = read_row<C, VEC>(in[n].row(w * kStep + s), lane);
-            uint32_t m = 0;
-#pragma unroll
-            for (int c = 0; c < C; ++c) m = max(m, channel<C, VEC>(lane, c) < t.channels ? mag_bits(v.v[c]) : 0u);
-#pragma unroll
-            for (int h = 0; h < HALVES; ++h) {
-                const int run = (n * kStep + s) * HALVES + h;
-                const uint32_t r = __reduce_max_sync(~0u, lane * HALVES / 32 == h ? m : 0u);
-                if (lane == run % 32) mine[run / 32] = r;
+            Vec<C> v = read_row<C, VEC>(in[n].row(w * kStep + s), lane);
+            if (part) {
+                if (channel<C, VEC>(lane, 0) >= t.channels) v.v[0] = 0.0f;
+                if (channel<C, VEC>(lane, 1) >= t.channels) v.v[1] = 0.0f;
             }
+            const uint32_t r = __reduce_max_sync(~0u, max(mag_bits(v.v[0]), mag_bits(v.v[1])));
+            if (lane == n * kStep + s) mine = r;
         }
-    float inv[SETS];
+    float inv, scale;
+    pack8_factors(__uint_as_float(mine), inv, scale);
     const int64_t row0 = t.row + w * kStep, runs = (g.D + 63) / 64;
     const int left = t.tokens - w * kStep;
-#pragma unroll
-    for (int k = 0; k < SETS; ++k) {
-        float scale;
-        pack8_factors(__uint_as_float(mine[k]), inv[k], scale);
-        const int run = 32 * k + lane, h = run % HALVES, s = run / HALVES % kStep, n = run / HALVES / kStep;
-        if (n < NIN && s < left && h * 64 < t.channels) {
-            float* to = n == 0 ? g.x8.scale : n == 1 ? g.f8.scale : g.i8.scale;
-            to[(row0 + s) * runs + t.d0 / 64 + h] = scale;
-        }
+    if (lane < NIN * kStep && lane % kStep < left) {
+        float* to = lane < kStep ? g.x8.scale : lane < 2 * kStep ? g.f8.scale : g.i8.scale;
+        to[(row0 + lane % kStep) * runs + t.d0 / 64] = scale;
     }
+    const bool in_row = 2 * lane < t.channels;
 #pragma unroll
     for (int n = 0; n < NIN; ++n) {
         int8_t* at = (n == 0 ? g.x8.q : n == 1 ? g.f8.q : g.i8.q) + row0 * g.D + t.d0;
 #pragma unroll
         for (int s = 0; s < kStep; ++s, at += g.D) {
-            const int run = (n * kStep + s) * HALVES;
-            float k = __shfl_sync(~0u, inv[run / 32], run % 32);
-            if (HALVES == 2) {
-                const float k1 = __shfl_sync(~0u, inv[run / 32], run % 32 + 1);
-                if (lane >= 16) k = k1;
-            }
-            if (s >= left) continue;
+            const float k = __shfl_sync(~0u, inv, n * kStep + s);
             const Vec<C> v = read_row<C, VEC>(in[n].row(w * kStep + s), lane);
-            uint32_t q = 0;
-#pragma unroll
-            for (int c = 0; c < C; ++c) q |= (uint32_t)pack8_q(v.v[c], k) << (8 * c);
+            const uint32_t q0 = (uint32_t)pack8_q(v.v[0], k), q1 = (uint32_t)pack8_q(v.v[1], k);
+            if (s >= left) continue;
             if (VEC && wide8) {
-                if (C * lane < t.channels) {
-                    if constexpr (C == 4) *reinterpret_cast<uint32_t*>(at + 4 * lane) = q;
-                    else *reinterpret_cast<uint16_t*>(at + 2 * lane) = (uint16_t)q;
-                }
+                if (in_row) *reinterpret_cast<uint16_t*>(at + 2 * lane) = (uint16_t)__byte_perm(q0, q1, 0x0040);
             } else {
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-                    if (channel<C, VEC>(lane, c) < t.channels) at[channel<C, VEC>(lane, c)] = (int8_t)(q >> (8 * c));
+                if (channel<C, VEC>(lane, 0) < t.channels) at[channel<C, VEC>(lane, 0)] = (int8_t)q0;
+                if (channel<C, VEC>(lane, 1) < t.channels) at[channel<C, VEC>(lane, 1)] = (int8_t)q1;
             }
         }
     }
@@ -358,31 +340,29 @@ constexpr size_t forward_stage_bytes()
     return (size_t)inputs_of(GATE) * kTok * Rows<T, 32 * C, VEC>::kPitch;
 }
 
-// Starts the copies of a tile's inputs (V: their type in memory) by the
-// managers: the copy engine's own tiles by the first of them, or a token's rows
-// by each.
-template <typename V, int C, bool VEC, int NIN>
-__device__ __forceinline__ void copy_inputs(const Args& g, const Maps& maps, const Tile& t, int m, unsigned char* stage,
-                                            uint64_t* full)
+// A tile's inputs (V: their type in memory) on their way into a stage: by the
+// copy engine, started by one manager, or by the warps that compute, each its
+// own rows.
+template <typename V, int C, int NIN>
+__device__ __forceinline__ void copy_inputs(const Maps& maps, const Tile& t, int64_t L, unsigned char* stage, uint64_t* full)
 {
-    constexpr int CH = 32 * C, kPitch = Rows<V, CH, VEC>::kPitch;
-    if constexpr (VEC) {
-        if (m != 0) return;
-        barrier_expect(full, NIN * kTok * kPitch);
+    constexpr int kPitch = Rows<V, 32 * C, true>::kPitch;
+    barrier_expect(full, NIN * kTok * kPitch);
 #pragma unroll
-        for (int n = 0; n < NIN; ++n)
-            copy_tile(&maps.in[n], (int)t.d0, (int)(t.row - t.b * g.L), (int)t.b, stage + n * kTok * kPitch, full);
-    } else {
-        if (m >= t.tokens) return;
-        constexpr bool held = sizeof(V) == 1;
-        const int64_t ld = held ? g.D : g.ld;
+    for (int n = 0; n < NIN; ++n)
+        copy_tile(&maps.in[n], (int)t.d0, (int)(t.row - t.b * L), (int)t.b, stage + n * kTok * kPitch, full);
+}
+template <typename V, int C, int NIN>
+__device__ __forceinline__ void copy_input_rows(const Args& g, const Tile& t, int w, int lane, unsigned char* stage)
+{
+    constexpr int CH = 32 * C, kPitch = Rows<V, CH, false>::kPitch;
+    constexpr bool held = sizeof(V) == 1;
+    const int64_t ld = held ? g.D : g.ld;
 #pragma unroll
-        for (int n = 0; n < NIN; ++n) {
-            const V* base = (const V*)(held ? (const void*)(n == 0 ? g.x8.q : n == 1 ? g.f8.q : g.i8.q)
-                                            : n == 0 ? g.x : n == 1 ? g.f : g.i);
-            copy_row<V>(base + (t.row + m) * ld + t.d0, t.channels, base + (g.B * g.L - 1) * ld + g.D,
-                        stage + (n * kTok + m) * kPitch, full);
-        }
+    for (int n = 0; n < NIN; ++n) {
+        const V* base = (const V*)(held ? (const void*)(n == 0 ? g.x8.q : n == 1 ? g.f8.q : g.i8.q)
+                                        : n == 0 ? g.x : n == 1 ? g.f : g.i);
+        copy_rows<V, CH, kPitch>(base, ld, base + (g.B * g.L - 1) * ld + g.D, t, w, lane, stage + n * kTok * kPitch);
     }
 }
 
@@ -401,7 +381,7 @@ __device__ __forceinline__ void put_tile_data(const Args& g, M& mem, int st, con
 }
 
 template <typename T, int C, int GATE, bool VEC, bool PACK>
-__device__ __forceinline__ void forward_compute(const Args& g, TileMem<C>& mem, const unsigned char* stages)
+__device__ __forceinline__ void forward_compute(const Args& g, TileMem<C>& mem, unsigned char* stages)
 {
     constexpr int NIN = inputs_of(GATE), CH = 32 * C;
     constexpr size_t kBytes = forward_stage_bytes<T, C, VEC, GATE>();
@@ -414,6 +394,14 @@ __device__ __forceinline__ void forward_compute(const Args& g, TileMem<C>& mem, 
         barrier_wait(g, &mem.full[st], it >> 1 & 1);
         const Tile& t = mem.tile[it & 3];
         if (t.ticket >= g.tiles) return;
+        if constexpr (!VEC) {
+            const Tile& u = mem.tile[(it + 1) & 3];
+            if (it == 0) copy_input_rows<T, C, NIN>(g, t, w, lane, stages);
+            copies_commit();
+            if (u.ticket < g.tiles) copy_input_rows<T, C, NIN>(g, u, w, lane, stages + (st ^ 1) * kBytes);
+            copies_commit();
+            copies_wait();
+        }
         const int n = min(max(t.valid - w * kStep, 0), kStep), left = t.tokens - w * kStep, channels = t.channels;
         const uint32_t resets = mem.resets[st][w / 4] >> (w % 4 * kStep) & 0xffu;
         const unsigned char* stage = stages + st * kBytes;
@@ -459,7 +447,8 @@ __device__ __forceinline__ void forward_manage(const Args& g, const Maps& maps, 
     auto reset_of = [&](const Tile& t) { return g.reset && t.ticket < g.tiles && m < t.tokens && g.reset[t.row + m]; };
     auto lam_of = [&](const Tile& t) { return get_lane<K>(lru && t.ticket < g.tiles ? g.lam + t.d0 : nullptr, m, t.channels); };
     auto copies = [&](const Tile& t, int st) {
-        if (t.ticket < g.tiles) copy_inputs<T, C, VEC, inputs_of(GATE)>(g, maps, t, m, stages + st * kBytes, &mem.full[st]);
+        if (VEC && m == 0 && t.ticket < g.tiles)
+            copy_inputs<T, C, inputs_of(GATE)>(maps, t, g.L, stages + st * kBytes, &mem.full[st]);
     };
     for (int k = 0; k < 2; ++k) {
         const Tile& t = mem.tile[k];
@@ -483,7 +472,7 @@ __device__ __forceinline__ void forward_manage(const Args& g, const Maps& maps, 
         const bool reset = reset_of(coming);
         const Vec<K> start = get_lane<K>(g.h0 && search.block == 0 ? g.h0 + t.b * g.D + t.d0 : nullptr, m, t.channels);
         meet<kMaps>();
-        if (VEC) copies(coming, st);                       // the stage has been read
+        copies(coming, st);                                // the stage has been read
         Map<K> own = Map<K>::of(1.0f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) own = lane_map<K>(mem.map[w], m).after(own);
@@ -496,7 +485,6 @@ __device__ __forceinline__ void forward_manage(const Args& g, const Maps& maps, 
             h = lane_map<K>(mem.map[w], m)(h);
         }
         meet_arrive<kCarry>();
-        if (!VEC) copies(coming, st);                      // row by row, which takes longer
         if (!t.last) search.publish_up(near, own, h);
         else if (g.h_last) put_lane<K>(g.h_last + t.b * g.D + t.d0, h, m, t.channels);
         if (g.states) put_lane<K>(g.states + t.k * g.D + t.d0, carry, m, t.channels);
@@ -695,7 +683,7 @@ __device__ __forceinline__ void write_gradients(const Args& g, const Rows<T, 32 
 }
 
 template <typename T, int C, int GATE, bool VEC, bool PACKED>
-__device__ __forceinline__ void backward_compute(const Args& g, BackMem<C>& mem, const unsigned char* stages)
+__device__ __forceinline__ void backward_compute(const Args& g, BackMem<C>& mem, unsigned char* stages)
 {
     using Stage = BackStage<T, C, VEC, PACKED>;
     using V = typename Stage::V;
@@ -710,6 +698,19 @@ __device__ __forceinline__ void backward_compute(const Args& g, BackMem<C>& mem,
         barrier_wait(g, &mem.full[st], it >> 1 & 1);
         const Tile& t = mem.tile[it & 3];
         if (t.ticket >= g.tiles) break;
+        if constexpr (!VEC) {
+            auto rows = [&](const Tile& u, unsigned char* to) {
+                const T* dy = (const T*)g.dy;
+                copy_rows<T, CH, Rows<T, CH, VEC>::kPitch>(dy, g.D, dy + g.B * g.L * g.D, u, w, lane, to);
+                copy_input_rows<V, C, NIN>(g, u, w, lane, to + Stage::kDy);
+            };
+            const Tile& u = mem.tile[(it + 1) & 3];
+            if (it == 0) rows(t, stages);
+            copies_commit();
+            if (u.ticket < g.tiles) rows(u, stages + (st ^ 1) * Stage::bytes(NIN));
+            copies_commit();
+            copies_wait();
+        }
         const int n = min(max(t.valid - w * kStep, 0), kStep), left = t.tokens - w * kStep, channels = t.channels;
         const uint32_t resets = mem.resets[st][w / 4] >> (w % 4 * kStep) & 0xffu;
         const bool edge = PACKED && w == 0 && t.row % g.L > 0;
@@ -784,19 +785,11 @@ __device__ __forceinline__ void backward_manage(const Args& g, const Maps& maps,
         return PACKED && valid(t) && m < t.tokens ? h.scale[(t.row + m) * (int64_t)g.cgs + t.d0 / 64] : 0.0f;
     };
     auto copies = [&](const Tile& t, int st) {
-        if (!valid(t)) return;
+        if (!VEC || m != 0 || !valid(t)) return;
         unsigned char* stage = stages + st * Stage::bytes(NIN);
-        if constexpr (VEC) {
-            if (m == 0) {
-                barrier_expect(&mem.full[st], Stage::kDy);
-                copy_tile(&maps.dy, (int)t.d0, (int)(t.row - t.b * g.L), (int)t.b, stage, &mem.full[st]);
-            }
-        } else if (m < t.tokens) {
-            const T* dy = (const T*)g.dy;
-            copy_row<T>(dy + (t.row + m) * g.D + t.d0, t.channels, dy + g.B * g.L * g.D,
-                        stage + m * Rows<T, CH, VEC>::kPitch, &mem.full[st]);
-        }
-        copy_inputs<typename Stage::V, C, VEC, NIN>(g, maps, t, m, stage + Stage::kDy, &mem.full[st]);
+        barrier_expect(&mem.full[st], Stage::kDy);
+        copy_tile(&maps.dy, (int)t.d0, (int)(t.row - t.b * g.L), (int)t.b, stage, &mem.full[st]);
+        copy_inputs<typename Stage::V, C, NIN>(maps, t, g.L, stage + Stage::kDy, &mem.full[st]);
     };
     copies(mem.tile[0], 0);
     put_tile_data<K, GATE>(g, mem, 0, mem.tile[0], m, lam_of(mem.tile[0]), reset_of(mem.tile[0]));
@@ -833,7 +826,7 @@ __device__ __forceinline__ void backward_manage(const Args& g, const Maps& maps,
         for (int n = 0; n < NIN; ++n) scale[n] = scale_of(coming, n);
         const Vec<K> start = get_lane<K>(g.dh_last && search.block == 0 ? g.dh_last + t.b * g.D + t.d0 : nullptr, m, t.channels);
         meet<kMaps>();                                     // the tile before is through
-        if (VEC) copies(coming, st);
+        copies(coming, st);
         if (it > 0) flush(mem.tile[(it - 1) & 3]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -841,7 +834,6 @@ __device__ __forceinline__ void backward_manage(const Args& g, const Maps& maps,
             state = lane_map<K>(mem.map[w], m)(state);
         }
         meet_arrive<kStates>();
-        if (!VEC) copies(coming, st);
         if (PACKED && g.edge_h && t.order > 0) put_lane<K>(g.edge_h + (t.k + 1) * g.D + t.d0, state, m, t.channels);
         put_tile_data<K, GATE>(g, mem, st, coming, m, lam, reset);
 #pragma unroll

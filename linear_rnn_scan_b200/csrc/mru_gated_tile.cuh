@@ -434,44 +434,55 @@ __device__ __forceinline__ void copy_tile(const CUtensorMap* map, int d0, int t,
         : "memory");
 }
 
-// A row's piece of an input whose rows start anywhere into shared memory, by
-// one thread: the aligned 16-byte pieces that hold it, except where they would
-// end behind the last row, which goes element by element.
-template <typename V>
-__device__ __forceinline__ void copy_row(const V* from, int channels, const V* end, unsigned char* to, uint64_t* full)
+// A warp's tokens of an input whose rows start anywhere, into its rows of a
+// stage: the aligned words that hold a row (one that ends behind the last row
+// only as far as that goes).
+template <typename V, int CH, int PITCH>
+__device__ __forceinline__ void copy_rows(const V* base, int64_t ld, const V* end, const Tile& t, int w, int lane,
+                                          unsigned char* to)
 {
-    uintptr_t first = reinterpret_cast<uintptr_t>(from);
-    const unsigned off = (unsigned)(first & 15);
-    first -= off;
-    const int bytes = (channels * (int)sizeof(V) + (int)off + 15) & ~15;
-    if (first + (uintptr_t)bytes > reinterpret_cast<uintptr_t>(end)) {
-        V* put = reinterpret_cast<V*>(to + off);
-        for (int c = 0; c < channels; ++c) put[c] = from[c];
-        return;
+#pragma unroll
+    for (int s = 0; s < kStep; ++s) {
+        const int r = w * kStep + s;
+        if (r >= t.tokens) break;
+        const V* from = base + (t.row + r) * ld + t.d0;
+        const uintptr_t first = reinterpret_cast<uintptr_t>(from) & ~(uintptr_t)3;
+        const int words = (int)((reinterpret_cast<uintptr_t>(from + t.channels) - first + 3) / 4);
+#pragma unroll
+        for (int k = 0; k < (CH * (int)sizeof(V) / 4 + 32) / 32; ++k) {
+            const int i = lane + 32 * k;
+            if (i >= words) continue;
+            const uintptr_t at = first + 4 * (uintptr_t)i, left = reinterpret_cast<uintptr_t>(end) - at;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(shared_address(to + r * PITCH + 4 * i)), "l"(at),
+                         "r"(left < 4 ? (int)left : 4)
+                         : "memory");
+        }
     }
-    barrier_expect(full, bytes);
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     shared_address(to)),
-                 "l"(first), "r"(bytes), "r"(shared_address(full))
-                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the latest group of the lane's copies are there, for its warp.
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
 }
 
 // Where an input's rows lie in a stage: pitch, and (not VEC) how far a row
-// starts behind its 16 bytes.
+// starts behind its first word.
 template <typename V, int CH, bool VEC>
 struct Rows {
-    static constexpr int kPitch = CH * (int)sizeof(V) + (VEC ? 0 : 32);
+    static constexpr int kPitch = CH * (int)sizeof(V) + (VEC ? 0 : 16);
     const unsigned char* base;
-    unsigned off, step;                  // of the tile's first row, and of a row to the next, modulo 16
+    unsigned off, step;                  // of the tile's first row, and of a row to the next, modulo 4
     Rows() = default;
     __device__ __forceinline__ Rows(const unsigned char* b, const void* from, int64_t ld, const Tile& t) : base(b)
     {
-        off = VEC ? 0 : (unsigned)(reinterpret_cast<uintptr_t>((const V*)from + t.row * ld + t.d0) & 15);
-        step = VEC ? 0 : (unsigned)((ld * (int64_t)sizeof(V)) & 15);
+        off = VEC ? 0 : (unsigned)(reinterpret_cast<uintptr_t>((const V*)from + t.row * ld + t.d0) & 3);
+        step = VEC ? 0 : (unsigned)((ld * (int64_t)sizeof(V)) & 3);
     }
     __device__ __forceinline__ const V* row(int r) const
     {
-        return reinterpret_cast<const V*>(base + r * kPitch + (VEC ? 0 : (off + r * step) & 15));
+        return reinterpret_cast<const V*>(base + r * kPitch + (VEC ? 0 : (off + r * step) & 3));
     }
 };
 
@@ -510,9 +521,9 @@ __device__ __forceinline__ Vec<C> read_row(const V* row, int lane)
         }
     } else {
         static_assert(C == 2, "8-bit rows: two channels to a lane");
-        const char2 q = *reinterpret_cast<const char2*>(row + 2 * lane);
-        r.v[0] = (float)(signed char)q.x;
-        r.v[1] = (float)(signed char)q.y;
+        const uint32_t q = flip_bytes(*reinterpret_cast<const uint16_t*>(row + 2 * lane));
+        r.v[0] = byte_f32<0>(q);
+        r.v[1] = byte_f32<1>(q);
     }
     return r;
 }

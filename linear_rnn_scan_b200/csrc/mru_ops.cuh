@@ -225,6 +225,16 @@ __device__ __forceinline__ int pack8_q(float x, float inv)
     return __float_as_int(__fadd_rn(__fmul_rn(x, inv), 12582912.0f)) & 0xff;
 }
 
+// The four signed bytes of a word as floats: with the sign bit flipped a byte
+// is q + 128, which the mantissa of 2^23 holds (the conversion instruction
+// runs at a quarter of an addition's rate).
+template <int K>
+__device__ __forceinline__ float byte_f32(uint32_t flipped)
+{
+    return __uint_as_float(__byte_perm(flipped, 0x4b000000u, 0x7440 + K)) - 8388736.0f;
+}
+__device__ __forceinline__ uint32_t flip_bytes(uint32_t w) { return w ^ 0x80808080u; }
+
 // max of magnitudes as bit patterns, in which NaN stays above everything.
 __device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
