@@ -435,28 +435,26 @@ __device__ __forceinline__ void copy_tile(const CUtensorMap* map, int d0, int t,
 }
 
 // A warp's tokens of an input whose rows start anywhere, into its rows of a
-// stage: the aligned words that hold a row (one that ends behind the last row
-// only as far as that goes).
+// stage: the aligned 16-byte pieces that hold a row (one that ends behind the
+// last row only as far as that goes), the pieces of its 8 rows one to a lane.
 template <typename V, int CH, int PITCH>
 __device__ __forceinline__ void copy_rows(const V* base, int64_t ld, const V* end, const Tile& t, int w, int lane,
                                           unsigned char* to)
 {
+    constexpr int kPieces = PITCH / 16;
+    const uintptr_t row0 = reinterpret_cast<uintptr_t>(base + (t.row + w * kStep) * ld + t.d0);
+    const int64_t pitch = ld * (int64_t)sizeof(V);
+    const int bytes = t.channels * (int)sizeof(V), rows = min(t.tokens - w * kStep, kStep);
+    to += w * kStep * PITCH;
 #pragma unroll
-    for (int s = 0; s < kStep; ++s) {
-        const int r = w * kStep + s;
-        if (r >= t.tokens) break;
-        const V* from = base + (t.row + r) * ld + t.d0;
-        const uintptr_t first = reinterpret_cast<uintptr_t>(from) & ~(uintptr_t)3;
-        const int words = (int)((reinterpret_cast<uintptr_t>(from + t.channels) - first + 3) / 4);
-#pragma unroll
-        for (int k = 0; k < (CH * (int)sizeof(V) / 4 + 32) / 32; ++k) {
-            const int i = lane + 32 * k;
-            if (i >= words) continue;
-            const uintptr_t at = first + 4 * (uintptr_t)i, left = reinterpret_cast<uintptr_t>(end) - at;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(shared_address(to + r * PITCH + 4 * i)), "l"(at),
-                         "r"(left < 4 ? (int)left : 4)
-                         : "memory");
-        }
+    for (int k = 0; k < (kStep * kPieces + 31) / 32; ++k) {
+        const int i = lane + 32 * k, r = i / kPieces, c = i - r * kPieces;
+        const uintptr_t row = row0 + (uintptr_t)(r * pitch), at = (row & ~(uintptr_t)15) + 16 * c;
+        if (r >= rows || at >= row + bytes) continue;
+        const uintptr_t left = reinterpret_cast<uintptr_t>(end) - at;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(shared_address(to + r * PITCH + 16 * c)), "l"(at),
+                     "r"(left < 16 ? (int)left : 16)
+                     : "memory");
     }
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -468,21 +466,21 @@ __device__ __forceinline__ void copies_wait()
 }
 
 // Where an input's rows lie in a stage: pitch, and (not VEC) how far a row
-// starts behind its first word.
+// starts behind its 16 bytes.
 template <typename V, int CH, bool VEC>
 struct Rows {
     static constexpr int kPitch = CH * (int)sizeof(V) + (VEC ? 0 : 16);
     const unsigned char* base;
-    unsigned off, step;                  // of the tile's first row, and of a row to the next, modulo 4
+    unsigned off, step;                  // of the tile's first row, and of a row to the next, modulo 16
     Rows() = default;
     __device__ __forceinline__ Rows(const unsigned char* b, const void* from, int64_t ld, const Tile& t) : base(b)
     {
-        off = VEC ? 0 : (unsigned)(reinterpret_cast<uintptr_t>((const V*)from + t.row * ld + t.d0) & 3);
-        step = VEC ? 0 : (unsigned)((ld * (int64_t)sizeof(V)) & 3);
+        off = VEC ? 0 : (unsigned)(reinterpret_cast<uintptr_t>((const V*)from + t.row * ld + t.d0) & 15);
+        step = VEC ? 0 : (unsigned)((ld * (int64_t)sizeof(V)) & 15);
     }
     __device__ __forceinline__ const V* row(int r) const
     {
-        return reinterpret_cast<const V*>(base + r * kPitch + (VEC ? 0 : (off + r * step) & 3));
+        return reinterpret_cast<const V*>(base + r * kPitch + (VEC ? 0 : (off + r * step) & 15));
     }
 };
 
