@@ -41,7 +41,9 @@ __device__ __forceinline__ void load_token(const Args& g, int64_t row, int64_t d
 }
 
 // What a token's gradient d is multiplied with: dx = cx d, df = cf d, di = ci d
-// and, for lam, q d.  a: the decay, p = h_{t-1}.
+// and, for lam, q d.  a: the decay, p = h_{t-1}.  The lru gate takes exp(-f) and
+// exp(-i) (of the logits as clamped) in place of f and i, so that they need not
+// be found twice.
 template <int GATE, bool NEAR = false>
 __device__ __forceinline__ void gradient_factors(float x, float f, float i, float csp, float p, float& a, float& b,
                                                  float& cx, float& cf, float& ci, float& q)
@@ -57,9 +59,8 @@ __device__ __forceinline__ void gradient_factors(float x, float f, float i, floa
         b = cx * x;
         cf = a * cx * (p - x);
     } else {
-        float sf, nf, si, ni, m;
-        sigmoid2(f, sf, nf);
-        sigmoid2(i, si, ni);
+        const float sf = rcp(1.0f + f), si = rcp(1.0f + i);
+        float m;
         const float la = -csp * sf;
         exp_expm1_neg<NEAR>(la, a, m);
         const float v = -m * (1.0f + a);                   // 1 - a^2
@@ -67,11 +68,12 @@ __device__ __forceinline__ void gradient_factors(float x, float f, float i, floa
         const float sx = si * x, u = v * r;
         cx = u * si;
         b = u * sx;
-        ci = b * ni;
+        ci = b * (i * si);
         q = la * a * (p - sx * a * r);
-        cf = q * nf;
+        cf = q * (f * sf);
     }
 }
+__device__ __forceinline__ float exp_neg(float v) { return ex2(-kLog2e * logit(v)); }
 
 constexpr int kShort = 8;                // tokens up to which a thread takes a channel alone
 
@@ -122,6 +124,7 @@ __global__ void __launch_bounds__(128) k_gated_short_bwd(Args g)
         float x, f, i, u;
         load_token<T, GATE, PACKED>(g, row, d, x, f, i);
         if (reset) h = 0.0f;
+        if (GATE == MRU_GATE_LRU) { f = exp_neg(f); i = exp_neg(i); }
         gradient_factors<GATE>(x, f, i, csp, h, a[t], u, cx[t], cf[t], ci[t], q[t]);
         h = carry_in(a[t], h) + u;
         if (reset) a[t] = 0.0f;
@@ -544,11 +547,12 @@ __device__ __forceinline__ Vec<C> input_row(const R& in, const float* scale, int
     return v;
 }
 
-// The map of a warp's tokens; a and, for the sigmoid gate, cx = 1 - a stay.
+// The map of a warp's tokens.  What the factors need of the gates again stays:
+// a, and in cx 1 - a (sigmoid) or in cf and ci exp(-f) and exp(-i) (lru).
 template <int C, bool VEC, int GATE, bool PACKED, bool SPECIAL, bool NEAR, typename R>
 __device__ __forceinline__ Map<C> back_map(const R (&in)[inputs_of(GATE)], const float (&scale)[3][kTok], int w, int lane,
                                            const Vec<C>& csp, int n, uint32_t resets, Vec<C> (&a)[kStep],
-                                           Vec<C> (&cx)[kStep])
+                                           Vec<C> (&cx)[kStep], Vec<C> (&cf)[kStep], Vec<C> (&ci)[kStep])
 {
     Map<C> m = Map<C>::of(1.0f);
 #pragma unroll
@@ -556,7 +560,7 @@ __device__ __forceinline__ Map<C> back_map(const R (&in)[inputs_of(GATE)], const
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             a[s].v[c] = 1.0f;
-            cx[s].v[c] = 0.0f;
+            cx[s].v[c] = cf[s].v[c] = ci[s].v[c] = 0.0f;
         }
         if (SPECIAL && s >= n) continue;
         const int row = w * kStep + s;
@@ -571,6 +575,12 @@ __device__ __forceinline__ Map<C> back_map(const R (&in)[inputs_of(GATE)], const
             if (GATE == MRU_GATE_SIGMOID) {
                 sigmoid2(f.v[c], a[s].v[c], cx[s].v[c]);
                 b = cx[s].v[c] * x.v[c];
+            } else if (GATE == MRU_GATE_LRU) {
+                cf[s].v[c] = exp_neg(f.v[c]);
+                ci[s].v[c] = exp_neg(i.v[c]);
+                float d;                                   // a - 1
+                exp_expm1_neg<NEAR>(-csp.v[c] * rcp(1.0f + cf[s].v[c]), a[s].v[c], d);
+                b = root(-d * (1.0f + a[s].v[c])) * rcp(1.0f + ci[s].v[c]) * x.v[c];
             } else {
                 gates<GATE, NEAR>(x.v[c], f.v[c], i.v[c], csp.v[c], a[s].v[c], b);
             }
@@ -594,15 +604,10 @@ __device__ __forceinline__ Map<C> back_factors(const R (&in)[inputs_of(GATE)], c
     Vec<C> q[kStep];
 #pragma unroll
     for (int s = 0; s < kStep; ++s) {
-        cf[s] = ci[s] = q[s] = Vec<C>{};
+        q[s] = Vec<C>{};
         if (SPECIAL && s >= n) continue;
         const int row = w * kStep + s;
         const Vec<C> x = input_row<C, VEC, PACKED>(in[0], scale[0], row, lane);
-        Vec<C> f = x, i = x;
-        if constexpr (GATE == MRU_GATE_LRU) {
-            f = input_row<C, VEC, PACKED>(in[1], scale[1], row, lane);
-            i = input_row<C, VEC, PACKED>(in[2], scale[2], row, lane);
-        }
         const bool reset = SPECIAL && (resets >> s & 1);
         if (reset) h = Vec<C>{};
 #pragma unroll
@@ -617,7 +622,7 @@ __device__ __forceinline__ Map<C> back_factors(const R (&in)[inputs_of(GATE)], c
                 cf[s].v[c] = a[s].v[c] * cx[s].v[c] * (h.v[c] - x.v[c]);
                 h.v[c] = fmaf(a[s].v[c], h.v[c], b);
             } else {
-                gradient_factors<GATE, NEAR>(x.v[c], f.v[c], i.v[c], csp.v[c], h.v[c], a[s].v[c], b, cx[s].v[c],
+                gradient_factors<GATE, NEAR>(x.v[c], cf[s].v[c], ci[s].v[c], csp.v[c], h.v[c], a[s].v[c], b, cx[s].v[c],
                                              cf[s].v[c], ci[s].v[c], q[s].v[c]);
                 h.v[c] = fmaf(a[s].v[c], h.v[c], b);
             }
@@ -728,9 +733,9 @@ __device__ __forceinline__ void backward_compute(const Args& g, BackMem<C>& mem,
         Vec<C> a[kStep], cx[kStep], cf[kStep], ci[kStep], dl0, dl1;
         Map<C> own;
         const float (&scale)[3][kTok] = mem.scale[st];
-        if (special) own = back_map<C, VEC, GATE, PACKED, true, false>(in, scale, w, lane, csp, n, resets, a, cx);
-        else if (near) own = back_map<C, VEC, GATE, PACKED, false, lru>(in, scale, w, lane, csp, n, resets, a, cx);
-        else own = back_map<C, VEC, GATE, PACKED, false, false>(in, scale, w, lane, csp, n, resets, a, cx);
+        if (special) own = back_map<C, VEC, GATE, PACKED, true, false>(in, scale, w, lane, csp, n, resets, a, cx, cf, ci);
+        else if (near) own = back_map<C, VEC, GATE, PACKED, false, lru>(in, scale, w, lane, csp, n, resets, a, cx, cf, ci);
+        else own = back_map<C, VEC, GATE, PACKED, false, false>(in, scale, w, lane, csp, n, resets, a, cx, cf, ci);
         put_map<C, VEC>(mem.map[w], lane, own);
         meet_arrive<kMaps>();
         meet<kStates>();
@@ -893,6 +898,7 @@ __global__ void __launch_bounds__(128) k_gated_edge(Args g)
         const float p = g.reset && g.reset[row] ? 0.0f : g.edge_h[at], dt = g.edge_d[at];
         float x, f, i, a, u, cx, cf, ci;
         load_token<T, GATE, true>(g, row, d, x, f, i);
+        if (GATE == MRU_GATE_LRU) { f = exp_neg(f); i = exp_neg(i); }
         gradient_factors<GATE>(x, f, i, csp, p, a, u, cx, cf, ci, q);
         ((T*)g.df)[row * g.ldg + d] = from_f32<T>(cf * dt);
         q *= dt;
