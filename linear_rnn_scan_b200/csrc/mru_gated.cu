@@ -238,20 +238,21 @@ __device__ __forceinline__ bool all_near(const Vec<C>& csp)
 // 8-bit copies of a warp's tokens.  A run of 64 channels is a warp's row; the
 // largest magnitudes of all runs (input, token) are found first and a lane
 // takes the factors of one of them for all.
-template <typename T, int C, bool VEC, int NIN>
+// PLAIN: all of the tile's tokens and channels are there, and pairs of bytes
+// can be written.
+template <typename T, int C, bool VEC, int NIN, bool PLAIN>
 __device__ __forceinline__ void pack_rows(const Args& g, const Tile& t, int w, int lane,
-                                          const Rows<T, 32 * C, VEC> (&in)[NIN], bool wide8)
+                                          const Rows<T, 32 * C, VEC> (&in)[NIN])
 {
     static_assert(C == 2, "a row is one run of 64 channels");
     static_assert(NIN * kStep <= 32, "a lane to a run");
-    const bool part = t.channels < 64;                       // what lies behind the last channel does not count
     uint32_t mine = 0;
 #pragma unroll
     for (int n = 0; n < NIN; ++n)
 #pragma unroll
         for (int s = 0; s < kStep; ++s) {
             Vec<C> v = read_row<C, VEC>(in[n].row(w * kStep + s), lane);
-            if (part) {
+            if (!PLAIN) {                                    // what lies behind the last channel does not count
                 if (channel<C, VEC>(lane, 0) >= t.channels) v.v[0] = 0.0f;
                 if (channel<C, VEC>(lane, 1) >= t.channels) v.v[1] = 0.0f;
             }
@@ -266,19 +267,18 @@ __device__ __forceinline__ void pack_rows(const Args& g, const Tile& t, int w, i
         float* to = lane < kStep ? g.x8.scale : lane < 2 * kStep ? g.f8.scale : g.i8.scale;
         to[(row0 + lane % kStep) * runs + t.d0 / 64] = scale;
     }
-    const bool in_row = 2 * lane < t.channels;
 #pragma unroll
     for (int n = 0; n < NIN; ++n) {
         int8_t* at = (n == 0 ? g.x8.q : n == 1 ? g.f8.q : g.i8.q) + row0 * g.D + t.d0;
+        if (PLAIN) at += 2 * lane;
 #pragma unroll
         for (int s = 0; s < kStep; ++s, at += g.D) {
             const float k = __shfl_sync(~0u, inv, n * kStep + s);
             const Vec<C> v = read_row<C, VEC>(in[n].row(w * kStep + s), lane);
-            const uint32_t q0 = (uint32_t)pack8_q(v.v[0], k), q1 = (uint32_t)pack8_q(v.v[1], k);
-            if (s >= left) continue;
-            if (VEC && wide8) {
-                if (in_row) *reinterpret_cast<uint16_t*>(at + 2 * lane) = (uint16_t)__byte_perm(q0, q1, 0x0040);
-            } else {
+            const uint32_t q0 = (uint32_t)pack8_bits(v.v[0], k), q1 = (uint32_t)pack8_bits(v.v[1], k);
+            if (PLAIN) {
+                *reinterpret_cast<uint16_t*>(at) = (uint16_t)__byte_perm(q0, q1, 0x0040);
+            } else if (s < left) {
                 if (channel<C, VEC>(lane, 0) < t.channels) at[channel<C, VEC>(lane, 0)] = (int8_t)q0;
                 if (channel<C, VEC>(lane, 1) < t.channels) at[channel<C, VEC>(lane, 1)] = (int8_t)q1;
             }
@@ -412,7 +412,10 @@ __device__ __forceinline__ void forward_compute(const Args& g, TileMem<C>& mem, 
         in[0] = Rows<T, CH, VEC>(stage, g.x, g.ld, t);
         in[1] = Rows<T, CH, VEC>(stage + kTok * Rows<T, CH, VEC>::kPitch, g.f, g.ld, t);
         if constexpr (NIN == 3) in[2] = Rows<T, CH, VEC>(stage + 2 * kTok * Rows<T, CH, VEC>::kPitch, g.i, g.ld, t);
-        if constexpr (PACK) pack_rows<T, C, VEC, NIN>(g, t, w, lane, in, wide8);
+        if constexpr (PACK) {
+            if (VEC && wide8 && left >= kStep && channels == CH) pack_rows<T, C, VEC, NIN, true>(g, t, w, lane, in);
+            else pack_rows<T, C, VEC, NIN, false>(g, t, w, lane, in);
+        }
         Vec<C> csp = {};
         if (GATE == MRU_GATE_LRU) csp = read_row<C, VEC>(&mem.csp[st][0], lane);
         const bool special = n < kStep || resets;

@@ -220,10 +220,11 @@ __device__ __forceinline__ void pack8_factors(float amax, float& inv, float& sca
 }
 // The integer of x * inv (at most 127 in size), ties to even: next to 1.5 * 2^23
 // floats are whole numbers, and the low byte of the sum's bits is the integer's.
-__device__ __forceinline__ int pack8_q(float x, float inv)
+__device__ __forceinline__ int pack8_bits(float x, float inv)
 {
-    return __float_as_int(__fadd_rn(__fmul_rn(x, inv), 12582912.0f)) & 0xff;
+    return __float_as_int(__fadd_rn(__fmul_rn(x, inv), 12582912.0f));
 }
+__device__ __forceinline__ int pack8_q(float x, float inv) { return pack8_bits(x, inv) & 0xff; }
 
 // The four signed bytes of a word as floats: with the sign bit flipped a byte
 // is q + 128, which the mantissa of 2^23 holds (the conversion instruction
