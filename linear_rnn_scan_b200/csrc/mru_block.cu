@@ -1092,14 +1092,14 @@ mru_status mru_block_norm(const mru_block_problem* p, const mru_block_params* pr
 size_t mru_block_backward_workspace_size(const mru_block_problem* p)
 {
     if (check_problem(p) != MRU_OK) return 0;
-    if (p->rows == 0 || p->D == 0) return 256;
+    if (p->rows == 0 || p->D == 0) return 256;                       // never 0: that is an invalid problem
     // the larger of the two column layouts
     size_t parts = 0;
     for (bool vec : {false, true}) {
         const size_t n = (size_t)most_parts(shape_of(p->rows, p->D, vec));
         if (n > parts) parts = n;
     }
-    return 256 + align256(5 * parts * (size_t)p->D * 4);
+    return align256(5 * parts * (size_t)p->D * 4);
 }
 
 mru_status mru_block_norm_backward(const mru_block_problem* p, const mru_block_params* prm, const void* r_out,
@@ -1122,7 +1122,7 @@ mru_status mru_block_norm_backward(const mru_block_problem* p, const mru_block_p
         if (!aligned(v, 4)) return MRU_ERR_INVALID_ARG;
     if (!any) {
         if (ws_bytes < mru_block_backward_workspace_size(p)) return MRU_ERR_WORKSPACE;
-        cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(uint32_t), s);
+        cudaError_t e = cudaSuccess;
         for (float* v : {gr.dw_y, gr.db_y, gr.ds, gr.dw_z, gr.db_z})
             if (e == cudaSuccess && v && D > 0) e = cudaMemsetAsync(v, 0, D * 4, s);
         return cuda_status(e);
@@ -1172,11 +1172,10 @@ mru_status mru_block_norm_backward(const mru_block_problem* p, const mru_block_p
     if (saved) { a.r8 = saved->r; a.y8 = saved->y; a.g8 = saved->g; }
     a.dro = dr_out; a.dz = dz; a.dr = dr; a.dy = dy; a.dg = dg;
     a.has_y = has_y; a.has_z = has_z;
-    a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + 256);
+    a.part = reinterpret_cast<float*>(ws);
     const Shape sh = shape_of(p->rows, p->D, vec);
     a.cluster = sh.cluster;
-    cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(uint32_t), s);
-    if (e != cudaSuccess) return MRU_ERR_CUDA;
+    cudaError_t e;
     const bool full = p->norm == MRU_NORM_LAYER || gr.db_y || gr.db_z, packed = saved != nullptr;
     if (p->dtype == MRU_BF16)
         e = packed ? (full ? run_backward<__nv_bfloat16, true, true>(sh, a, vec, s)

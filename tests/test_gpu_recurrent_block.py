@@ -393,6 +393,63 @@ def test_recurrence_bounded_waits(backward):
     assert t.equal(gr.dx, want[3].dx) and t.equal(gr.df, want[3].df) and t.equal(gr.dh0, want[3].dh0)
 
 
+@pytest.mark.parametrize("D", [64, 200, 199])
+def test_recurrence_two_streams_at_once(D):
+    """Calls that run side by side, each with its own workspace, give what they
+    give alone."""
+    t = torch()
+    cases = []
+    for seed in (61, 62):
+        v, g = make_gated("sigmoid", "f32", 2, 3000, D, seed=seed)
+        cases.append((v, g, run_gated_backward("sigmoid", "f32", v, g)))
+    p = mru.gated_problem(2, 3000, D, gate="sigmoid", x_dtype="f32")
+    dev = [{k: _dev(u) for k, u in {**v, **g}.items()} for v, g, _ in cases]
+    streams = [t.cuda.Stream() for _ in cases]
+    t.cuda.synchronize()
+    for _ in range(10):
+        outs = []
+        for d, st in zip(dev, streams):
+            rest = {k: d[k] for k in ("reset", "lens")}
+            y, h, saved = mru.gated_scan_t(p, d["x"], d["f"], h0=d["h0"], save="full", stream=st, **rest)
+            gr = mru.gated_scan_backward_t(p, d["dy"], saved, x=d["x"], f=d["f"], dh_last=d["dh_last"], stream=st, **rest)
+            outs.append((y, h, saved.states, gr.dx, gr.df, gr.dh0))
+        t.cuda.synchronize()
+        for got, (_, _, want) in zip(outs, cases):
+            for a, b in zip(got, (want[0], want[1], want[2].states, want[3].dx, want[3].df, want[3].dh0)):
+                assert t.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: with decays of zero the recurrence returns its
+    input and its gradient; a row's norm, gate and 8-bit copy are the same at
+    the far end as in a small call."""
+    t = torch()
+    L, D = 131200, 16384
+    assert L * D > 2 ** 31
+    x = t.empty(1, L, D, dtype=t.bfloat16, device="cuda").normal_()
+    f = t.zeros_like(x)
+    p = mru.gated_problem(1, L, D, gate="decay")
+    y, h_last, saved = mru.gated_scan_t(p, x, f, save="full")
+    assert t.equal(y, x) and t.equal(h_last, x[:, -1].float()) and t.equal(saved.states[:, 1:], x[:, 63:-1:64].float())
+    gr = mru.gated_scan_backward_t(p, x, saved, x=x, f=f)
+    assert t.equal(gr.dx, x) and t.equal(gr.df[:, 1:], x[:, 1:] * x[:, :-1]) and (gr.df[:, 0] == 0).all()
+    del gr, saved, f
+    rows, far = x.view(L, D), slice(L - 40, L)
+    b, few = mru.block_problem(L, D), mru.block_problem(40, D)
+    gates = y.view(L, D)
+    out, z, _ = mru.block_norm_t(b, rows, y=rows, g=gates)
+    o, n, _ = mru.block_norm_t(few, rows[far], y=rows[far], g=gates[far])
+    assert t.equal(out[far], o) and t.equal(z[far], n)
+    a = mru.block_norm_backward_t(b, r_out=out, y=rows, g=gates, dr_out=rows, dz=z)
+    c = mru.block_norm_backward_t(few, r_out=o, y=rows[far], g=gates[far], dr_out=rows[far], dz=n)
+    assert t.equal(a.dr[far], c.dr) and t.equal(a.dy[far], c.dy) and t.equal(a.dg[far], c.dg)
+    del a, out, z
+    q, s = mru.pack8_t(rows)
+    q1, s1 = mru.pack8_t(rows[far])
+    assert t.equal(q[far], q1) and t.equal(s[far], s1)
+    assert t.equal(mru.unpack8_t(q, s, dtype=t.bfloat16)[far], mru.unpack8_t(q1, s1, dtype=t.bfloat16))
+
+
 # ------------------------------------------------------------------ block ---
 
 def make_block(norm, act, dtype, rows, D, seed):
