@@ -43,18 +43,20 @@ struct BArgs {
 // How a thread's columns lie: in pieces of 16 bytes of the rows' type (U = 8 or
 // 4 columns), a team's pieces side by side (kWide; kExact: every one of them
 // is there and the CTA has 128 threads, so that offsets are constants), or one
-// by one (kSingle).  NV eights of columns to a thread; D counts as 0 for rows
+// by one (kSingle: a warp or 128 threads to a row).  NV eights of columns to a thread; D counts as 0 for rows
 // past the end.
 enum Lay { kSingle, kWide, kExact };
 template <Lay LAY>
-__device__ __forceinline__ unsigned threads() { return LAY == kExact ? 128u : blockDim.x; }
-template <typename T, int NV, Lay LAY>
+__device__ __forceinline__ unsigned threads() { return LAY == kWide ? blockDim.x : 128u; }
+template <typename T, int NV, Lay LAY, int TEAM>
 struct Cols {
     static constexpr int U = LAY ? 16 / (int)sizeof(T) : 1, N = 8 / U;     // columns of a piece, pieces of an eight
+    static constexpr int kTeam = TEAM ? TEAM : 128;                        // kSingle: threads of a row
     int c0, gap, D;
-    __device__ __forceinline__ int step() const { return LAY == kExact ? 128 : gap; }
+    __device__ __forceinline__ int step() const { return LAY == kExact ? 128 : LAY == kSingle ? kTeam : gap; }
     __device__ __forceinline__ int at(int e) const { return c0 + e / U * (U * step()) + e % U; }
     __device__ __forceinline__ bool ok(int e) const { return LAY == kExact || at(e) < D; }
+    __device__ __forceinline__ static int lane() { return threadIdx.x % kTeam; }
 };
 
 // A piece of a row.
@@ -88,8 +90,8 @@ __device__ __forceinline__ void store_piece(__nv_bfloat16* p, const F2* v)
 }
 
 // The k-th eight of a thread's columns to a row in memory, and of a parameter.
-template <typename T, int NV, Lay LAY>
-__device__ __forceinline__ void store_eight(T* row, const Cols<T, NV, LAY>& c, int k, const F2 (&v)[4])
+template <typename T, int NV, Lay LAY, int TEAM>
+__device__ __forceinline__ void store_eight(T* row, const Cols<T, NV, LAY, TEAM>& c, int k, const F2 (&v)[4])
 {
     if constexpr (LAY != kSingle) {
 #pragma unroll
@@ -103,13 +105,17 @@ __device__ __forceinline__ void store_eight(T* row, const Cols<T, NV, LAY>& c, i
         }
     }
 }
-template <typename T, int NV, Lay LAY>
-__device__ __forceinline__ void load_param(const float* p, float none, const Cols<T, NV, LAY>& c, int k, F2 (&v)[4])
+template <typename T, int NV, Lay LAY, int TEAM>
+__device__ __forceinline__ void load_param(const float* p, float none, const Cols<T, NV, LAY, TEAM>& c, int k, F2 (&v)[4])
 {
+    if constexpr (LAY == kSingle) {                          // p: the block's copy in shared memory
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = both(none);
-    if (!p) return;
-    if constexpr (LAY != kSingle) {
+        for (int j = 0; j < 4; ++j)
+            v[j] = F2{p[c.lane() + (8 * k + 2 * j) * c.step()], p[c.lane() + (8 * k + 2 * j + 1) * c.step()]};
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = both(none);
+        if (!p) return;
 #pragma unroll
         for (int i = 0; i < c.N; ++i)
             if (c.ok(8 * k + i * c.U)) {
@@ -117,16 +123,24 @@ __device__ __forceinline__ void load_param(const float* p, float none, const Col
                 for (int h = 0; h < c.U / 4; ++h)
                     load_piece(p + (unsigned)(c.at(8 * k + i * c.U) + 4 * h), v + (i * c.U + 4 * h) / 2);
             }
-    } else {
-        // without a branch to a load: a column that is not there reads the last one
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v[j] = F2{p[min(c.at(8 * k + 2 * j), c.D - 1)], p[min(c.at(8 * k + 2 * j + 1), c.D - 1)]};
     }
 }
+// kSingle: the parameters of a CTA's columns in shared memory, `cols` to each,
+// so that a thread reads its own at constant distances.
+__device__ __forceinline__ mru_block_params keep_params(const mru_block_params& prm, float* to, int first, int cols, int D)
+{
+    auto one = [&](const float* from, float none, float* put) {
+        for (int k = threadIdx.x; k < cols; k += blockDim.x) put[k] = from && first + k < D ? from[first + k] : none;
+        return put;
+    };
+    const mru_block_params r = {one(prm.w_y, 1.0f, to), one(prm.b_y, 0.0f, to + cols), one(prm.s, 1.0f, to + 2 * cols),
+                                one(prm.w_z, 1.0f, to + 3 * cols), one(prm.b_z, 0.0f, to + 4 * cols)};
+    __syncthreads();
+    return r;
+}
 // Columns that are not there become zero.
-template <typename T, int NV, Lay LAY>
-__device__ __forceinline__ void mask(const Cols<T, NV, LAY>& c, int k, F2 (&v)[4])
+template <typename T, int NV, Lay LAY, int TEAM>
+__device__ __forceinline__ void mask(const Cols<T, NV, LAY, TEAM>& c, int k, F2 (&v)[4])
 {
     if constexpr (LAY == kWide) {
 #pragma unroll
@@ -158,8 +172,8 @@ __device__ __forceinline__ void in_turn() { asm volatile("" ::: "memory"); }
 // Writes a row's 8-bit copy.  A run of 64 channels is a piece of 64 / U lanes
 // in a row, or (TEAM 8 with pieces of 4) both pieces of its 8 lanes.  The
 // pitch is `D`; columns that are not there are zero in v and not written.
-template <int TEAM, typename T, int NV, Lay LAY>
-__device__ __forceinline__ void store_packed(const mru_packed8& h, int64_t row, int D, const Cols<T, NV, LAY>& c, int k,
+template <typename T, int NV, Lay LAY, int TEAM>
+__device__ __forceinline__ void store_packed(const mru_packed8& h, int64_t row, int D, const Cols<T, NV, LAY, TEAM>& c, int k,
                                              const F2 (&v)[4])
 {
     constexpr int U = c.U, N = c.N;
@@ -238,7 +252,7 @@ __host__ __device__ constexpr int stages_of(int plain, int held)
 
 // One input of the rows.  V: its type in memory; T: the type whose pieces the
 // columns lie in.
-template <typename V, typename T, int NV, Lay LAY>
+template <typename V, typename T, int NV, Lay LAY, int TEAM>
 struct Feed {
     const V* next;                         // of the row to copy next, at the thread's (kSingle: the CTA's) first column
     const V* now;                          // of the row to read next
@@ -249,7 +263,7 @@ struct Feed {
           end(reinterpret_cast<uintptr_t>((const V*)base + (rows - 1) * ld + D))
     {
     }
-    __device__ __forceinline__ void copy(unsigned stage, const Cols<T, NV, LAY>& c, int cols)
+    __device__ __forceinline__ void copy(unsigned stage, const Cols<T, NV, LAY, TEAM>& c, int cols)
     {
         constexpr int U = c.U, BYTES = U * (int)sizeof(V);
         if constexpr (LAY != kSingle) {
@@ -260,7 +274,7 @@ struct Feed {
             const uintptr_t first = reinterpret_cast<uintptr_t>(next) & ~(uintptr_t)15;
             const uintptr_t last = reinterpret_cast<uintptr_t>(next + cols);
             const int pieces = cols > 0 ? (int)((last - first + 15) / 16) : 0;
-            for (int k = threadIdx.x; k < pieces; k += blockDim.x) {
+            for (int k = c.lane(); k < pieces; k += c.kTeam) {
                 const uintptr_t from = first + 16 * (uintptr_t)k;
                 copy_async<16>(stage + 16 * k, (const void*)from, end - from < 16 ? (int)(end - from) : 16);
             }
@@ -268,14 +282,14 @@ struct Feed {
         next += jump;
     }
     // kSingle: the thread's e-th column of the row to read.
-    __device__ __forceinline__ float one(const unsigned char* stage, const Cols<T, NV, LAY>& c, int e) const
+    __device__ __forceinline__ float one(const unsigned char* stage, const Cols<T, NV, LAY, TEAM>& c, int e) const
     {
         const V* row = reinterpret_cast<const V*>(stage + (reinterpret_cast<uintptr_t>(now) & 15));
-        if constexpr (sizeof(V) == 1) return (float)row[threadIdx.x + e * c.step()];
-        else return to_f32(row[threadIdx.x + e * c.step()]);
+        if constexpr (sizeof(V) == 1) return (float)row[c.lane() + e * c.step()];
+        else return to_f32(row[c.lane() + e * c.step()]);
     }
     // The thread's k-th eight columns of the row to read.
-    __device__ __forceinline__ void read(const unsigned char* stage, const Cols<T, NV, LAY>& c, int k, F2 (&v)[4]) const
+    __device__ __forceinline__ void read(const unsigned char* stage, const Cols<T, NV, LAY, TEAM>& c, int k, F2 (&v)[4]) const
     {
         if constexpr (LAY == kSingle) {
 #pragma unroll
@@ -297,16 +311,16 @@ struct Feed {
 };
 
 // The same for values held in 8 bits.
-template <typename T, int NV, Lay LAY>
+template <typename T, int NV, Lay LAY, int TEAM>
 struct HeldFeed {
-    Feed<int8_t, T, NV, LAY> q;
+    Feed<int8_t, T, NV, LAY, TEAM> q;
     const float *next, *now;               // scales of the rows
     int64_t jump;
     __device__ __forceinline__ HeldFeed(const mru_packed8& h, int64_t row, int64_t step, int64_t rows, int D, int c0)
         : q(h.q, row, step, D, rows, D, c0), next(h.scale + row * ((D + 63) / 64)), now(next), jump(step * ((D + 63) / 64))
     {
     }
-    __device__ __forceinline__ void copy(unsigned stage, const Cols<T, NV, LAY>& c, int cols)
+    __device__ __forceinline__ void copy(unsigned stage, const Cols<T, NV, LAY, TEAM>& c, int cols)
     {
         q.copy(stage, c, cols);
         if constexpr (LAY != kSingle) {
@@ -318,7 +332,7 @@ struct HeldFeed {
             next += jump;
         }
     }
-    __device__ __forceinline__ void read(const unsigned char* stage, const Cols<T, NV, LAY>& c, int k, F2 (&v)[4]) const
+    __device__ __forceinline__ void read(const unsigned char* stage, const Cols<T, NV, LAY, TEAM>& c, int k, F2 (&v)[4]) const
     {
         if constexpr (LAY == kSingle) {
             auto one = [&](int e) { return q.one(stage, c, e) * now[min(c.at(e), c.D - 1) / 64]; };
@@ -468,8 +482,8 @@ __device__ __forceinline__ void activation(int act, F2 (&g)[N], F2 (&da)[N])
 }
 
 // v - mean (layer norm) and 1 / sqrt(mean square + eps) of a row.
-template <int TEAM, typename T, int NV, Lay LAY>
-__device__ __forceinline__ float normalise(const BArgs& p, const Cols<T, NV, LAY>& c, F2 (&v)[NV][4], ReduceMem& m, int& phase)
+template <typename T, int NV, Lay LAY, int TEAM>
+__device__ __forceinline__ float normalise(const BArgs& p, const Cols<T, NV, LAY, TEAM>& c, F2 (&v)[NV][4], ReduceMem& m, int& phase)
 {
     const float inv_d = 1.0f / (float)p.D;
     float s[1] = {0.0f};
@@ -495,9 +509,9 @@ __device__ __forceinline__ float normalise(const BArgs& p, const Cols<T, NV, LAY
 // The thread's place: team (row within the CTA's rows), columns, and the
 // first column and the number of columns of its CTA.
 template <int TEAM, typename T, int NV, Lay LAY>
-__device__ __forceinline__ Cols<T, NV, LAY> place(const BArgs& p, int64_t& row, int64_t& step, int& first, int& cols)
+__device__ __forceinline__ Cols<T, NV, LAY, TEAM> place(const BArgs& p, int64_t& row, int64_t& step, int& first, int& cols)
 {
-    Cols<T, NV, LAY> c;
+    Cols<T, NV, LAY, TEAM> c;
     c.D = p.D;
     if constexpr (TEAM > 0) {
         const int teams = blockDim.x / TEAM;
@@ -527,14 +541,19 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
     int phase = 0, first, cols;
     if (TEAM == 0) clear(mem, p.cluster);
     int64_t row, step;
-    const Cols<T, NV, LAY> c = place<TEAM, T, NV, LAY>(p, row, step, first, cols);
+    const Cols<T, NV, LAY, TEAM> c = place<TEAM, T, NV, LAY>(p, row, step, first, cols);
     // teams of a warp take their shuffles together: rows past the end go through the motions
     const int64_t last = TEAM ? (p.rows + step - 1) / step * step : p.rows;
     const bool gate = p.has_y && p.act != MRU_ACT_NONE;
-    const unsigned plane = NV * 8 * sizeof(T) * threads<LAY>() + (LAY ? 0 : kMargin), stage_size = 3 * plane;
-    const unsigned base = (unsigned)__cvta_generic_to_shared(ring);
+    const unsigned wide = LAY ? threads<LAY>() : (unsigned)c.kTeam, teams = LAY ? 1u : blockDim.x / c.kTeam;
+    const unsigned plane = NV * 8 * sizeof(T) * wide + (LAY ? 0 : kMargin), stage_size = 3 * plane * teams;
+    const unsigned mine = LAY ? 0u : threadIdx.x / c.kTeam * 3 * plane;    // kSingle: the row's part of a stage
+    const unsigned base = (unsigned)__cvta_generic_to_shared(ring) + mine;
+    mru_block_params prm = p.prm;
+    if constexpr (LAY == kSingle)
+        prm = keep_params(p.prm, reinterpret_cast<float*>(ring + STAGES * stage_size), first, c.kTeam * 8 * NV, p.D);
     const int start = LAY ? c.c0 : first;
-    Feed<T, T, NV, LAY> fr(p.r, row, step, p.D, p.rows, p.D, start), fy(p.y, row, step, p.ldy, p.rows, p.D, start),
+    Feed<T, T, NV, LAY, TEAM> fr(p.r, row, step, p.D, p.rows, p.D, start), fy(p.y, row, step, p.ldy, p.rows, p.D, start),
         fg(p.g, row, step, p.ldg, p.rows, p.D, start);
     int64_t coming = row;
     unsigned to = 0, from = 0;                             // stages to fill and to read next, in bytes
@@ -553,17 +572,18 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
     for (; row < last; row += step) {
         const bool live = row < p.rows;
         const int64_t rr = live ? row : 0, here = rr * p.D;
-        Cols<T, NV, LAY> cc = c;
+        Cols<T, NV, LAY, TEAM> cc = c;
         if (TEAM && !live) cc.D = 0;
         if constexpr (LAY == kSingle) {
             copy_wait<STAGES - 2>();
-            __syncthreads();                               // every thread's pieces; the last row's stage is free
+            if (TEAM) __syncwarp();
+            else __syncthreads();                          // every thread's pieces; the last row's stage is free
             fill();
         } else {
             fill();
             copy_wait<STAGES - 1>();
         }
-        const unsigned char* stage = ring + from;
+        const unsigned char* stage = ring + mine + from;
         from = from == (STAGES - 1) * stage_size ? 0 : from + stage_size;
         F2 r[NV][4], y[NV][4];
 #pragma unroll
@@ -572,21 +592,21 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 fy.read(stage + plane, cc, k, y[k]);
-                if constexpr (PACK && LAY != kSingle) store_packed<TEAM>(p.y8, rr, p.D, cc, k, y[k]);
+                if constexpr (PACK && LAY != kSingle) store_packed(p.y8, rr, p.D, cc, k, y[k]);
             }
-            const float rstd = normalise<TEAM>(p, cc, y, mem, phase);
+            const float rstd = normalise(p, cc, y, mem, phase);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 F2 w[4], b[4], g[4];
-                load_param(p.prm.w_y, 1.0f, cc, k, w);
-                load_param(p.prm.b_y, 0.0f, cc, k, b);
+                load_param(prm.w_y, 1.0f, cc, k, w);
+                load_param(prm.b_y, 0.0f, cc, k, b);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) y[k][j] = fma2(y[k][j] * both(rstd), w[j], b[j]);
                 if (gate) fg.read(stage + 2 * plane, cc, k, g);
                 if constexpr (PACK && LAY != kSingle) {
-                    if (gate) store_packed<TEAM>(p.g8, rr, p.D, cc, k, g);
+                    if (gate) store_packed(p.g8, rr, p.D, cc, k, g);
                 }
-                load_param(p.prm.s, 1.0f, cc, k, w);
+                load_param(prm.s, 1.0f, cc, k, w);
                 activation<false>(p.act, g, b);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) r[k][j] = fma2(w[j] * both(p.rs) * g[j], y[k][j], r[k][j]);
@@ -602,16 +622,16 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
             for (int k = 0; k < NV; ++k) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) y[k][j] = F2{to_f32(from_f32<T>(r[k][j].x)), to_f32(from_f32<T>(r[k][j].y))};
-                store_packed<TEAM>(p.r8, rr, p.D, cc, k, y[k]);
+                store_packed(p.r8, rr, p.D, cc, k, y[k]);
             }
         }
         if (p.has_z) {
-            const float rstd = normalise<TEAM>(p, cc, r, mem, phase);
+            const float rstd = normalise(p, cc, r, mem, phase);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 F2 w[4], b[4];
-                load_param(p.prm.w_z, 1.0f, cc, k, w);
-                load_param(p.prm.b_z, 0.0f, cc, k, b);
+                load_param(prm.w_z, 1.0f, cc, k, w);
+                load_param(prm.b_z, 0.0f, cc, k, b);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) r[k][j] = fma2(r[k][j] * both(rstd), w[j], b[j]);
                 store_eight((T*)p.z + here, cc, k, r[k]);
@@ -622,8 +642,8 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
 }
 
 // A CTA's (cluster's) sums over its rows of one parameter's gradient.
-template <int TEAM, typename T, int NV, Lay LAY>
-__device__ __forceinline__ void write_part(const BArgs& p, const Cols<T, NV, LAY>& c, int which, const F2 (&acc)[NV][4], float* sums)
+template <typename T, int NV, Lay LAY, int TEAM>
+__device__ __forceinline__ void write_part(const BArgs& p, const Cols<T, NV, LAY, TEAM>& c, int which, const F2 (&acc)[NV][4], float* sums)
 {
     float* to = p.part + ((int64_t)which * p.parts + blockIdx.x / p.cluster) * p.D;
     if constexpr (TEAM > 0) {
@@ -661,7 +681,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
     int phase = 0, first, cols;
     if (TEAM == 0) clear(mem, p.cluster);
     int64_t row, step;
-    const Cols<T, NV, LAY> c = place<TEAM, T, NV, LAY>(p, row, step, first, cols);
+    const Cols<T, NV, LAY, TEAM> c = place<TEAM, T, NV, LAY>(p, row, step, first, cols);
     const int64_t last = TEAM ? (p.rows + step - 1) / step * step : p.rows;
     const float inv_d = 1.0f / (float)p.D;
     const bool layer = FULL && p.norm == MRU_NORM_LAYER, gate = p.has_y && p.act != MRU_ACT_NONE;
@@ -674,13 +694,18 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             if (FULL) dby[k][j] = dbz[k][j] = both(0.0f);
         }
     // a stage: dr', dz, then r', y, g
-    const unsigned plane = NV * 8 * sizeof(T) * threads<LAY>() + (LAY ? 0 : kMargin);
-    const unsigned next = PACKED ? NV * (LAY ? held_bytes<T>() : 8) * threads<LAY>() + (LAY ? 0 : kMargin) : plane;
-    const unsigned stage_size = 2 * plane + 3 * next, at_r = 2 * plane, at_y = at_r + next, at_g = at_y + next;
-    const unsigned base = (unsigned)__cvta_generic_to_shared(ring);
+    const unsigned wide = LAY ? threads<LAY>() : (unsigned)c.kTeam, teams = LAY ? 1u : blockDim.x / c.kTeam;
+    const unsigned plane = NV * 8 * sizeof(T) * wide + (LAY ? 0 : kMargin);
+    const unsigned next = PACKED ? NV * (LAY ? held_bytes<T>() : 8) * wide + (LAY ? 0 : kMargin) : plane;
+    const unsigned stage_size = (2 * plane + 3 * next) * teams, at_r = 2 * plane, at_y = at_r + next, at_g = at_y + next;
+    const unsigned mine = LAY ? 0u : threadIdx.x / c.kTeam * (2 * plane + 3 * next);     // kSingle: the row's part
+    const unsigned base = (unsigned)__cvta_generic_to_shared(ring) + mine;
+    mru_block_params prm = p.prm;
+    if constexpr (LAY == kSingle)
+        prm = keep_params(p.prm, reinterpret_cast<float*>(ring + STAGES * stage_size), first, c.kTeam * 8 * NV, p.D);
     const int start = LAY ? c.c0 : first;
-    using In = typename std::conditional<PACKED, HeldFeed<T, NV, LAY>, Feed<T, T, NV, LAY>>::type;
-    Feed<T, T, NV, LAY> fdr(p.dro, row, step, p.D, p.rows, p.D, start), fdz(p.dz, row, step, p.D, p.rows, p.D, start);
+    using In = typename std::conditional<PACKED, HeldFeed<T, NV, LAY, TEAM>, Feed<T, T, NV, LAY, TEAM>>::type;
+    Feed<T, T, NV, LAY, TEAM> fdr(p.dro, row, step, p.D, p.rows, p.D, start), fdz(p.dz, row, step, p.D, p.rows, p.D, start);
     auto input = [&](const mru_packed8& h, const void* src, int64_t ld) {
         if constexpr (PACKED) return In(h, row, step, p.rows, p.D, start);
         else return In(src, row, step, ld, p.rows, p.D, start);
@@ -705,17 +730,18 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
     for (; row < last; row += step) {
         const bool live = row < p.rows;
         const int64_t rr = live ? row : 0, here = rr * p.D;
-        Cols<T, NV, LAY> cc = c;
+        Cols<T, NV, LAY, TEAM> cc = c;
         if (TEAM && !live) cc.D = 0;
         if constexpr (LAY == kSingle) {
             copy_wait<STAGES - 2>();
-            __syncthreads();                               // every thread's pieces; the last row's stage is free
+            if (TEAM) __syncwarp();
+            else __syncthreads();                          // every thread's pieces; the last row's stage is free
             fill();
         } else {
             fill();
             copy_wait<STAGES - 1>();
         }
-        const unsigned char* stage = ring + from;
+        const unsigned char* stage = ring + mine + from;
         from = from == (STAGES - 1) * stage_size ? 0 : from + stage_size;
         float mean_r = 0.0f, mean_y = 0.0f;
         if (layer) {
@@ -755,7 +781,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             if (p.has_z) {
                 fdz.read(stage + plane, cc, k, u);
                 centred(fr, at_r, mean_r, k, r);
-                load_param(p.prm.w_z, 1.0f, cc, k, w);
+                load_param(prm.w_z, 1.0f, cc, k, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) u[j] = u[j] * w[j];
                 s[0] += dot(r, r);
@@ -783,7 +809,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             if (p.has_z) {
                 centred(fr, at_r, mean_r, k, v);
                 fdz.read(stage + plane, cc, k, g);
-                load_param(p.prm.w_z, 1.0f, cc, k, w);
+                load_param(prm.w_z, 1.0f, cc, k, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     v[j] = v[j] * rstd;
@@ -798,8 +824,8 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             if (p.dr) store_eight((T*)p.dr + here, cc, k, e);
             if (!p.has_y) continue;
             centred(fy, at_y, mean_y, k, y[k]);
-            load_param(p.prm.w_y, 1.0f, cc, k, w);
-            load_param(p.prm.b_y, 0.0f, cc, k, n);
+            load_param(prm.w_y, 1.0f, cc, k, w);
+            load_param(prm.b_y, 0.0f, cc, k, n);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 y[k][j] = y[k][j] * both(rstd_y);
@@ -808,7 +834,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             if (gate) fg.read(stage + at_g, cc, k, g);
             F2 sc[4];
             activation<true>(p.act, g, v);                 // v: act'(g)
-            load_param(p.prm.s, 1.0f, cc, k, sc);
+            load_param(prm.s, 1.0f, cc, k, sc);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const F2 re = e[j] * both(p.rs), dm = re * sc[j], dn = dm * g[j];
@@ -841,12 +867,12 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             store_eight((T*)p.dy + rr * p.lddy, cc, k, u[k]);
         }
     }
-    write_part<TEAM>(p, c, 0, dwy, sums);
-    write_part<TEAM>(p, c, 1, ds, sums);
-    write_part<TEAM>(p, c, 2, dwz, sums);
+    write_part(p, c, 0, dwy, sums);
+    write_part(p, c, 1, ds, sums);
+    write_part(p, c, 2, dwz, sums);
     if constexpr (FULL) {
-        write_part<TEAM>(p, c, 3, dby, sums);
-        write_part<TEAM>(p, c, 4, dbz, sums);
+        write_part(p, c, 3, dby, sums);
+        write_part(p, c, 4, dbz, sums);
     }
     if (TEAM == 0 && p.cluster > 1) cg::this_cluster().sync();
 }
@@ -891,14 +917,14 @@ struct Shape {
 Shape shape_of(int64_t rows, int64_t D, bool vec)
 {
     Shape s;
-    s.team = !vec ? 0 : D <= 64 ? 8 : D <= 256 ? 32 : 0;
+    s.team = D <= 64 && vec ? 8 : D <= 256 ? 32 : 0;
     s.cluster = 1;
     if (s.team) {
         s.threads = 256;
         s.units = div_up(rows, 256 / s.team);
     } else {
         while (s.cluster * kCtaCols < D) s.cluster *= 2;
-        s.threads = (int)(div_up(div_up(D, 16 * s.cluster), 32) * 32);
+        s.threads = vec ? (int)(div_up(div_up(D, 16 * s.cluster), 32) * 32) : 128;
         s.units = rows;
     }
     s.exact = !s.team && s.threads == 128 && (int64_t)kCtaCols * s.cluster == D;
@@ -971,7 +997,12 @@ template <typename T, bool PACK>
 cudaError_t run_forward(const Shape& sh, BArgs& p, bool vec, cudaStream_t s)
 {
     constexpr int n = stages_of<T>(3, 0), one = n * stage_bytes<T>(1, 3, 0), two = n * stage_bytes<T>(2, 3, 0);
-    if (!vec) return launch<k_block<T, 0, 2, kSingle, false>>(sh, p, two, n * 3 * kMargin, 0, s);
+    constexpr int keep = 5 * 8 * (int)sizeof(float);       // kSingle: a thread's parameters
+    if (!vec) {
+        if (sh.team) return launch<k_block<T, 32, 1, kSingle, false>>(sh, p, one, n * 3 * kMargin * 8 + 32 * keep, 0, s);
+        if (p.D <= kCtaCols / 2) return launch<k_block<T, 0, 1, kSingle, false>>(sh, p, one + keep, n * 3 * kMargin, 0, s);
+        return launch<k_block<T, 0, 2, kSingle, false>>(sh, p, two + 2 * keep, n * 3 * kMargin, 0, s);
+    }
     if (sh.team == 8) return launch<k_block<T, 8, 1, kWide, PACK>>(sh, p, one, 0, 0, s);
     if (sh.team == 32) return launch<k_block<T, 32, 1, kWide, PACK>>(sh, p, one, 0, 0, s);
     if (sh.exact) return launch<k_block<T, 0, 2, kExact, PACK>>(sh, p, two, 0, 0, s);
@@ -984,7 +1015,14 @@ cudaError_t run_backward(const Shape& sh, BArgs& p, bool vec, cudaStream_t s)
     constexpr int plain = PACKED ? 2 : 5, held = PACKED ? 3 : 0, n = stages_of<T>(plain, held);
     constexpr int one = n * stage_bytes<T>(1, plain, held), two = n * stage_bytes<T>(2, plain, held);
     const int64_t most = most_parts(sh);
-    if (!vec) return launch<k_block_bwd<T, 0, 2, kSingle, PACKED, FULL>>(sh, p, two, n * 5 * kMargin, most, s);
+    constexpr int keep = 5 * 8 * (int)sizeof(float);
+    if (!vec) {
+        if (sh.team)
+            return launch<k_block_bwd<T, 32, 1, kSingle, PACKED, FULL>>(sh, p, one, n * 5 * kMargin * 8 + 32 * keep, most, s);
+        if (p.D <= kCtaCols / 2)
+            return launch<k_block_bwd<T, 0, 1, kSingle, PACKED, FULL>>(sh, p, one + keep, n * 5 * kMargin, most, s);
+        return launch<k_block_bwd<T, 0, 2, kSingle, PACKED, FULL>>(sh, p, two + 2 * keep, n * 5 * kMargin, most, s);
+    }
     if (sh.team == 8) return launch<k_block_bwd<T, 8, 1, kWide, PACKED, FULL>>(sh, p, one, 0, most, s);
     if (sh.team == 32) return launch<k_block_bwd<T, 32, 1, kWide, PACKED, FULL>>(sh, p, one, 0, most, s);
     if (sh.exact) return launch<k_block_bwd<T, 0, 2, kExact, PACKED, FULL>>(sh, p, two, 0, most, s);
