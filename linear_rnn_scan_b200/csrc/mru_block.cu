@@ -677,7 +677,9 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ ReduceMem mem;
     __shared__ float sums[TEAM ? 2048 : 1];
-    constexpr int PLAIN = PACKED ? 2 : 5, HELD = PACKED ? 3 : 0, STAGES = stages_of<T>(PLAIN, HELD);
+    constexpr int PLAIN = PACKED ? 2 : 5, HELD = PACKED ? 3 : 0;
+    constexpr bool KEEP = LAY != kSingle && TEAM == 0;
+    constexpr int STAGES = KEEP ? 2 : stages_of<T>(PLAIN, HELD);
     int phase = 0, first, cols;
     if (TEAM == 0) clear(mem, p.cluster);
     int64_t row, step;
@@ -711,6 +713,36 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
         else return In(src, row, step, ld, p.rows, p.D, start);
     };
     In fr = input(p.r8, p.r, p.D), fy = input(p.y8, p.y, p.ldy), fg = input(p.g8, p.g, p.ldg);
+    // A CTA's threads keep their columns of the parameters w_y, b_y, s, w_z in
+    // shared memory: beside the rows on their way the L1 cache is too small to
+    // hold them (they came from L2 for every row, as many bytes as the row).
+    float4* kept = reinterpret_cast<float4*>(ring + STAGES * stage_size) + threadIdx.x;
+    auto param = [&](const float* from, float none, int which, int k, F2 (&v)[4]) {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 q = kept[((which * NV + k) * 2 + h) * threads<LAY>()];
+                v[2 * h] = F2{q.x, q.y};
+                v[2 * h + 1] = F2{q.z, q.w};
+            }
+        } else {
+            load_param(from, none, c, k, v);
+        }
+    };
+    if constexpr (KEEP) {
+        const float* from[4] = {prm.w_y, prm.b_y, prm.s, prm.w_z};
+#pragma unroll
+        for (int which = 0; which < 4; ++which)
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                F2 v[4];
+                load_param(from[which], which == 1 ? 0.0f : 1.0f, c, k, v);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    kept[((which * NV + k) * 2 + h) * threads<LAY>()] =
+                        make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
+            }
+    }
     int64_t coming = row;
     unsigned to = 0, from = 0;
     auto fill = [&]() {
@@ -781,7 +813,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             if (p.has_z) {
                 fdz.read(stage + plane, cc, k, u);
                 centred(fr, at_r, mean_r, k, r);
-                load_param(prm.w_z, 1.0f, cc, k, w);
+                param(prm.w_z, 1.0f, 3, k, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) u[j] = u[j] * w[j];
                 s[0] += dot(r, r);
@@ -809,7 +841,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             if (p.has_z) {
                 centred(fr, at_r, mean_r, k, v);
                 fdz.read(stage + plane, cc, k, g);
-                load_param(prm.w_z, 1.0f, cc, k, w);
+                param(prm.w_z, 1.0f, 3, k, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     v[j] = v[j] * rstd;
@@ -824,8 +856,8 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             if (p.dr) store_eight((T*)p.dr + here, cc, k, e);
             if (!p.has_y) continue;
             centred(fy, at_y, mean_y, k, y[k]);
-            load_param(prm.w_y, 1.0f, cc, k, w);
-            load_param(prm.b_y, 0.0f, cc, k, n);
+            param(prm.w_y, 1.0f, 0, k, w);
+            param(prm.b_y, 0.0f, 1, k, n);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 y[k][j] = y[k][j] * both(rstd_y);
@@ -834,7 +866,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             if (gate) fg.read(stage + at_g, cc, k, g);
             F2 sc[4];
             activation<true>(p.act, g, v);                 // v: act'(g)
-            load_param(prm.s, 1.0f, cc, k, sc);
+            param(prm.s, 1.0f, 2, k, sc);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const F2 re = e[j] * both(p.rs), dm = re * sc[j], dn = dm * g[j];
@@ -1025,8 +1057,9 @@ cudaError_t run_backward(const Shape& sh, BArgs& p, bool vec, cudaStream_t s)
     }
     if (sh.team == 8) return launch<k_block_bwd<T, 8, 1, kWide, PACKED, FULL>>(sh, p, one, 0, most, s);
     if (sh.team == 32) return launch<k_block_bwd<T, 32, 1, kWide, PACKED, FULL>>(sh, p, one, 0, most, s);
-    if (sh.exact) return launch<k_block_bwd<T, 0, 2, kExact, PACKED, FULL>>(sh, p, two, 0, most, s);
-    return launch<k_block_bwd<T, 0, 2, kWide, PACKED, FULL>>(sh, p, two, 0, most, s);
+    constexpr int kept = 2 * stage_bytes<T>(2, plain, held) + 2 * 4 * 8 * (int)sizeof(float);
+    if (sh.exact) return launch<k_block_bwd<T, 0, 2, kExact, PACKED, FULL>>(sh, p, kept, 0, most, s);
+    return launch<k_block_bwd<T, 0, 2, kWide, PACKED, FULL>>(sh, p, kept, 0, most, s);
 }
 
 mru_status check_problem(const mru_block_problem* p)
