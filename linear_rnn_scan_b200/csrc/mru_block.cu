@@ -138,6 +138,44 @@ __device__ __forceinline__ mru_block_params keep_params(const mru_block_params& 
     __syncthreads();
     return r;
 }
+// The others: a CTA's threads keep their own columns of the parameters there,
+// COUNT of them.  Beside the rows on their way the L1 cache is too small for
+// them: they came from L2 for every row, as many bytes as the row itself.
+template <bool KEEP, int NV>
+struct Kept {
+    float4* at;
+    int step;
+    template <int COUNT, typename COLS>
+    __device__ __forceinline__ void fill(const float* const (&from)[COUNT], const float (&none)[COUNT], const COLS& c)
+    {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int which = 0; which < COUNT; ++which)
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    F2 v[4];
+                    load_param(from[which], none[which], c, k, v);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        at[((which * NV + k) * 2 + h) * step] = make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
+                }
+        }
+    }
+    template <typename COLS>
+    __device__ __forceinline__ void read(const float* from, float none, int which, const COLS& c, int k, F2 (&v)[4]) const
+    {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 q = at[((which * NV + k) * 2 + h) * step];
+                v[2 * h] = F2{q.x, q.y};
+                v[2 * h + 1] = F2{q.z, q.w};
+            }
+        } else {
+            load_param(from, none, c, k, v);
+        }
+    }
+};
 // Columns that are not there become zero.
 template <typename T, int NV, Lay LAY, int TEAM>
 __device__ __forceinline__ void mask(const Cols<T, NV, LAY, TEAM>& c, int k, F2 (&v)[4])
@@ -532,12 +570,12 @@ __device__ __forceinline__ Cols<T, NV, LAY, TEAM> place(const BArgs& p, int64_t&
     return c;
 }
 
-template <typename T, int TEAM, int NV, Lay LAY, bool PACK>
+template <typename T, int TEAM, int NV, Lay LAY, bool PACK, bool KEEP>
 __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs p)
 {
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ ReduceMem mem;
-    constexpr int STAGES = stages_of<T>(3, 0);
+    constexpr int STAGES = KEEP ? 2 : stages_of<T>(3, 0);
     int phase = 0, first, cols;
     if (TEAM == 0) clear(mem, p.cluster);
     int64_t row, step;
@@ -555,6 +593,8 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
     const int start = LAY ? c.c0 : first;
     Feed<T, T, NV, LAY, TEAM> fr(p.r, row, step, p.D, p.rows, p.D, start), fy(p.y, row, step, p.ldy, p.rows, p.D, start),
         fg(p.g, row, step, p.ldg, p.rows, p.D, start);
+    Kept<KEEP, NV> kept{reinterpret_cast<float4*>(ring + STAGES * stage_size) + threadIdx.x, (int)threads<LAY>()};
+    kept.fill({prm.w_y, prm.b_y, prm.s, prm.w_z, prm.b_z}, {1.0f, 0.0f, 1.0f, 1.0f, 0.0f}, c);
     int64_t coming = row;
     unsigned to = 0, from = 0;                             // stages to fill and to read next, in bytes
     auto fill = [&]() {
@@ -598,15 +638,15 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 F2 w[4], b[4], g[4];
-                load_param(prm.w_y, 1.0f, cc, k, w);
-                load_param(prm.b_y, 0.0f, cc, k, b);
+                kept.read(prm.w_y, 1.0f, 0, cc, k, w);
+                kept.read(prm.b_y, 0.0f, 1, cc, k, b);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) y[k][j] = fma2(y[k][j] * both(rstd), w[j], b[j]);
                 if (gate) fg.read(stage + 2 * plane, cc, k, g);
                 if constexpr (PACK && LAY != kSingle) {
                     if (gate) store_packed(p.g8, rr, p.D, cc, k, g);
                 }
-                load_param(prm.s, 1.0f, cc, k, w);
+                kept.read(prm.s, 1.0f, 2, cc, k, w);
                 activation<false>(p.act, g, b);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) r[k][j] = fma2(w[j] * both(p.rs) * g[j], y[k][j], r[k][j]);
@@ -630,8 +670,8 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 F2 w[4], b[4];
-                load_param(prm.w_z, 1.0f, cc, k, w);
-                load_param(prm.b_z, 0.0f, cc, k, b);
+                kept.read(prm.w_z, 1.0f, 3, cc, k, w);
+                kept.read(prm.b_z, 0.0f, 4, cc, k, b);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) r[k][j] = fma2(r[k][j] * both(rstd), w[j], b[j]);
                 store_eight((T*)p.z + here, cc, k, r[k]);
@@ -713,36 +753,8 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
         else return In(src, row, step, ld, p.rows, p.D, start);
     };
     In fr = input(p.r8, p.r, p.D), fy = input(p.y8, p.y, p.ldy), fg = input(p.g8, p.g, p.ldg);
-    // A CTA's threads keep their columns of the parameters w_y, b_y, s, w_z in
-    // shared memory: beside the rows on their way the L1 cache is too small to
-    // hold them (they came from L2 for every row, as many bytes as the row).
-    float4* kept = reinterpret_cast<float4*>(ring + STAGES * stage_size) + threadIdx.x;
-    auto param = [&](const float* from, float none, int which, int k, F2 (&v)[4]) {
-        if constexpr (KEEP) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float4 q = kept[((which * NV + k) * 2 + h) * threads<LAY>()];
-                v[2 * h] = F2{q.x, q.y};
-                v[2 * h + 1] = F2{q.z, q.w};
-            }
-        } else {
-            load_param(from, none, c, k, v);
-        }
-    };
-    if constexpr (KEEP) {
-        const float* from[4] = {prm.w_y, prm.b_y, prm.s, prm.w_z};
-#pragma unroll
-        for (int which = 0; which < 4; ++which)
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                F2 v[4];
-                load_param(from[which], which == 1 ? 0.0f : 1.0f, c, k, v);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    kept[((which * NV + k) * 2 + h) * threads<LAY>()] =
-                        make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
-            }
-    }
+    Kept<KEEP, NV> kept{reinterpret_cast<float4*>(ring + STAGES * stage_size) + threadIdx.x, (int)threads<LAY>()};
+    kept.fill({prm.w_y, prm.b_y, prm.s, prm.w_z}, {1.0f, 0.0f, 1.0f, 1.0f}, c);
     int64_t coming = row;
     unsigned to = 0, from = 0;
     auto fill = [&]() {
@@ -813,7 +825,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             if (p.has_z) {
                 fdz.read(stage + plane, cc, k, u);
                 centred(fr, at_r, mean_r, k, r);
-                param(prm.w_z, 1.0f, 3, k, w);
+                kept.read(prm.w_z, 1.0f, 3, cc, k, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) u[j] = u[j] * w[j];
                 s[0] += dot(r, r);
@@ -841,7 +853,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             if (p.has_z) {
                 centred(fr, at_r, mean_r, k, v);
                 fdz.read(stage + plane, cc, k, g);
-                param(prm.w_z, 1.0f, 3, k, w);
+                kept.read(prm.w_z, 1.0f, 3, cc, k, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     v[j] = v[j] * rstd;
@@ -856,8 +868,8 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             if (p.dr) store_eight((T*)p.dr + here, cc, k, e);
             if (!p.has_y) continue;
             centred(fy, at_y, mean_y, k, y[k]);
-            param(prm.w_y, 1.0f, 0, k, w);
-            param(prm.b_y, 0.0f, 1, k, n);
+            kept.read(prm.w_y, 1.0f, 0, cc, k, w);
+            kept.read(prm.b_y, 0.0f, 1, cc, k, n);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 y[k][j] = y[k][j] * both(rstd_y);
@@ -866,7 +878,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
             if (gate) fg.read(stage + at_g, cc, k, g);
             F2 sc[4];
             activation<true>(p.act, g, v);                 // v: act'(g)
-            param(prm.s, 1.0f, 2, k, sc);
+            kept.read(prm.s, 1.0f, 2, cc, k, sc);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const F2 re = e[j] * both(p.rs), dm = re * sc[j], dn = dm * g[j];
@@ -1024,21 +1036,30 @@ cudaError_t launch(const Shape& sh, BArgs& p, int per_thread, int extra, int64_t
 
 // The column layout's instance: teams of 8 lanes and of a warp, CTAs whose
 // columns may all be there, and the one for rows that cannot be read in
-// aligned pieces of 8 columns.
+// aligned pieces of 8 columns.  bf16 rows of one CTA keep their parameters in
+// shared memory: 32768 x 2048 RMS norm 128 -> 118 us, layer norm 162 -> 138.
+// fp32 rows (110.5 -> 112.1) and clusters (16384 x 4096 191 -> 224, 4096 x
+// 16384 215 -> 266), which want the CTAs that it costs, do not; the backward's
+// CTAs, fewer and with more parameters to read twice, always do (bf16 280 -> 204,
+// fp32 204 -> 204, 16384 x 4096 416 -> 307).
 template <typename T, bool PACK>
 cudaError_t run_forward(const Shape& sh, BArgs& p, bool vec, cudaStream_t s)
 {
     constexpr int n = stages_of<T>(3, 0), one = n * stage_bytes<T>(1, 3, 0), two = n * stage_bytes<T>(2, 3, 0);
     constexpr int keep = 5 * 8 * (int)sizeof(float);       // kSingle: a thread's parameters
     if (!vec) {
-        if (sh.team) return launch<k_block<T, 32, 1, kSingle, false>>(sh, p, one, n * 3 * kMargin * 8 + 32 * keep, 0, s);
-        if (p.D <= kCtaCols / 2) return launch<k_block<T, 0, 1, kSingle, false>>(sh, p, one + keep, n * 3 * kMargin, 0, s);
-        return launch<k_block<T, 0, 2, kSingle, false>>(sh, p, two + 2 * keep, n * 3 * kMargin, 0, s);
+        if (sh.team) return launch<k_block<T, 32, 1, kSingle, false, false>>(sh, p, one, n * 3 * kMargin * 8 + 32 * keep, 0, s);
+        if (p.D <= kCtaCols / 2) return launch<k_block<T, 0, 1, kSingle, false, false>>(sh, p, one + keep, n * 3 * kMargin, 0, s);
+        return launch<k_block<T, 0, 2, kSingle, false, false>>(sh, p, two + 2 * keep, n * 3 * kMargin, 0, s);
     }
-    if (sh.team == 8) return launch<k_block<T, 8, 1, kWide, PACK>>(sh, p, one, 0, 0, s);
-    if (sh.team == 32) return launch<k_block<T, 32, 1, kWide, PACK>>(sh, p, one, 0, 0, s);
-    if (sh.exact) return launch<k_block<T, 0, 2, kExact, PACK>>(sh, p, two, 0, 0, s);
-    return launch<k_block<T, 0, 2, kWide, PACK>>(sh, p, two, 0, 0, s);
+    if (sh.team == 8) return launch<k_block<T, 8, 1, kWide, PACK, false>>(sh, p, one, 0, 0, s);
+    if (sh.team == 32) return launch<k_block<T, 32, 1, kWide, PACK, false>>(sh, p, one, 0, 0, s);
+    constexpr int kept = 2 * stage_bytes<T>(2, 3, 0) + 2 * 5 * 8 * (int)sizeof(float);
+    if constexpr (sizeof(T) == 2) {
+        if (sh.exact && sh.cluster == 1) return launch<k_block<T, 0, 2, kExact, PACK, true>>(sh, p, kept, 0, 0, s);
+    }
+    if (sh.exact) return launch<k_block<T, 0, 2, kExact, PACK, false>>(sh, p, two, 0, 0, s);
+    return launch<k_block<T, 0, 2, kWide, PACK, false>>(sh, p, two, 0, 0, s);
 }
 
 template <typename T, bool PACKED, bool FULL>
