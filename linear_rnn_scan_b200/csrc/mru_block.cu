@@ -43,8 +43,8 @@ struct BArgs {
 // How a thread's columns lie: in pieces of 16 bytes of the rows' type (U = 8 or
 // 4 columns), a team's pieces side by side (kWide; kExact: every one of them
 // is there and the CTA has 128 threads, so that offsets are constants), or one
-// by one (kSingle: a warp or 128 threads to a row).  NV eights of columns to a thread; D counts as 0 for rows
-// past the end.
+// by one (kSingle: a warp or 128 threads to a row).  NV eights of columns to a
+// thread; D counts as 0 for rows past the end.
 enum Lay { kSingle, kWide, kExact };
 template <Lay LAY>
 __device__ __forceinline__ unsigned threads() { return LAY == kWide ? blockDim.x : 128u; }
@@ -247,7 +247,7 @@ __device__ __forceinline__ void store_packed(const mru_packed8& h, int64_t row, 
 
 // ------------------------------------------------------- rows on their way ---
 //
-// The coming rows' inputs are copied to shared memory asynchronously, 2 to 4
+// The coming rows' inputs are copied to shared memory asynchronously, 1 to 3
 // rows ahead, so that the memory's latency is covered by rows in flight and
 // not by resident warps (whose registers hold whole rows).  kWide, kExact:
 // every thread copies its own columns and reads them back itself, without a
@@ -570,6 +570,11 @@ __device__ __forceinline__ Cols<T, NV, LAY, TEAM> place(const BArgs& p, int64_t&
     return c;
 }
 
+// The forward.  Bound by bytes: three reads and two writes of the type.  B200,
+// of the measured copy rate: 32768 x 2048 bf16 118 us (88 %), 16384 x 2048 fp32
+// 111 us (94 %).  Rows of a cluster wait for its barriers, about a microsecond
+// each with their skew: 16384 x 4096 191 us (55 %), 4096 x 16384 214 us (49 %),
+// with 8-bit copies 272 us (50 %).
 template <typename T, int TEAM, int NV, Lay LAY, bool PACK, bool KEEP>
 __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs p)
 {
@@ -711,6 +716,12 @@ __device__ __forceinline__ void write_part(const BArgs& p, const Cols<T, NV, LAY
 // FULL: layer norm, or sums for the biases.  The inputs are read from their
 // stage where they are used, twice where that is cheaper than holding them:
 // only what the second reduction has to wait for stays in registers.
+// With e = dr' + N'(dz w_z) and dm = rs s e: dr = e, dg = dm n act'(g) and dy =
+// N'(dm act(g) w_y), where N'(u) = rstd (u - mean(u)[layer] - yhat mean(u yhat)).
+// Bound by bytes where a CTA holds a row: five reads and three writes, 32768 x
+// 2048 bf16 204 us (82 % of the measured copy rate), fp32 16384 x 2048 204 us
+// (82 %); layer norm 275 us (61 %: more sums and registers, 3 CTAs to an SM);
+// clusters by their barriers: 16384 x 4096 307 us, 4096 x 16384 367 us.
 template <typename T, int TEAM, int NV, Lay LAY, bool PACKED, bool FULL>
 __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BArgs p)
 {

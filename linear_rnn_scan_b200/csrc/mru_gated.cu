@@ -501,6 +501,15 @@ __device__ __forceinline__ void forward_manage(const Args& g, const Maps& maps, 
     }
 }
 
+// The forward.  A tile's map is (P, H), the product of its decays and its state
+// from zero, so a carry is applied as P h + H and maps compose in any grouping.
+// Bound by bytes: (inputs + 1) of the type per element and a state per 64
+// tokens; what it misses of that goes to the wait for a carry, from one tile's
+// map to the next one's (2 to 3 blocks to an SM cover it in part).  B200, of
+// the measured copy rate: sigmoid bf16 B4 L4096 D8192 176 us (71 %), decay fp32
+// B1 L65536 D2048 364 us (69 %), lru fp32 B8 L4096 D1024 100 us (84 %); the lru
+// gate's calls of the special-function unit (two sigmoids, an exponential, a
+// root per element) hold bf16 to 150 us (55 %) at B8 L4096 D2048, with 8-bit copies 272 us (43 %).
 template <typename T, int C, int GATE, bool VEC, bool PACK>
 __global__ void __launch_bounds__(kThreads, C == 2 ? 3 : 2) k_gated_tile(Args g, const __grid_constant__ Maps maps)
 {
@@ -869,6 +878,14 @@ __device__ __forceinline__ void backward_manage(const Args& g, const Maps& maps,
     if (it > 0) flush(mem.tile[(it - 1) & 3]);
 }
 
+// The backward: d_t = dy_t + a_{t+1} d_{t+1} runs from the last tile like the
+// forward, the states are run again inside the tile from the one kept at its
+// start, and both meet in registers, so that every input and dy are read once.
+// Two channels to a lane: the decays, factors and dy of 8 tokens take the
+// registers of two blocks.  B200: sigmoid bf16 B4 L4096 D8192 338 us (62 % of
+// the measured copy rate), decay fp32 B1 L65536 D2048 519 us (80 %); lru is
+// bound by instructions and the special-function unit: bf16 B8 L4096 D2048
+// 353 us (41 %), from 8-bit copies 440 us (26 %).
 template <typename T, int C, int GATE, bool VEC, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 2) k_gated_tile_bwd(Args g, const __grid_constant__ Maps maps)
 {

@@ -70,7 +70,9 @@ __device__ __forceinline__ int64_t quotient(int64_t k, int32_t d)
 }
 
 // Pieces of 16 channels, `rows` x `per_row`; a row's pieces fill whole runs of
-// lanes (per_row a multiple of 4 lanes' pieces, the last ones empty).
+// lanes (per_row a multiple of 4 lanes' pieces, the last ones empty).  Bound by
+// bytes, 3 + 1/16 of bf16: 32768 x 2048 to and from 8 bits 81 us (79 % of the
+// measured copy rate).
 template <typename T>
 __global__ void __launch_bounds__(256) k_pack8_wide(int64_t rows, int32_t D, int32_t per_row, int64_t ld,
                                                     const T* __restrict__ x, int8_t* __restrict__ q,
