@@ -7,6 +7,7 @@
 // 16 columns to a thread, packed fp32 arithmetic and sums exchanged by halves
 // of a warp keep the instructions per element below what memory allows.
 #include <cooperative_groups.h>
+#include <stddef.h>
 #include <string.h>
 
 #include <atomic>
@@ -409,18 +410,53 @@ struct HeldFeed {
 // Sums over a row's team, the same bits in every thread.  TEAM > 0: lanes of a
 // warp; 0: the CTA, and its cluster where there is one.  Buffers alternate, so
 // that one barrier serves a reduction: a buffer is written again only after
-// the next reduction's barrier, which every reader has reached.
+// the next reduction's barrier, which every reader has reached.  CTAs of a
+// cluster send their sums with stores that count on the receiver's mbarrier: a
+// barrier of the whole cluster would also wait for the rows' stores to memory.
 struct ReduceMem {
     float4 warp[2][4];                     // [sum], a warp to a component; warps that are not there stay 0
     float4 cta[2][4][2];                   // [sum], a CTA of the cluster to a component; the same
+    uint64_t full[2];                      // the cluster's sums are there
 };
+// Bits of a thread's `phase`: the buffer in turn, its mbarrier's parity, and
+// whether a wait gave up.
+constexpr int kBuffer = 1, kParity = 2, kLost = 4;
 
-__device__ __forceinline__ void clear(ReduceMem& m, int cluster)
+__device__ __forceinline__ unsigned shared_at(const void* p) { return (unsigned)__cvta_generic_to_shared(p); }
+
+template <bool MANY>
+__device__ __forceinline__ void clear(ReduceMem& m)
 {
     float* f = reinterpret_cast<float*>(&m);
-    for (int k = threadIdx.x; k < (int)(sizeof(ReduceMem) / 4); k += blockDim.x) f[k] = 0.0f;
-    if (cluster > 1) cg::this_cluster().sync();            // before another CTA writes here
-    else __syncthreads();
+    for (int k = threadIdx.x; k < (int)(offsetof(ReduceMem, full) / 4); k += blockDim.x) f[k] = 0.0f;
+    if constexpr (MANY) {
+        if (threadIdx.x == 0) {
+            for (int k = 0; k < 2; ++k) asm volatile("mbarrier.init.shared.b64 [%0], 1;" ::"r"(shared_at(&m.full[k])) : "memory");
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        cg::this_cluster().sync();                         // before another CTA writes here
+    } else {
+        __syncthreads();
+    }
+}
+
+// Waits for the cluster's sums, 2 s at most; false: it gave up.
+__device__ __forceinline__ bool sums_there(unsigned barrier, unsigned parity)
+{
+    uint64_t t0 = 0;
+    for (int n = 0;; ++n) {
+        unsigned done;
+        asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                     : "=r"(done)
+                     : "r"(barrier), "r"(parity)
+                     : "memory");
+        if (done) return true;
+        if ((n & 255) != 255) continue;
+        uint64_t t;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        if (t0 == 0) t0 = t;
+        if (t - t0 > 2000000000ull) return false;
+    }
 }
 
 // N sums of a warp: halves of it take over half of the sums each, so that 4
@@ -448,7 +484,7 @@ __device__ __forceinline__ float warp_sums(const float (&v)[N], int lane)
     return r;
 }
 
-template <int TEAM, int N>
+template <int TEAM, bool MANY, int N>
 __device__ __forceinline__ void team_sum(float (&v)[N], ReduceMem& m, int cluster, int& phase)
 {
     if constexpr (TEAM > 0) {
@@ -458,30 +494,40 @@ __device__ __forceinline__ void team_sum(float (&v)[N], ReduceMem& m, int cluste
             for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(~0u, v[k], o);
     } else {
         const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+        const int buffer = MANY ? phase & kBuffer : phase;
         const float r = warp_sums(v, lane);
-        if (lane % (32 / N) == 0) reinterpret_cast<float*>(&m.warp[phase][lane * N / 32])[warp] = r;
+        if (lane % (32 / N) == 0) reinterpret_cast<float*>(&m.warp[buffer][lane * N / 32])[warp] = r;
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const float4 q = m.warp[phase][k];
+            const float4 q = m.warp[buffer][k];
             v[k] = (q.x + q.y) + (q.z + q.w);
         }
-        if (cluster > 1) {
-            cg::cluster_group cl = cg::this_cluster();
-            const unsigned rank = cl.block_rank();
-            if ((int)threadIdx.x < cluster) {
-                float* to = cl.map_shared_rank(reinterpret_cast<float*>(&m.cta[phase][0][0]), threadIdx.x);
-#pragma unroll
-                for (int k = 0; k < N; ++k) to[8 * k + rank] = v[k];
+        if constexpr (MANY) {
+            const unsigned barrier = shared_at(&m.full[buffer]);
+            if (threadIdx.x == 0)
+                asm volatile("mbarrier.arrive.expect_tx.relaxed.cta.shared::cta.b64 _, [%0], %1;" ::"r"(barrier),
+                             "r"(cluster * N * 4)
+                             : "memory");
+            if ((int)threadIdx.x < cluster * N) {          // a thread to a CTA and a sum: within the first warp
+                const unsigned rank = cg::this_cluster().block_rank(), to = threadIdx.x % cluster, k = threadIdx.x / cluster;
+                const float sum = N == 1 ? v[0] : N == 2 ? (k ? v[N - 1] : v[0]) : k & 2 ? (k & 1 ? v[N - 1] : v[N / 2]) : (k & 1 ? v[N > 1] : v[0]);
+                asm volatile(
+                    "{\n.reg .u32 a, b;\nmapa.shared::cluster.u32 a, %0, %2;\nmapa.shared::cluster.u32 b, %1, %2;\n"
+                    "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [a], %3, [b];\n}" ::"r"(
+                        shared_at(&m.cta[buffer][k][0]) + 4 * rank),
+                    "r"(barrier), "r"(to), "r"(__float_as_uint(sum))
+                    : "memory");
             }
-            cl.sync();
+            if (!(phase & kLost) && !sums_there(barrier, phase / kParity & 1)) phase |= kLost;
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                const float4 q = m.cta[phase][k][0], u = m.cta[phase][k][1];
+                const float4 q = m.cta[buffer][k][0], u = m.cta[buffer][k][1];
                 v[k] = ((q.x + q.y) + (q.z + q.w)) + ((u.x + u.y) + (u.z + u.w));
+                if (phase & kLost) v[k] = __uint_as_float(0x7fc00000u);
             }
         }
-        phase ^= 1;
+        phase ^= MANY && (phase & kBuffer) ? kBuffer | kParity : kBuffer;
     }
 }
 
@@ -520,7 +566,7 @@ __device__ __forceinline__ void activation(int act, F2 (&g)[N], F2 (&da)[N])
 }
 
 // v - mean (layer norm) and 1 / sqrt(mean square + eps) of a row.
-template <typename T, int NV, Lay LAY, int TEAM>
+template <bool MANY, typename T, int NV, Lay LAY, int TEAM>
 __device__ __forceinline__ float normalise(const BArgs& p, const Cols<T, NV, LAY, TEAM>& c, F2 (&v)[NV][4], ReduceMem& m, int& phase)
 {
     const float inv_d = 1.0f / (float)p.D;
@@ -528,7 +574,7 @@ __device__ __forceinline__ float normalise(const BArgs& p, const Cols<T, NV, LAY
     if (p.norm == MRU_NORM_LAYER) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) s[0] += total(v[k]);
-        team_sum<TEAM>(s, m, p.cluster, phase);
+        team_sum<TEAM, MANY>(s, m, p.cluster, phase);
         const F2 mean = both(-s[0] * inv_d);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -540,7 +586,7 @@ __device__ __forceinline__ float normalise(const BArgs& p, const Cols<T, NV, LAY
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) s[0] += dot(v[k], v[k]);
-    team_sum<TEAM>(s, m, p.cluster, phase);
+    team_sum<TEAM, MANY>(s, m, p.cluster, phase);
     return inv_root(fmaf(s[0], inv_d, p.eps));
 }
 
@@ -575,14 +621,14 @@ __device__ __forceinline__ Cols<T, NV, LAY, TEAM> place(const BArgs& p, int64_t&
 // 111 us (94 %).  Rows of a cluster wait for its barriers, about a microsecond
 // each with their skew: 16384 x 4096 191 us (55 %), 4096 x 16384 214 us (49 %),
 // with 8-bit copies 272 us (50 %).
-template <typename T, int TEAM, int NV, Lay LAY, bool PACK, bool KEEP>
+template <typename T, int TEAM, int NV, Lay LAY, bool PACK, bool KEEP, bool MANY>
 __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs p)
 {
-    extern __shared__ __align__(16) unsigned char ring[];
+    extern __shared__ __align__(128) unsigned char ring[];             // a warp's pieces in whole lines: 16384 x 2048 f32 126 -> 110 us
     __shared__ ReduceMem mem;
     constexpr int STAGES = KEEP ? 2 : stages_of<T>(3, 0);
     int phase = 0, first, cols;
-    if (TEAM == 0) clear(mem, p.cluster);
+    if (TEAM == 0) clear<MANY>(mem);
     int64_t row, step;
     const Cols<T, NV, LAY, TEAM> c = place<TEAM, T, NV, LAY>(p, row, step, first, cols);
     // teams of a warp take their shuffles together: rows past the end go through the motions
@@ -639,7 +685,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
                 fy.read(stage + plane, cc, k, y[k]);
                 if constexpr (PACK && LAY != kSingle) store_packed(p.y8, rr, p.D, cc, k, y[k]);
             }
-            const float rstd = normalise(p, cc, y, mem, phase);
+            const float rstd = normalise<MANY>(p, cc, y, mem, phase);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 F2 w[4], b[4], g[4];
@@ -671,7 +717,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
             }
         }
         if (p.has_z) {
-            const float rstd = normalise(p, cc, r, mem, phase);
+            const float rstd = normalise<MANY>(p, cc, r, mem, phase);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 F2 w[4], b[4];
@@ -683,7 +729,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs 
             }
         }
     }
-    if (TEAM == 0 && p.cluster > 1) cg::this_cluster().sync();     // peers may still write this CTA's sums
+    if constexpr (MANY) cg::this_cluster().sync();     // peers may still write this CTA's sums
 }
 
 // A CTA's (cluster's) sums over its rows of one parameter's gradient.
@@ -722,17 +768,17 @@ __device__ __forceinline__ void write_part(const BArgs& p, const Cols<T, NV, LAY
 // 2048 bf16 204 us (82 % of the measured copy rate), fp32 16384 x 2048 204 us
 // (82 %); layer norm 275 us (61 %: more sums and registers, 3 CTAs to an SM);
 // clusters by their barriers: 16384 x 4096 307 us, 4096 x 16384 367 us.
-template <typename T, int TEAM, int NV, Lay LAY, bool PACKED, bool FULL>
+template <typename T, int TEAM, int NV, Lay LAY, bool PACKED, bool FULL, bool MANY>
 __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BArgs p)
 {
-    extern __shared__ __align__(16) unsigned char ring[];
+    extern __shared__ __align__(128) unsigned char ring[];             // a warp's pieces in whole lines: 16384 x 2048 f32 126 -> 110 us
     __shared__ ReduceMem mem;
     __shared__ float sums[TEAM ? 2048 : 1];
     constexpr int PLAIN = PACKED ? 2 : 5, HELD = PACKED ? 3 : 0;
     constexpr bool KEEP = LAY != kSingle && TEAM == 0;
     constexpr int STAGES = KEEP ? 2 : stages_of<T>(PLAIN, HELD);
     int phase = 0, first, cols;
-    if (TEAM == 0) clear(mem, p.cluster);
+    if (TEAM == 0) clear<MANY>(mem);
     int64_t row, step;
     const Cols<T, NV, LAY, TEAM> c = place<TEAM, T, NV, LAY>(p, row, step, first, cols);
     const int64_t last = TEAM ? (p.rows + step - 1) / step * step : p.rows;
@@ -813,7 +859,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
                     s[1] += total(v);
                 }
             }
-            team_sum<TEAM>(s, mem, p.cluster, phase);
+            team_sum<TEAM, MANY>(s, mem, p.cluster, phase);
             mean_r = -s[0] * inv_d;
             mean_y = -s[1] * inv_d;
         }
@@ -844,7 +890,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
                 if (FULL) s[3] += total(u);
             }
         }
-        team_sum<TEAM>(s, mem, p.cluster, phase);
+        team_sum<TEAM, MANY>(s, mem, p.cluster, phase);
         // a row past the end adds nothing to the sums, whatever eps is
         const float rstd_y = live ? inv_root(fmaf(s[2], inv_d, p.eps)) : 0.0f;
         const F2 rstd = both(live ? inv_root(fmaf(s[0], inv_d, p.eps)) : 0.0f);
@@ -909,7 +955,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
         fy.done();
         fg.done();
         if (!p.has_y) continue;
-        team_sum<TEAM>(t, mem, p.cluster, phase);
+        team_sum<TEAM, MANY>(t, mem, p.cluster, phase);
         const F2 t1 = both(-t[0] * inv_d), t0 = both(layer ? -t[1] * inv_d : 0.0f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -929,7 +975,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BA
         write_part(p, c, 3, dby, sums);
         write_part(p, c, 4, dbz, sums);
     }
-    if (TEAM == 0 && p.cluster > 1) cg::this_cluster().sync();
+    if constexpr (MANY) cg::this_cluster().sync();
 }
 
 struct GradOut {
@@ -1059,18 +1105,23 @@ cudaError_t run_forward(const Shape& sh, BArgs& p, bool vec, cudaStream_t s)
     constexpr int n = stages_of<T>(3, 0), one = n * stage_bytes<T>(1, 3, 0), two = n * stage_bytes<T>(2, 3, 0);
     constexpr int keep = 5 * 8 * (int)sizeof(float);       // kSingle: a thread's parameters
     if (!vec) {
-        if (sh.team) return launch<k_block<T, 32, 1, kSingle, false, false>>(sh, p, one, n * 3 * kMargin * 8 + 32 * keep, 0, s);
-        if (p.D <= kCtaCols / 2) return launch<k_block<T, 0, 1, kSingle, false, false>>(sh, p, one + keep, n * 3 * kMargin, 0, s);
-        return launch<k_block<T, 0, 2, kSingle, false, false>>(sh, p, two + 2 * keep, n * 3 * kMargin, 0, s);
+        if (sh.team) return launch<k_block<T, 32, 1, kSingle, false, false, false>>(sh, p, one, n * 3 * kMargin * 8 + 32 * keep, 0, s);
+        if (p.D <= kCtaCols / 2) return launch<k_block<T, 0, 1, kSingle, false, false, false>>(sh, p, one + keep, n * 3 * kMargin, 0, s);
+        if (sh.cluster > 1)
+            return launch<k_block<T, 0, 2, kSingle, false, false, true>>(sh, p, two + 2 * keep, n * 3 * kMargin, 0, s);
+        return launch<k_block<T, 0, 2, kSingle, false, false, false>>(sh, p, two + 2 * keep, n * 3 * kMargin, 0, s);
     }
-    if (sh.team == 8) return launch<k_block<T, 8, 1, kWide, PACK, false>>(sh, p, one, 0, 0, s);
-    if (sh.team == 32) return launch<k_block<T, 32, 1, kWide, PACK, false>>(sh, p, one, 0, 0, s);
+    if (sh.team == 8) return launch<k_block<T, 8, 1, kWide, PACK, false, false>>(sh, p, one, 0, 0, s);
+    if (sh.team == 32) return launch<k_block<T, 32, 1, kWide, PACK, false, false>>(sh, p, one, 0, 0, s);
+    if (sh.cluster > 1)
+        return sh.exact ? launch<k_block<T, 0, 2, kExact, PACK, false, true>>(sh, p, two, 0, 0, s)
+                        : launch<k_block<T, 0, 2, kWide, PACK, false, true>>(sh, p, two, 0, 0, s);
     constexpr int kept = 2 * stage_bytes<T>(2, 3, 0) + 2 * 5 * 8 * (int)sizeof(float);
     if constexpr (sizeof(T) == 2) {
-        if (sh.exact && sh.cluster == 1) return launch<k_block<T, 0, 2, kExact, PACK, true>>(sh, p, kept, 0, 0, s);
+        if (sh.exact) return launch<k_block<T, 0, 2, kExact, PACK, true, false>>(sh, p, kept, 0, 0, s);
     }
-    if (sh.exact) return launch<k_block<T, 0, 2, kExact, PACK, false>>(sh, p, two, 0, 0, s);
-    return launch<k_block<T, 0, 2, kWide, PACK, false>>(sh, p, two, 0, 0, s);
+    if (sh.exact) return launch<k_block<T, 0, 2, kExact, PACK, false, false>>(sh, p, two, 0, 0, s);
+    return launch<k_block<T, 0, 2, kWide, PACK, false, false>>(sh, p, two, 0, 0, s);
 }
 
 template <typename T, bool PACKED, bool FULL>
@@ -1082,16 +1133,21 @@ cudaError_t run_backward(const Shape& sh, BArgs& p, bool vec, cudaStream_t s)
     constexpr int keep = 5 * 8 * (int)sizeof(float);
     if (!vec) {
         if (sh.team)
-            return launch<k_block_bwd<T, 32, 1, kSingle, PACKED, FULL>>(sh, p, one, n * 5 * kMargin * 8 + 32 * keep, most, s);
+            return launch<k_block_bwd<T, 32, 1, kSingle, PACKED, FULL, false>>(sh, p, one, n * 5 * kMargin * 8 + 32 * keep, most, s);
         if (p.D <= kCtaCols / 2)
-            return launch<k_block_bwd<T, 0, 1, kSingle, PACKED, FULL>>(sh, p, one + keep, n * 5 * kMargin, most, s);
-        return launch<k_block_bwd<T, 0, 2, kSingle, PACKED, FULL>>(sh, p, two + 2 * keep, n * 5 * kMargin, most, s);
+            return launch<k_block_bwd<T, 0, 1, kSingle, PACKED, FULL, false>>(sh, p, one + keep, n * 5 * kMargin, most, s);
+        if (sh.cluster > 1)
+            return launch<k_block_bwd<T, 0, 2, kSingle, PACKED, FULL, true>>(sh, p, two + 2 * keep, n * 5 * kMargin, most, s);
+        return launch<k_block_bwd<T, 0, 2, kSingle, PACKED, FULL, false>>(sh, p, two + 2 * keep, n * 5 * kMargin, most, s);
     }
-    if (sh.team == 8) return launch<k_block_bwd<T, 8, 1, kWide, PACKED, FULL>>(sh, p, one, 0, most, s);
-    if (sh.team == 32) return launch<k_block_bwd<T, 32, 1, kWide, PACKED, FULL>>(sh, p, one, 0, most, s);
+    if (sh.team == 8) return launch<k_block_bwd<T, 8, 1, kWide, PACKED, FULL, false>>(sh, p, one, 0, most, s);
+    if (sh.team == 32) return launch<k_block_bwd<T, 32, 1, kWide, PACKED, FULL, false>>(sh, p, one, 0, most, s);
     constexpr int kept = 2 * stage_bytes<T>(2, plain, held) + 2 * 4 * 8 * (int)sizeof(float);
-    if (sh.exact) return launch<k_block_bwd<T, 0, 2, kExact, PACKED, FULL>>(sh, p, kept, 0, most, s);
-    return launch<k_block_bwd<T, 0, 2, kWide, PACKED, FULL>>(sh, p, kept, 0, most, s);
+    if (sh.cluster > 1)
+        return sh.exact ? launch<k_block_bwd<T, 0, 2, kExact, PACKED, FULL, true>>(sh, p, kept, 0, most, s)
+                        : launch<k_block_bwd<T, 0, 2, kWide, PACKED, FULL, true>>(sh, p, kept, 0, most, s);
+    if (sh.exact) return launch<k_block_bwd<T, 0, 2, kExact, PACKED, FULL, false>>(sh, p, kept, 0, most, s);
+    return launch<k_block_bwd<T, 0, 2, kWide, PACKED, FULL, false>>(sh, p, kept, 0, most, s);
 }
 
 mru_status check_problem(const mru_block_problem* p)
