@@ -478,7 +478,9 @@ mru_status mru_block_norm(const mru_block_problem* p, const mru_block_params* pr
  * and the parameters' sums over rows.  dr_out or dz may be NULL (zero; not
  * both).  dr may be NULL when not wanted; y (or its copy) NULL: no block
  * before, then dy and dg are NULL.  The same call gives the same bits every
- * time.  Nothing can fail on the device: the workspace has no status word. */
+ * time.  Nothing is found on the device: the workspace has no status word.  (The
+ * CTAs that share a row wider than 2048 wait for each other's sums, for 2 s at
+ * most; a wait that gives up leaves NaN in what the row's sums reach.) */
 size_t mru_block_backward_workspace_size(const mru_block_problem* p);
 mru_status mru_block_norm_backward(const mru_block_problem* p, const mru_block_params* prm, const void* r_out,
                                    const void* y, const void* g, const mru_block_saved* saved, const void* dr_out,

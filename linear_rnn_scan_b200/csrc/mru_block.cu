@@ -412,7 +412,9 @@ struct HeldFeed {
 // that one barrier serves a reduction: a buffer is written again only after
 // the next reduction's barrier, which every reader has reached.  CTAs of a
 // cluster send their sums with stores that count on the receiver's mbarrier: a
-// barrier of the whole cluster would also wait for the rows' stores to memory.
+// barrier of the whole cluster also waits for the rows' stores to memory (4096 x
+// 16384 bf16 forward 214 us with it, 166 without).  A CTA sends its sums of the
+// next reduction only when it has read these, so two buffers do.
 struct ReduceMem {
     float4 warp[2][4];                     // [sum], a warp to a component; warps that are not there stay 0
     float4 cta[2][4][2];                   // [sum], a CTA of the cluster to a component; the same
@@ -440,7 +442,9 @@ __device__ __forceinline__ void clear(ReduceMem& m)
     }
 }
 
-// Waits for the cluster's sums, 2 s at most; false: it gave up.
+// Waits for the cluster's sums, 2 s at most (its CTAs run at the same time, so
+// nothing but a fault can keep them away); false: it gave up, and the row's
+// sums become NaN.
 __device__ __forceinline__ bool sums_there(unsigned barrier, unsigned parity)
 {
     uint64_t t0 = 0;
@@ -618,9 +622,9 @@ __device__ __forceinline__ Cols<T, NV, LAY, TEAM> place(const BArgs& p, int64_t&
 
 // The forward.  Bound by bytes: three reads and two writes of the type.  B200,
 // of the measured copy rate: 32768 x 2048 bf16 118 us (88 %), 16384 x 2048 fp32
-// 111 us (94 %).  Rows of a cluster wait for its barriers, about a microsecond
-// each with their skew: 16384 x 4096 191 us (55 %), 4096 x 16384 214 us (49 %),
-// with 8-bit copies 272 us (50 %).
+// 110 us (95 %).  Rows of a cluster wait for its other CTAs' sums: 16384 x 4096
+// 151 us (69 %), 4096 x 16384 166 us (63 %), with 8-bit copies 265 us (52 %;
+// beside the wait, instructions of the packing).
 template <typename T, int TEAM, int NV, Lay LAY, bool PACK, bool KEEP, bool MANY>
 __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 4 : 5) k_block(BArgs p)
 {
@@ -766,8 +770,9 @@ __device__ __forceinline__ void write_part(const BArgs& p, const Cols<T, NV, LAY
 // N'(dm act(g) w_y), where N'(u) = rstd (u - mean(u)[layer] - yhat mean(u yhat)).
 // Bound by bytes where a CTA holds a row: five reads and three writes, 32768 x
 // 2048 bf16 204 us (82 % of the measured copy rate), fp32 16384 x 2048 204 us
-// (82 %); layer norm 275 us (61 %: more sums and registers, 3 CTAs to an SM);
-// clusters by their barriers: 16384 x 4096 307 us, 4096 x 16384 367 us.
+// (82 %); layer norm 273 us (61 %: more sums and registers, 3 CTAs to an SM);
+// clusters by the wait for their CTAs' sums: 16384 x 4096 249 us (67 %), 4096 x
+// 16384 300 us (55 %), from 8-bit copies 329 us (42 %).
 template <typename T, int TEAM, int NV, Lay LAY, bool PACKED, bool FULL, bool MANY>
 __global__ void __launch_bounds__(TEAM ? 256 : 128, TEAM ? 2 : 3) k_block_bwd(BArgs p)
 {
@@ -1095,8 +1100,9 @@ cudaError_t launch(const Shape& sh, BArgs& p, int per_thread, int extra, int64_t
 // columns may all be there, and the one for rows that cannot be read in
 // aligned pieces of 8 columns.  bf16 rows of one CTA keep their parameters in
 // shared memory: 32768 x 2048 RMS norm 128 -> 118 us, layer norm 162 -> 138.
-// fp32 rows (110.5 -> 112.1) and clusters (16384 x 4096 191 -> 224, 4096 x
-// 16384 215 -> 266), which want the CTAs that it costs, do not; the backward's
+// fp32 rows (110.5 -> 112.1) and clusters (4096 x 16384 166 -> 174, with 8-bit
+// copies 265 -> 310; 16384 x 4096 alone 151 -> 146), which want the CTAs that it
+// costs, do not; the backward's
 // CTAs, fewer and with more parameters to read twice, always do (bf16 280 -> 204,
 // fp32 204 -> 204, 16384 x 4096 416 -> 307).
 template <typename T, bool PACK>
