@@ -743,3 +743,40 @@ def test_matrix_scan_block_with_8bit_checkpoint():
     _close(out.view(-1, Do), ref["r"], ref["r_err"])
     want = orb.block_backward("rms", "none", r=orb.held8(_np(x).reshape(-1, D)), dz=_np(dx).reshape(-1, D))
     _close(gi.dr, want["dr"], want["dr_err"])
+
+
+@pytest.mark.parametrize("norm,D", [("rms", 4096), ("layer", 6000), ("rms", 8200), ("layer", 16384)])
+def test_block_clusters_two_streams_and_replayed(norm, D):
+    """Rows that several CTAs share: the same bits in calls side by side, with
+    many rows to a cluster, in a replayed graph, and for the rows one by one."""
+    t = torch()
+    rows = 1500
+    p = mru.block_problem(rows, D, norm=norm, act="silu", x_dtype="bf16")
+    gen = t.Generator(device="cuda").manual_seed(D)
+    r, y, g, dr, dz = (t.randn(rows, D, device="cuda", generator=gen).bfloat16() for _ in range(5))
+    w = {k: t.randn(D, device="cuda", generator=gen) for k in ("w_y", "s", "w_z")}
+
+    def step(stream=None):
+        out, z, _ = mru.block_norm_t(p, r, y=y, g=g, stream=stream, **w)
+        b = mru.block_norm_backward_t(p, r_out=out, y=y, g=g, dr_out=dr, dz=dz, stream=stream, **w)
+        return out, z, b.dr, b.dy, b.dg, b.dw_y, b.ds, b.dw_z
+
+    want = step()
+    t.cuda.synchronize()
+    streams = [t.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        outs = [step(st) for st in streams]
+        t.cuda.synchronize()
+        for got in outs:
+            assert all(t.equal(a, b) for a, b in zip(got, want))
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        graph.replay()
+    t.cuda.synchronize()
+    assert all(t.equal(a, b) for a, b in zip(got, want))
+    one = mru.block_problem(1, D, norm=norm, act="silu", x_dtype="bf16")
+    for k in (0, 733, rows - 1):
+        out, z, _ = mru.block_norm_t(one, r[k:k + 1], y=y[k:k + 1], g=g[k:k + 1], **w)
+        assert t.equal(out[0], want[0][k]) and t.equal(z[0], want[1][k])
